@@ -1,5 +1,7 @@
-"""Python binding of libgguf_qk (include/gguf_qk.h): GGUF Q8_0 / Q4_K dequant and
-fused dequant x activation products on an MI355X (gfx950).
+"""Python binding of libgguf_qk (include/gguf_qk.h, gguf_kv.h, gguf_file.h): GGUF
+Q8_0 / Q4_K dequant, fused dequant x activation products, and the steps around
+them (paged key-value cache, single-token attention, log probabilities) on an
+MI355X (gfx950).
 
 Argument marshalling only: each function takes torch device tensors, passes
 their raw pointers, sizes and the current HIP stream to the C entry point of
@@ -10,9 +12,12 @@ the first call raises.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 import struct
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -70,6 +75,16 @@ _SIGS = {
     "gguf_rmsnorm_f32": (ctypes.c_int, [_P, _P, ctypes.c_float, _P, _I64, _P]),
     "gguf_swiglu_f32": (ctypes.c_int, [_P, _P, _P, _I64, _P]),
     "gguf_add_f32": (ctypes.c_int, [_P, _P, _P, _I64, _P]),
+    "gguf_kv_page_bytes": (_I64, [ctypes.c_int, _I64, _I64, _I64]),
+    "gguf_kv_append": (ctypes.c_int, [_P, _P, _P, ctypes.c_int32, _I64, _I64, _P, _P, _P, _P, _I64, _I64, _P]),
+    "gguf_attn_decode_workspace": (_I64, [_P, _I64, _I64, _I64, ctypes.c_int32]),
+    "gguf_attn_decode": (ctypes.c_int, [_P, _P, _I64, _P, _I64, _I64, _I64, _P, _I64, _P, _I64, ctypes.c_float,
+                                        _I64, ctypes.c_int32, _P, _I64, _P]),
+    "gguf_kv_evict_workspace": (_I64, [_P, _I64, _I64, _I64]),
+    "gguf_kv_evict": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _I64, _I64, _P, _I64, _P]),
+    "gguf_logprobs_workspace": (_I64, [_I64, _I64, ctypes.c_int32]),
+    "gguf_logprobs": (ctypes.c_int, [_P, ctypes.c_int32, _I64, _I64, _I64, _P, _I64, ctypes.c_int32, _P, _P, _P,
+                                     _P, _P, _I64, _P]),
     "gguf_tensor_nbytes": (_I64, [ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(ctypes.c_int64)]),
     "gguf_file_open": (ctypes.c_int, [ctypes.c_char_p, ctypes.POINTER(ctypes.c_void_p)]),
     "gguf_file_close": (None, [_P]),
@@ -567,6 +582,273 @@ def gguf_add_f32(a, b, out=None, stream=None):
     _check(lib().gguf_add_f32(_vec(a, "a"), _vec(b, "b", n), _vec(out, "out", n), n, _stream(stream)),
            "gguf_add_f32")
     return out
+
+
+# ------------------------------------------------- paged key-value cache (include/gguf_kv.h)
+
+class KvCacheStruct(ctypes.Structure):
+    """struct gguf_kv_cache of the C ABI."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("pos", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("type", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+
+
+class KvCache:
+    """One layer's paged key-value cache: device tensors the caller owns (`k` and
+    `v` of n_pages * gguf_kv_page_bytes(...) bytes each, any dtype; optional
+    `weight` fp32 and `pos` int32 planes of n_pages * n_kv_heads * page_size) and
+    the C description of them. The layout is in include/gguf_kv.h. Keeps the
+    tensors alive.
+
+    type is TENSOR_F16, TENSOR_BF16 or TYPE_Q8_0. KvCache.empty allocates."""
+
+    def __init__(self, k, v, type, n_kv_heads, head_dim, page_size, weight=None, pos=None):
+        page = gguf_kv_page_bytes(type, n_kv_heads, head_dim, page_size)
+        if page < 0:
+            raise GgufQkArgumentError(page, "KvCache")
+        kp, vp = _dev(k, "k"), _dev(v, "v")
+        nbytes = k.numel() * k.element_size()
+        if nbytes == 0 or nbytes % page:
+            raise ValueError(f"k holds {nbytes} bytes, not whole pages of {page}")
+        if v.numel() * v.element_size() != nbytes:
+            raise ValueError("k and v must hold the same number of bytes")
+        self.n_pages = nbytes // page
+        slots = self.n_pages * n_kv_heads * page_size
+        for t, name, dt in ((weight, "weight", torch.float32), (pos, "pos", torch.int32)):
+            if t is not None:
+                _dev(t, name, dt)
+                if t.numel() != slots:
+                    raise ValueError(f"{name} holds {t.numel()} values, expected {slots}")
+        _one_device(k, v, weight, pos)
+        self.k, self.v, self.weight, self.pos = k, v, weight, pos
+        self.type, self.n_kv_heads, self.head_dim, self.page_size = type, n_kv_heads, head_dim, page_size
+        self.device = k.device
+        self.struct = KvCacheStruct(kp, vp, None if weight is None else weight.data_ptr(),
+                                    None if pos is None else pos.data_ptr(), self.n_pages, type, n_kv_heads,
+                                    head_dim, page_size)
+        self.address = ctypes.addressof(self.struct)
+
+    @classmethod
+    def empty(cls, type, n_pages, n_kv_heads, head_dim, page_size, device="cuda:0", planes=False):
+        """A cache of zeros; with `planes` it has weight and pos (for eviction)."""
+        page = gguf_kv_page_bytes(type, n_kv_heads, head_dim, page_size)
+        if page < 0:
+            raise GgufQkArgumentError(page, "KvCache.empty")
+        k, v = (torch.zeros(n_pages * page, dtype=torch.uint8, device=device) for _ in range(2))
+        w = p = None
+        if planes:
+            w = torch.zeros((n_pages, n_kv_heads, page_size), dtype=torch.float32, device=device)
+            p = torch.zeros((n_pages, n_kv_heads, page_size), dtype=torch.int32, device=device)
+        return cls(k, v, type, n_kv_heads, head_dim, page_size, weight=w, pos=p)
+
+
+def _one_device(first, *rest):
+    for t in rest:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on two devices: {first.device} and {t.device}")
+
+
+def _call(device, stream, run):
+    """Runs run(stream handle) with the tensors' device current (the library works
+    on the current device) and, where a stream is given, that stream current for
+    what run allocates."""
+    index = device.index
+    if stream is None and index == torch.cuda.current_device():
+        return run(torch.cuda.current_stream().cuda_stream)
+    with contextlib.ExitStack() as on:
+        on.enter_context(torch.cuda.device(device))
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
+            on.enter_context(torch.cuda.stream(stream))
+        return run(torch.cuda.current_stream().cuda_stream)
+
+
+def _rows2d(t, name, row, dtypes):
+    """(pointer, row stride) of [n, row] values whose rows may lie apart."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be one of {dtypes}, got {t.dtype}")
+    if t.dim() == 3 and t.shape[1] * t.shape[2] == row and t.stride(2) == 1 and (
+            t.shape[1] == 1 or t.stride(1) == t.shape[2]):
+        stride = t.stride(0)
+    elif t.dim() == 2 and t.shape[1] == row and (row == 1 or t.stride(1) == 1):
+        stride = t.stride(0)
+    else:
+        raise ValueError(f"{name} must be rows of {row} consecutive values, got {tuple(t.shape)}")
+    return t.data_ptr(), (max(stride, row) if t.shape[0] < 2 else stride)
+
+
+def _table(t):
+    p = _dev(t, "page_table", torch.int32)
+    if t.dim() != 2 or t.shape[1] < 1:
+        raise ValueError("page_table must be [n_seqs, pages]")
+    return p
+
+
+def _ints(t, name, n):
+    p = _dev(t, name, torch.int32)
+    if t.numel() != n:
+        raise ValueError(f"{name} holds {t.numel()} values, expected {n}")
+    return p
+
+
+def _work(workspace, need, device):
+    """A workspace of `need` bytes: the caller's, or one of the call's own."""
+    if need < 0:
+        raise GgufQkArgumentError(need, "workspace")
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    return workspace, _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+
+
+def gguf_kv_page_bytes(type_id: int, n_kv_heads: int, head_dim: int, page_size: int) -> int:
+    """Bytes of one page of K (and of V), or a negative status."""
+    return lib().gguf_kv_page_bytes(type_id, n_kv_heads, head_dim, page_size)
+
+
+def gguf_kv_append(cache: KvCache, k, v, page_table, slot, seq=None, pos=None, stream=None):
+    """Write tokens (rows of k and v, fp32 or bf16 [n_tokens, n_kv_heads * head_dim],
+    rows may lie apart) to slot[t] of sequence seq[t] (None: t). A token with a
+    slot or seq out of range is dropped."""
+    row = cache.n_kv_heads * cache.head_dim
+    dtypes = (torch.float32, torch.bfloat16)
+    (kp, ks), (vp, vs) = _rows2d(k, "k", row, dtypes), _rows2d(v, "v", row, dtypes)
+    n = k.shape[0]
+    if v.shape[0] != n or v.dtype != k.dtype or (n > 1 and ks != vs):
+        raise ValueError("k and v must have the same rows, type and row stride")
+    tp, sp = _table(page_table), _ints(slot, "slot", n)
+    qp = None if seq is None else _ints(seq, "seq", n)
+    pp = None if pos is None else _ints(pos, "pos", n)
+    _one_device(cache.k, k, v, page_table, slot, seq, pos)
+    src = TENSOR_F32 if k.dtype == torch.float32 else TENSOR_BF16
+    if n == 0:   # empty tensors have no address
+        return
+    _check(_call(cache.device, stream, lambda st: lib().gguf_kv_append(
+        cache.address, kp, vp, src, ks if n > 1 else row, n, qp, sp, pp, tp, page_table.shape[1],
+        page_table.shape[0], st)), "gguf_kv_append")
+
+
+def gguf_attn_decode_workspace(cache: KvCache, n_seqs: int, n_heads: int, max_len: int, track: bool = False) -> int:
+    """Bytes of workspace of a gguf_attn_decode call (any window), or a negative status."""
+    return lib().gguf_attn_decode_workspace(cache.address, n_seqs, n_heads, max_len, int(track))
+
+
+def gguf_attn_decode(cache: KvCache, q, page_table, lengths, max_len, scale=None, window=0, track=False, out=None,
+                     workspace=None, stream=None):
+    """Attention of one new token per sequence: q fp32 [n_seqs, n_heads, head_dim] or
+    [n_seqs, n_heads * head_dim] over the first lengths[s] slots of the cache
+    (the last `window` of them where given), scale 1 / sqrt(head_dim) unless
+    given. Returns out, fp32 of q's shape. With `track` the cache's weight grows
+    by the attention each slot received. `workspace`: a tensor of at least
+    gguf_attn_decode_workspace bytes that no overlapping call uses (None: the
+    call allocates one)."""
+    d = cache.head_dim
+    n = q.shape[0]
+    row = math.prod(q.shape[1:])
+    if row == 0 or row % d:
+        raise ValueError("q must be [n_seqs, n_heads, head_dim]")
+    qp, qs = _rows2d(q, "q", row, (torch.float32,))
+    heads = row // d
+    tp, lp = _table(page_table), _ints(lengths, "lengths", n)
+    if page_table.shape[0] != n:
+        raise ValueError("one row of page_table per sequence")
+    _one_device(cache.k, q, page_table, lengths, out, workspace)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    max_len = int(max_len)
+
+    def run(st):
+        o = torch.empty(q.shape, dtype=torch.float32, device=q.device) if out is None else out
+        op, os_ = _rows2d(o, "out", row, (torch.float32,))
+        if o.shape[0] != n:
+            raise ValueError("out must have one row per sequence")
+        if n == 0:   # empty tensors have no address
+            return o
+        need = 0 if workspace is not None else gguf_attn_decode_workspace(cache, n, heads, max_len, track)
+        ws, wp, wn = _work(workspace, need, cache.device)
+        _check(lib().gguf_attn_decode(cache.address, qp, qs, op, os_, n, heads, tp, page_table.shape[1], lp, max_len,
+                                      scale, int(window), int(track), wp, wn, st), "gguf_attn_decode")
+        return o
+    return _call(cache.device, stream, run)
+
+
+def gguf_kv_evict_workspace(cache: KvCache, n_seqs: int, max_len: int, budget: int) -> int:
+    """Bytes of workspace of a gguf_kv_evict call, or a negative status."""
+    return lib().gguf_kv_evict_workspace(cache.address, n_seqs, max_len, budget)
+
+
+def gguf_kv_evict(cache: KvCache, page_table, lengths, max_len, budget, recent=0, workspace=None, stream=None):
+    """Cut every sequence longer than `budget` to the `budget` slots per kv head
+    that received most attention (the newest `recent` tokens always stay). Moves
+    the kept slots behind the budget into the vacated ones and updates lengths."""
+    tp = _table(page_table)
+    n = page_table.shape[0]
+    lp = _ints(lengths, "lengths", n)
+    _one_device(cache.k, page_table, lengths, workspace)
+    max_len, budget = int(max_len), int(budget)
+
+    if n == 0:
+        return
+
+    def run(st):
+        need = 0 if workspace is not None else gguf_kv_evict_workspace(cache, n, max_len, budget)
+        ws, wp, wn = _work(workspace, need, cache.device)
+        _check(lib().gguf_kv_evict(cache.address, n, tp, page_table.shape[1], lp, max_len, budget, int(recent), wp,
+                                   wn, st), "gguf_kv_evict")
+    _call(cache.device, stream, run)
+
+
+class Logprobs(NamedTuple):
+    """What gguf_logprobs returns (None for a part that was not asked for)."""
+    token_logprobs: Optional[torch.Tensor]   # fp32 [n_rows, n_tokens]
+    entropy: torch.Tensor                    # fp32 [n_rows]
+    top_ids: Optional[torch.Tensor]          # int32 [n_rows, top_k]
+    top_logprobs: Optional[torch.Tensor]     # fp32 [n_rows, top_k]
+
+
+def gguf_logprobs_workspace(n_rows: int, vocab: int, top_k: int) -> int:
+    """Bytes of workspace of a gguf_logprobs call, or a negative status."""
+    return lib().gguf_logprobs_workspace(n_rows, vocab, top_k)
+
+
+def gguf_logprobs(logits, tokens=None, top_k=0, workspace=None, stream=None) -> Logprobs:
+    """Log probabilities of the given tokens (int32 [n_rows, n_tokens] or [n_rows])
+    under logits (fp32 or bf16 [n_rows, vocab] or [vocab], rows may lie apart),
+    the entropy of each row, and its top_k tokens with theirs."""
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch tensor")
+    x = logits.unsqueeze(0) if logits.dim() == 1 else logits
+    if x.dim() != 2:
+        raise ValueError("logits must be [n_rows, vocab]")
+    n, vocab = x.shape
+    xp, xs = _rows2d(x, "logits", vocab, (torch.float32, torch.bfloat16))
+    m, tp = 0, None
+    if tokens is not None:
+        tp = _dev(tokens, "tokens", torch.int32)
+        m = tokens.numel() // n if n else 0
+        if tokens.numel() != n * m or (tokens.dim() > 1 and tokens.shape[0] != n):
+            raise ValueError("tokens must be [n_rows, n_tokens]")
+    _one_device(logits, tokens, workspace)
+
+    def run(st):
+        f32 = dict(dtype=torch.float32, device=x.device)
+        lp = torch.empty((n, m), **f32) if m else None
+        ent = torch.empty(n, **f32)
+        ids = torch.empty((n, top_k), dtype=torch.int32, device=x.device) if top_k else None
+        top = torch.empty((n, top_k), **f32) if top_k else None
+        if n == 0:
+            return Logprobs(lp, ent, ids, top)
+        need = 0 if workspace is not None else gguf_logprobs_workspace(n, vocab, top_k)
+        ws, wp, wn = _work(workspace, need, x.device)
+        _check(lib().gguf_logprobs(xp, TENSOR_F32 if x.dtype == torch.float32 else TENSOR_BF16, n, vocab, xs, tp, m,
+                                   top_k, None if lp is None else lp.data_ptr(), ent.data_ptr(),
+                                   None if ids is None else ids.data_ptr(), None if top is None else top.data_ptr(),
+                                   wp, wn, st), "gguf_logprobs")
+        return Logprobs(lp, ent, ids, top)
+    return _call(x.device, stream, run)
 
 
 # ------------------------------------------------------------------ GGUF files

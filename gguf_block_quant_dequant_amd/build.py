@@ -48,10 +48,15 @@ HIP_FLAGS = [
     "-mllvm", "-amdgpu-kernarg-preload-count=16",
 ]
 
+# Matrix accumulators in ordinary registers: the attention rescales them every
+# time a maximum grows, and from accumulation registers each pass would copy
+# them out and back.
+VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
 
-# (source, extra defines, object tag): the lanes-along-K launches are compiled
+# (source, extra flags, object tag): the lanes-along-K launches are compiled
 # once per block type (GGUF ids 12 Q4_K, 2 Q4_0, 14 Q6_K, 8 Q8_0; Q4_K also
-# with the fused epilogues) so that the heavy kernel families build in parallel.
+# with the fused epilogues), the attention kernels once per cache type, so that
+# the heavy kernel families build in parallel.
 UNITS = [
     ("gguf_qk.hip", [], "abi"),
     ("lk.hip", [], "lkplan"),
@@ -61,6 +66,12 @@ UNITS = [
     ("lk_typed.hip", ["-DGQK_LK_TYPE=14", "-DGQK_LK_EP=0"], "lk_q6_k"),
     ("lk_typed.hip", ["-DGQK_LK_TYPE=8", "-DGQK_LK_EP=0"], "lk_q8_0"),
     ("gguf_file.cpp", [], "file"),
+    ("kv.hip", [], "kv"),
+    ("attn.hip", [], "attn"),
+    ("attn_typed.hip", ["-DGQK_KV_KIND=0", *VGPR_FORM], "attn_f16"),
+    ("attn_typed.hip", ["-DGQK_KV_KIND=1", *VGPR_FORM], "attn_bf16"),
+    ("attn_typed.hip", ["-DGQK_KV_KIND=2", *VGPR_FORM], "attn_q8_0"),
+    ("logprobs.hip", [], "logprobs"),
 ]
 
 

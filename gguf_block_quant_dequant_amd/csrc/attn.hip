@@ -1,0 +1,165 @@
+// Entry points of the attention over the paged cache (include/gguf_kv.h):
+// checks, the split over the cache's length, launches; and the join kernels.
+#include "abi_check.hpp"
+#include "attn_launch.hpp"
+
+namespace gqk {
+
+constexpr int64_t kAttnMaxLen = int64_t(1) << 30;   // 32-bit position arithmetic
+constexpr int64_t kAttnBlocks = 1024;               // blocks a call aims for
+
+// How a call is cut and what its workspace holds.
+struct AttnPlan {
+  int32_t group, head_tiles, splits, chunk;
+  int64_t span, score_stride, most_splits;
+  int64_t ml_bytes, o_bytes, bytes;
+};
+
+static int attn_plan(const KvView& c, int64_t n_seqs, int64_t n_heads, int64_t max_len, int64_t window, bool track,
+                     AttnPlan* p) {
+  if (n_seqs < 0 || n_heads < 1 || n_heads % c.hkv || max_len < 0 || window < 0) return GGUF_QK_ERR_SHAPE;
+  if (n_seqs > 65535 || n_heads > 65535 || max_len > kAttnMaxLen) return GGUF_QK_ERR_LIMIT;
+  p->group = (int32_t)(n_heads / c.hkv);
+  p->head_tiles = (p->group + 15) / 16;
+  // positions a sequence can cover, from a tile's start
+  p->span = window > 0 && window < max_len - (kAttnTile - 1) ? window + kAttnTile - 1 : max_len;
+  if (p->span < 1) p->span = 1;
+  // Chunks of whole rounds of a block's waves; at least one round, at most 64
+  // pages (their ids lie one per lane) and 2048 positions.
+  const int64_t round = kAttnTile * kAttnWaves;
+  int64_t most = int64_t(64) << c.shift;
+  if (most > 2048) most = 2048;
+  const int64_t cells = n_seqs * c.hkv * p->head_tiles;
+  int64_t want = cells > 0 ? kAttnBlocks / cells : 1;   // splits
+  if (want < 1) want = 1;
+  int64_t chunk = ((p->span + want - 1) / want + round - 1) / round * round;
+  if (chunk < 2 * round) chunk = 2 * round;
+  if (chunk > most) chunk = most;
+  p->chunk = (int32_t)chunk;
+  p->splits = (int32_t)((p->span + chunk - 1) / chunk);   // <= 2^30 / 256
+  // No shorter span, as a window leaves, is cut into more splits than this
+  // (the count itself may grow as the span shrinks past a rounding of the chunk).
+  p->most_splits = (p->span + most - 1) / most;
+  if (p->most_splits < want) p->most_splits = want;
+  if (p->most_splits > (p->span + 2 * round - 1) / (2 * round)) p->most_splits = (p->span + 2 * round - 1) / (2 * round);
+  p->score_stride = track ? (max_len + kAttnTile - 1) / kAttnTile * kAttnTile : 0;
+  return GGUF_QK_OK;
+}
+
+// Sets the workspace's parts for `splits`; -1 where they do not fit.
+static int64_t attn_bytes(const KvView& c, int64_t n_seqs, int64_t n_heads, int64_t splits, bool track, AttnPlan* p) {
+  const int64_t rows = n_seqs * n_heads;
+  p->ml_bytes = splits > 1 || track ? abi_mul(rows, splits * 8) : 0;
+  p->o_bytes = splits > 1 ? abi_mul(rows, splits * c.dim * 4) : 0;
+  const int64_t score_bytes = track ? abi_mul(rows, p->score_stride * 4) : 0;
+  if (p->ml_bytes < 0 || p->o_bytes < 0 || score_bytes < 0) return -1;
+  p->ml_bytes = (p->ml_bytes + 15) / 16 * 16;
+  return p->bytes = p->ml_bytes + p->o_bytes + score_bytes;
+}
+
+template <int DIM>
+static void launch_join(const AttnArgs& a, int joins, int tiles, dim3 grid, hipStream_t stream) {
+  hipLaunchKernelGGL(attn_join_kernel<DIM>, grid, dim3(kJoinThreads), 0, stream, a, joins, tiles);
+}
+
+}  // namespace gqk
+
+using namespace gqk;
+
+extern "C" {
+
+int64_t gguf_attn_decode_workspace(const gguf_kv_cache* cache, int64_t n_seqs, int64_t n_heads,
+                                   int64_t max_len, int32_t track) {
+  KvView c;
+  int st = kv_view(cache, &c);
+  if (st) return st;
+  AttnPlan p;
+  st = attn_plan(c, n_seqs, n_heads, max_len, 0, track != 0, &p);
+  if (st) return st;
+  const int64_t b = attn_bytes(c, n_seqs, n_heads, p.most_splits, track != 0, &p);
+  return b < 0 ? GGUF_QK_ERR_LIMIT : b;
+}
+
+int gguf_attn_decode(const gguf_kv_cache* cache, const float* q, int64_t q_stride, float* out,
+                     int64_t out_stride, int64_t n_seqs, int64_t n_heads, const int32_t* page_table,
+                     int64_t table_stride, const int32_t* lengths, int64_t max_len, float scale,
+                     int64_t window, int32_t track, void* workspace, int64_t workspace_bytes,
+                     hipStream_t stream) {
+  AttnArgs a;
+  int st = kv_view(cache, &a.c);
+  if (st) return st;
+  if (!q || !out || !page_table || !lengths || (track && !a.c.weight)) return GGUF_QK_ERR_NULL;
+  AttnPlan p;
+  st = attn_plan(a.c, n_seqs, n_heads, max_len, window, track != 0, &p);
+  if (st) return st;
+  if (attn_bytes(a.c, n_seqs, n_heads, p.splits, track != 0, &p) < 0) return GGUF_QK_ERR_LIMIT;
+  const int64_t row = n_heads * a.c.dim;
+  if (table_stride < 1 || q_stride < row || out_stride < row || !(scale == scale) || scale > 3.0e38f ||
+      scale < -3.0e38f)
+    return GGUF_QK_ERR_SHAPE;
+  if (abi_mul(abi_mul(n_seqs, q_stride), 4) < 0 || abi_mul(abi_mul(n_seqs, out_stride), 4) < 0 ||
+      abi_mul(abi_mul(n_seqs, table_stride), 4) < 0)
+    return GGUF_QK_ERR_SHAPE;
+  if (!abi_aligned(q, 16) || !abi_aligned(out, 16) || q_stride % 4 || out_stride % 4 || !abi_aligned(page_table, 4) ||
+      !abi_aligned(lengths, 4) || !abi_aligned(workspace, 16))
+    return GGUF_QK_ERR_ALIGN;
+  if (n_seqs == 0) return GGUF_QK_OK;
+  if (p.bytes > 0 && !workspace) return GGUF_QK_ERR_NULL;
+  if (workspace_bytes < p.bytes) return GGUF_QK_ERR_LIMIT;
+  const int64_t qb = ((n_seqs - 1) * q_stride + row) * 4, ob = ((n_seqs - 1) * out_stride + row) * 4;
+  const int64_t tb = n_seqs * table_stride * 4, lb = n_seqs * 4;
+  const void* w = p.bytes > 0 ? workspace : nullptr;
+  if (abi_overlap(out, ob, q, qb) || abi_overlap(out, ob, page_table, tb) || abi_overlap(out, ob, lengths, lb) ||
+      kv_touches(a.c, out, ob) || abi_overlap(w, p.bytes, out, ob) || abi_overlap(w, p.bytes, q, qb) ||
+      abi_overlap(w, p.bytes, page_table, tb) || abi_overlap(w, p.bytes, lengths, lb) || kv_touches(a.c, w, p.bytes))
+    return GGUF_QK_ERR_ALIAS;
+  if (track) {
+    const int64_t wb = kv_plane_bytes(a.c);
+    if (abi_overlap(a.c.weight, wb, q, qb) || abi_overlap(a.c.weight, wb, page_table, tb) ||
+        abi_overlap(a.c.weight, wb, lengths, lb))
+      return GGUF_QK_ERR_ALIAS;
+  }
+  st = abi_device();
+  if (st) return st;
+  const int64_t tiles = (p.span + kWeightTile - 1) / kWeightTile;
+  const int64_t weight_blocks = track ? tiles * a.c.hkv : 0;
+  const int64_t joins = p.splits > 1 ? n_heads : 0;
+  if (joins + weight_blocks > INT32_MAX) return GGUF_QK_ERR_LIMIT;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.table = page_table;
+  a.lengths = lengths;
+  a.q = q;
+  a.out = out;
+  a.part_ml = reinterpret_cast<float*>(ws);
+  a.part_o = reinterpret_cast<float*>(ws + p.ml_bytes);
+  a.scores = reinterpret_cast<float*>(ws + p.ml_bytes + p.o_bytes);
+  a.table_stride = table_stride;
+  a.q_stride = q_stride;
+  a.out_stride = out_stride;
+  a.max_len = max_len;
+  a.window = window;
+  a.score_stride = p.score_stride;
+  a.n_heads = (int32_t)n_heads;
+  a.group = p.group;
+  a.head_tiles = p.head_tiles;
+  a.splits = p.splits;
+  a.chunk = p.chunk;
+  a.qscale = scale * 1.44269504088896340736f;
+  const dim3 grid((unsigned)p.splits, (unsigned)(a.c.hkv * p.head_tiles), (unsigned)n_seqs);
+  if (cache->type == GGUF_KV_TYPE_F16) launch_attn_f16(a, track != 0, grid, stream);
+  else if (cache->type == GGUF_KV_TYPE_BF16) launch_attn_bf16(a, track != 0, grid, stream);
+  else launch_attn_q8_0(a, track != 0, grid, stream);
+  st = abi_launched();
+  if (st || joins + weight_blocks == 0) return st;
+  const dim3 jgrid((unsigned)(joins + weight_blocks), (unsigned)n_seqs);
+  switch (a.c.dim) {
+    case 64: launch_join<64>(a, (int)joins, (int)tiles, jgrid, stream); break;
+    case 96: launch_join<96>(a, (int)joins, (int)tiles, jgrid, stream); break;
+    case 128: launch_join<128>(a, (int)joins, (int)tiles, jgrid, stream); break;
+    case 192: launch_join<192>(a, (int)joins, (int)tiles, jgrid, stream); break;
+    default: launch_join<256>(a, (int)joins, (int)tiles, jgrid, stream); break;
+  }
+  return abi_launched();
+}
+
+}  // extern "C"

@@ -1,0 +1,572 @@
+// Attention of one new token per sequence over the paged key-value cache
+// ("GGUF Inferencer in R", section 5.2.1, attend: softmax(q k^T / sqrt(d)) v),
+// the cache's positions split over blocks and joined.
+//
+// A wave takes 32 positions at a time and up to 16 query heads of one kv head:
+//   S^T = K Q^T   two 16 x 16 tiles, A = K (rows: positions), B = Q (columns: heads)
+//   O^T += V^T P^T   A = V^T (rows: dims), B = P^T (columns: heads)
+// Transposed products leave a lane with one head (its column) throughout: the
+// running maximum, sum and rescale are per-lane values, and the lane's eight
+// weights are already the B operand of the second product when the row of K
+// that feeds row r of tile t is position 8 (r / 4) + 4 t + r % 4 (a lane of
+// group g = lane / 16 then holds positions 8 g .. 8 g + 7). V is stored
+// transposed, so those eight positions of a dim are one aligned load. Nothing
+// goes through LDS but the join of a block's waves.
+//
+// The kernel reads each cache byte once: the bound is HBM. The matrix cores
+// run at a fraction of their rate (16 columns for n_heads / n_kv_heads heads,
+// times two or three parts of the fp32 operand), which costs nothing here and
+// keeps fp32 accuracy.
+#pragma once
+
+#include "device_common.hpp"
+#include "kv_cache.hpp"
+
+namespace gqk {
+
+struct AttnArgs {
+  KvView c;
+  const int32_t* table;
+  const int32_t* lengths;
+  const float* q;
+  float* out;
+  float* part_o;    // [n_seqs][n_heads][splits][dim], unnormalized (splits > 1)
+  float* part_ml;   // [n_seqs][n_heads][splits][2]: maximum (log2 domain) and sum
+  float* scores;    // [n_seqs][n_heads][score_stride] (track): log2-domain scores
+  int64_t table_stride, q_stride, out_stride, max_len, window, score_stride;
+  int32_t n_heads, group, head_tiles, splits, chunk;
+  float qscale;     // scale * log2(e)
+};
+
+constexpr int kAttnTile = 32;    // positions per step of a wave
+constexpr int kAttnWaves = 4;
+constexpr int kAttnThreads = kAttnWaves * 64;
+constexpr float kPScaleF16 = 16384.0f;   // softmax weights enter fp16 times 2^14: 2^-24 of the largest is normal
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8v __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// First position a sequence's attention covers, rounded down to a tile.
+__device__ __forceinline__ int attn_first(int n, int64_t window) {
+  return window > 0 && (int64_t)n > window ? (int)(n - window) : 0;
+}
+
+// Eight fp32 values as parts whose sum they are: three bf16 by truncation (8
+// significant bits each: exact), or two fp16 (22 bits).
+template <int KIND>
+struct Parts {
+  static constexpr int kN = KIND == kKvF16 ? 2 : 3;
+  uint4 p[kN];
+  __device__ __forceinline__ void set(const float (&x)[8]) {
+    uint32_t w[kN][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float a = x[2 * j], b = x[2 * j + 1];
+      if constexpr (KIND == kKvF16) {
+        const _Float16 ha = (_Float16)a, hb = (_Float16)b;
+        w[0][j] = (uint32_t)__builtin_bit_cast(uint16_t, ha) | (uint32_t)__builtin_bit_cast(uint16_t, hb) << 16;
+        const _Float16 la = (_Float16)(a - (float)ha), lb = (_Float16)(b - (float)hb);
+        w[1][j] = (uint32_t)__builtin_bit_cast(uint16_t, la) | (uint32_t)__builtin_bit_cast(uint16_t, lb) << 16;
+      } else {
+        const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+        const float ra = a - __uint_as_float(ua & 0xFFFF0000u), rb = b - __uint_as_float(ub & 0xFFFF0000u);
+        const uint32_t va = __float_as_uint(ra), vb = __float_as_uint(rb);
+        const float sa = ra - __uint_as_float(va & 0xFFFF0000u), sb = rb - __uint_as_float(vb & 0xFFFF0000u);
+        // bytes 2, 3 of each word
+        w[0][j] = __builtin_amdgcn_perm(ub, ua, 0x07060302u);
+        w[1][j] = __builtin_amdgcn_perm(vb, va, 0x07060302u);
+        w[2][j] = __builtin_amdgcn_perm(__float_as_uint(sb), __float_as_uint(sa), 0x07060302u);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kN; ++i) p[i] = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+  }
+};
+
+template <int KIND>
+__device__ __forceinline__ f32x4 attn_mfma(const uint4& a, const uint4& b, const f32x4& c) {
+  if constexpr (KIND == kKvF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8v, a), __builtin_bit_cast(bf16x8v, b), c,
+                                                   0, 0, 0);
+}
+
+// Eight int8 codes as bf16 (exact).
+__device__ __forceinline__ uint4 codes_bf16(const uint2& q) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t u = j < 2 ? q.x : q.y;
+    const float lo = (j & 1) ? sbyte2(u) : sbyte0(u), hi = (j & 1) ? sbyte3(u) : sbyte1(u);
+    w[j] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A wave's 32 positions of K or V as loaded.
+template <int KIND, int NB>
+struct AttnK {
+  uint4 x[2][KIND == kKvQ80 ? 1 : NB];
+  uint2 c[2][KIND == kKvQ80 ? NB : 1];
+  uint4 d[KIND == kKvQ80 ? NB : 1];   // scales of the lane's eight positions, [position][block]
+};
+template <int KIND, int NB>
+struct AttnV {
+  uint4 x[KIND == kKvQ80 ? 1 : 2 * NB];
+  uint2 c[KIND == kKvQ80 ? 2 * NB : 1];
+  uint4 d[KIND == kKvQ80 ? NB : 1];   // scales of the lane's eight positions, [block][position]
+};
+
+__device__ __forceinline__ uint4 load16(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
+__device__ __forceinline__ uint2 load8(const uint8_t* p) { return *reinterpret_cast<const uint2*>(p); }
+
+// Half i of a run of 16-byte words.
+template <int N>
+__device__ __forceinline__ float half_of(const uint4 (&d)[N], int i) {
+  const uint4& w = d[i >> 3];
+  const int j = (i >> 1) & 3;
+  const uint32_t u = j == 0 ? w.x : j == 1 ? w.y : j == 2 ? w.z : w.w;
+  return (i & 1) ? half_hi(u) : half_lo(u);
+}
+
+// One block: a chunk of one sequence's positions, up to 16 query heads of one
+// kv head; its waves take the chunk's 32-position tiles in turn and join in LDS.
+template <int KIND, int NB, bool TRACK>
+__global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArgs a) {
+  constexpr int DIM = NB * 32;
+  constexpr int NT = 2 * NB;   // 16-dim tiles of the output
+  using P = Parts<KIND>;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 15, g = lane >> 4;
+  const int split = blockIdx.x, s = blockIdx.z;
+  const int h = blockIdx.y / a.head_tiles, ht = blockIdx.y % a.head_tiles;
+  const int n = (int)kv_length(a.lengths[s], a.max_len, a.table_stride, a.c.shift);
+  const int first = attn_first(n, a.window);
+  const int begin = (first & ~(kAttnTile - 1)) + split * a.chunk;   // < 2^31: max_len <= 2^30
+  const int heads = a.group - ht * 16 < 16 ? a.group - ht * 16 : 16;   // valid columns
+  const int head0 = h * a.group + ht * 16;
+  if (begin >= n) {
+    // nothing here; a sequence without positions is zero (with more splits
+    // than one the join writes it)
+    if (a.splits == 1) {
+      for (int i = tid; i < heads * DIM; i += kAttnThreads)
+        a.out[(int64_t)s * a.out_stride + (int64_t)(head0 + i / DIM) * DIM + i % DIM] = 0.f;
+    }
+    return;
+  }
+  const int end = n - begin < a.chunk ? n : begin + a.chunk;
+
+  // the chunk's page ids, one per lane (a chunk spans at most 64 pages)
+  const int page0 = begin >> a.c.shift;
+  const int last_page = (end - 1) >> a.c.shift;
+  int32_t pid = 0;
+  bool bad = false;
+  if (page0 + lane <= last_page) {
+    pid = kv_page(a.table + (int64_t)s * a.table_stride, page0 + lane, a.table_stride, a.c.n_pages);
+    bad = pid < 0;
+  }
+  const bool any_bad = __any(bad);
+
+  const int k_row = 8 * (col >> 2) + (col & 3);   // + 4 t: the position in the tile of this lane's K row
+  const uint8_t* const kh = a.c.k + (int64_t)h * a.c.head_bytes;
+  const uint8_t* const vh = a.c.v + (int64_t)h * a.c.head_bytes;
+  const int64_t page_bytes = (int64_t)a.c.hkv * a.c.head_bytes;
+  const int smask = a.c.ps - 1;
+
+  auto page_at = [&](int local) -> int64_t {   // page id of the chunk's page `local` (uniform), 0 for a bad one
+    const int id = __builtin_amdgcn_readlane(pid, local);
+    return id < 0 ? 0 : id;
+  };
+  AttnK<KIND, NB> K;
+  AttnV<KIND, NB> V;
+  // A tile lies in one page, or in two of 16 positions; the second half of a
+  // last tile may have no page: lanes past the table hold page 0, whose values
+  // are then masked.
+  auto load_k = [&](int t0) {
+    const int local = (t0 >> a.c.shift) - page0;
+    int64_t base = page_at(local) * page_bytes;
+    if (a.c.ps == 16 && k_row >= 16) base = page_at((local + 1) & 63) * page_bytes;
+    const uint8_t* p = kh + base;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int slot = (t0 + k_row + 4 * t) & smask;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        if constexpr (KIND == kKvQ80) K.c[t][b] = load8(p + slot * DIM + b * 32 + 8 * g);
+        else K.x[t][b] = load16(p + (slot * DIM + b * 32 + 8 * g) * 2);
+      }
+    }
+    if constexpr (KIND == kKvQ80) {
+      int64_t dbase = page_at(local) * page_bytes;
+      if (a.c.ps == 16 && g >= 2) dbase = page_at((local + 1) & 63) * page_bytes;
+      const uint8_t* dp = kh + dbase + a.c.ps * DIM + ((t0 + 8 * g) & smask) * (NB * 2);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) K.d[b] = load16(dp + 16 * b);
+    }
+  };
+  auto load_v = [&](int t0) {
+    const int local = (t0 >> a.c.shift) - page0;
+    int64_t base = page_at(local) * page_bytes;
+    if (a.c.ps == 16 && g >= 2) base = page_at((local + 1) & 63) * page_bytes;
+    const uint8_t* p = vh + base;
+    const int slot = (t0 + 8 * g) & smask;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if constexpr (KIND == kKvQ80) V.c[t] = load8(p + (t * 16 + col) * a.c.ps + slot);
+      else V.x[t] = load16(p + ((t * 16 + col) * a.c.ps + slot) * 2);
+    }
+    if constexpr (KIND == kKvQ80) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) V.d[b] = load16(p + a.c.ps * DIM + (b * a.c.ps + slot) * 2);
+    }
+  };
+
+  // Tiles of positions that all count, [t_lo, t_hi), run through a loop that
+  // holds the next tile's loads in flight; the others (the window's first, the
+  // last, and every one of a chunk with a bad page) behind it, masked.
+  const int step = kAttnTile * kAttnWaves;
+  const int mine = begin + wave * kAttnTile;
+  int t_lo = mine, t_hi = end & ~(kAttnTile - 1);
+  if (t_lo < first) t_lo += step;
+  if (any_bad) t_hi = t_lo;
+  if (t_lo < t_hi) {
+    load_k(t_lo);
+    load_v(t_lo);
+  }
+
+  // q of this lane's head: the B operand, dims 32 b + 8 g .. + 7
+  P q[NB];
+  float sfac = 1.0f;   // undoes the row's power-of-two scale (F16)
+  {
+    float x[NB][8];
+    const bool live = col < heads;
+    const float* qp = a.q + (int64_t)s * a.q_stride + (int64_t)(head0 + (live ? col : 0)) * DIM + 8 * g;
+    float amax = 0.f;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const float4 u = *reinterpret_cast<const float4*>(qp + 32 * b);
+      const float4 v = *reinterpret_cast<const float4*>(qp + 32 * b + 4);
+      const float y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        x[b][j] = live ? y[j] * a.qscale : 0.f;
+        amax = fmaxf(amax, fabsf(x[b][j]));
+      }
+    }
+    if constexpr (KIND == kKvF16) {
+      // the row's largest magnitude to [512, 1024): both fp16 parts of every
+      // value that matters are normal numbers
+      amax = fmaxf(amax, __shfl_xor(amax, 16));
+      amax = fmaxf(amax, __shfl_xor(amax, 32));
+      int e = 0;
+      if (amax > 0.f && amax < __builtin_inff()) {
+        (void)__builtin_frexpf(amax, &e);
+        e = 10 - e;
+        e = e > 100 ? 100 : e < -100 ? -100 : e;
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[b][j] = __builtin_ldexpf(x[b][j], e);
+      sfac = __builtin_ldexpf(1.0f, -e);
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) q[b].set(x[b]);
+  }
+
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  f32x4 o[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) o[t] = zero;
+  float m = -__builtin_inff(), l = 0.f;   // of this lane's head; l over this lane's positions
+
+  // Scores of positions t0 + 8 g + j of this lane's head, from the K loaded.
+  auto scores = [&](float (&sc)[8]) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      f32x4 acc = zero;
+      if constexpr (KIND == kKvQ80) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const uint4 kc = codes_bf16(K.c[t][b]);
+          f32x4 r = zero;
+#pragma unroll
+          for (int i = P::kN - 1; i >= 0; --i) r = attn_mfma<KIND>(kc, q[b].p[i], r);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[i] = fmaf(r[i], half_of(K.d, (4 * t + i) * NB + b), acc[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[4 * t + i] = acc[i];
+      } else {
+#pragma unroll
+        for (int i = P::kN - 1; i >= 0; --i)
+#pragma unroll
+          for (int b = 0; b < NB; ++b) acc = attn_mfma<KIND>(K.x[t][b], q[b].p[i], acc);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[4 * t + i] = acc[i] * sfac;
+      }
+    }
+  };
+  auto keep_scores = [&](int t0, const float (&sc)[8]) {
+    if constexpr (TRACK) {
+      if (col < heads) {
+        float* sp = a.scores + ((int64_t)s * a.n_heads + head0 + col) * a.score_stride + t0 + 8 * g;
+        *reinterpret_cast<float4*>(sp) = make_float4(sc[0], sc[1], sc[2], sc[3]);
+        *reinterpret_cast<float4*>(sp + 4) = make_float4(sc[4], sc[5], sc[6], sc[7]);
+      }
+    }
+  };
+  // Running maximum and sum; p becomes the weights relative to the maximum.
+  auto softmax = [&](const float (&sc)[8], float (&p)[8]) {
+    float mx = fmaxf(fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3])), fmaxf(fmaxf(sc[4], sc[5]), fmaxf(sc[6], sc[7])));
+    mx = fmaxf(mx, __shfl_xor(mx, 16));
+    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    if (__any(mx > m)) {
+      const float mn = fmaxf(m, mx);
+      const float alpha = __builtin_amdgcn_exp2f(m - mn);   // mn is finite where a position counts
+      const float al = mn == -__builtin_inff() ? 1.0f : alpha;
+      m = mn;
+      l *= al;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) o[t] *= al;
+    }
+    const float base = m == -__builtin_inff() ? 0.f : m;   // nothing seen yet
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      p[j] = __builtin_amdgcn_exp2f(sc[j] - base);
+      l += p[j];
+    }
+  };
+  // O^T += V^T P^T, from the V given.
+  auto accumulate = [&](const AttnV<KIND, NB>& v, float (&p)[8]) {
+    if constexpr (KIND == kKvQ80) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        float pd[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) pd[j] = p[j] * half_of(v.d, 8 * b + j);
+        P pp;
+        pp.set(pd);
+#pragma unroll
+        for (int t = 2 * b; t < 2 * b + 2; ++t) {
+          const uint4 vc = codes_bf16(v.c[t]);
+#pragma unroll
+          for (int i = P::kN - 1; i >= 0; --i) o[t] = attn_mfma<KIND>(vc, pp.p[i], o[t]);
+        }
+      }
+    } else {
+      if constexpr (KIND == kKvF16) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[j] *= kPScaleF16;
+      }
+      P pp;
+      pp.set(p);
+#pragma unroll
+      for (int i = P::kN - 1; i >= 0; --i)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) o[t] = attn_mfma<KIND>(v.x[t], pp.p[i], o[t]);
+    }
+  };
+
+  for (int t0 = t_lo; t0 < t_hi; t0 += step) {
+    float sc[8], p[8];
+    scores(sc);
+    const bool more = t0 + step < t_hi;   // uniform over the wave
+    if (more) load_k(t0 + step);
+    keep_scores(t0, sc);
+    softmax(sc, p);
+    accumulate(V, p);
+    if (more) load_v(t0 + step);
+  }
+  for (int t0 = mine; t0 < end; t0 += step) {
+    if (t0 >= t_lo && t0 < t_hi) continue;
+    load_k(t0);
+    load_v(t0);
+    const int p0 = t0 + 8 * g;
+    int hi = end - p0, lo = first - p0;
+    hi = hi < 0 ? 0 : hi > 8 ? 8 : hi;
+    lo = lo < 0 ? 0 : lo > 8 ? 8 : lo;
+    uint32_t live = ((1u << hi) - 1u) & ~((1u << lo) - 1u);   // of the lane's eight positions
+    if (any_bad && __shfl(pid, ((p0 >> a.c.shift) - page0) & 63) < 0) live = 0u;
+    float sc[8], p[8];
+    scores(sc);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sc[j] = (live >> j & 1) ? sc[j] : -__builtin_inff();
+    keep_scores(t0, sc);
+    softmax(sc, p);
+    // V behind the length may hold anything: masked positions become 0 (Q8_0:
+    // their scales; any code is finite)
+    const uint32_t w0 = ((live & 1) ? 0xFFFFu : 0u) | ((live & 2) ? 0xFFFF0000u : 0u);
+    const uint32_t w1 = ((live & 4) ? 0xFFFFu : 0u) | ((live & 8) ? 0xFFFF0000u : 0u);
+    const uint32_t w2 = ((live & 16) ? 0xFFFFu : 0u) | ((live & 32) ? 0xFFFF0000u : 0u);
+    const uint32_t w3 = ((live & 64) ? 0xFFFFu : 0u) | ((live & 128) ? 0xFFFF0000u : 0u);
+    AttnV<KIND, NB> mv = V;
+    if constexpr (KIND == kKvQ80) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        mv.d[b] = make_uint4(V.d[b].x & w0, V.d[b].y & w1, V.d[b].z & w2, V.d[b].w & w3);
+    } else {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        mv.x[t] = make_uint4(V.x[t].x & w0, V.x[t].y & w1, V.x[t].z & w2, V.x[t].w & w3);
+    }
+    accumulate(mv, p);
+  }
+  if constexpr (KIND == kKvF16) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) o[t] *= 1.0f / kPScaleF16;
+  }
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+
+  // Join of the waves, 32 dims at a time: [wave][head][32 + 4 floats].
+  constexpr int kRow = 36;
+  __shared__ __align__(16) float ml[kAttnWaves][16][2];
+  __shared__ __align__(16) float part[kAttnWaves][16][kRow];
+  if (lane < 16) {
+    ml[wave][lane][0] = m;
+    ml[wave][lane][1] = l;
+  }
+  __syncthreads();
+  auto joined = [&](int c, float* wf) {   // weight of each wave, returns {M, L}
+    float M = ml[0][c][0];
+#pragma unroll
+    for (int w = 1; w < kAttnWaves; ++w) M = fmaxf(M, ml[w][c][0]);
+    const float base = M == -__builtin_inff() ? 0.f : M;
+    float L = 0.f;
+#pragma unroll
+    for (int w = 0; w < kAttnWaves; ++w) {
+      wf[w] = __builtin_amdgcn_exp2f(ml[w][c][0] - base);
+      L = fmaf(ml[w][c][1], wf[w], L);
+    }
+    return make_float2(M, L);
+  };
+  const bool partial = a.splits > 1;
+  if ((partial || TRACK) && tid < heads) {
+    float wf[kAttnWaves];
+    const float2 r = joined(tid, wf);
+    float* d = a.part_ml + (((int64_t)s * a.n_heads + head0 + tid) * a.splits + split) * 2;
+    d[0] = r.x;
+    d[1] = r.y;
+  }
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      *reinterpret_cast<f32x4*>(&part[wave][col][16 * t + 4 * g]) = o[2 * b + t];
+    __syncthreads();
+    for (int i = tid; i < heads * 8; i += kAttnThreads) {   // four dims each
+      const int c = i >> 3, d4 = (i & 7) * 4;
+      float wf[kAttnWaves];
+      const float2 r = joined(c, wf);
+      f32x4 sum = zero;
+#pragma unroll
+      for (int w = 0; w < kAttnWaves; ++w) sum += *reinterpret_cast<const f32x4*>(&part[w][c][d4]) * wf[w];
+      if (partial) {
+        *reinterpret_cast<f32x4*>(a.part_o + (((int64_t)s * a.n_heads + head0 + c) * a.splits + split) * DIM + 32 * b +
+                                  d4) = sum;
+      } else {
+        const float inv = r.y == 0.f ? 0.f : 1.0f / r.y;   // no position left: zeros
+        *reinterpret_cast<f32x4*>(a.out + (int64_t)s * a.out_stride + (int64_t)(head0 + c) * DIM + 32 * b + d4) =
+            sum * inv;
+      }
+    }
+    if (b + 1 < NB) __syncthreads();
+  }
+}
+
+// Maximum and sum of one head over the splits that hold positions, by one wave;
+// every lane returns them.
+__device__ __forceinline__ float2 attn_join_ml(const float* ml, int splits, int lane) {
+  float m = -__builtin_inff();
+  for (int i = lane; i < splits; i += 64) m = fmaxf(m, ml[2 * i]);
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+  const float base = m == -__builtin_inff() ? 0.f : m;
+  float l = 0.f;
+  for (int i = lane; i < splits; i += 64) l = fmaf(ml[2 * i + 1], __builtin_amdgcn_exp2f(ml[2 * i] - base), l);
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) l += __shfl_xor(l, d);
+  return make_float2(base, l);
+}
+
+constexpr int kJoinThreads = 256;
+constexpr int kWeightTile = 1024;   // positions per block of the weight update
+
+// Blocks x < join_blocks: the joined output of query head x. The others: the
+// weights of 1024 positions of one kv head, summed over its query heads in
+// order (p = exp2(score - max) / sum) and added to the slots' weight.
+template <int DIM>
+__global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const AttnArgs a, int join_blocks, int weight_tiles) {
+  constexpr int kLanes = DIM / 4;                    // float4 lanes of a row
+  constexpr int kGroups = kJoinThreads / kLanes;     // splits in flight side by side
+  const int s = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
+  const int n = (int)kv_length(a.lengths[s], a.max_len, a.table_stride, a.c.shift);
+  const int first = attn_first(n, a.window);
+  const int base = first & ~(kAttnTile - 1);
+  const int splits = n > base ? (n - base + a.chunk - 1) / a.chunk : 0;   // that wrote partials
+  if ((int)blockIdx.x < join_blocks) {
+    const int head = blockIdx.x;
+    const int64_t row = (int64_t)s * a.n_heads + head;
+    const float* ml = a.part_ml + row * a.splits * 2;
+    const float2 r = attn_join_ml(ml, splits, lane);
+    __shared__ __align__(16) f32x4 part[kGroups][kLanes];
+    const int c = tid % kLanes, grp = tid / kLanes;
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+    if (grp < kGroups) {
+      const float* po = a.part_o + row * a.splits * DIM + c * 4;
+#pragma unroll 4
+      for (int i = grp; i < splits; i += kGroups)
+        sum += *reinterpret_cast<const f32x4*>(po + (int64_t)i * DIM) * __builtin_amdgcn_exp2f(ml[2 * i] - r.x);
+      part[grp][c] = sum;
+    }
+    __syncthreads();
+    if (tid < kLanes) {
+      sum = part[0][tid];
+#pragma unroll
+      for (int i = 1; i < kGroups; ++i) sum += part[i][tid];
+      const float inv = r.y == 0.f ? 0.f : 1.0f / r.y;
+      *reinterpret_cast<f32x4*>(a.out + (int64_t)s * a.out_stride + (int64_t)head * DIM + tid * 4) = sum * inv;
+    }
+    return;
+  }
+  const int wb = blockIdx.x - join_blocks;
+  const int h = wb / weight_tiles;
+  const int p0 = base + (wb % weight_tiles) * kWeightTile;
+  if (p0 >= n) return;
+  __shared__ float2 hml[16];
+  const int pos = p0 + tid * 4;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int h0 = 0; h0 < a.group; h0 += 16) {
+    const int hn = a.group - h0 < 16 ? a.group - h0 : 16;
+    __syncthreads();
+    for (int i = tid >> 6; i < hn; i += kJoinThreads / 64) {
+      const float2 r = attn_join_ml(a.part_ml + ((int64_t)s * a.n_heads + h * a.group + h0 + i) * a.splits * 2, splits, lane);
+      if (lane == 0) hml[i] = make_float2(r.x, r.y == 0.f ? 0.f : 1.0f / r.y);
+    }
+    __syncthreads();
+    if (pos < n) {
+#pragma unroll 4
+      for (int i = 0; i < hn; ++i) {
+        const float4 sc = *reinterpret_cast<const float4*>(
+            a.scores + ((int64_t)s * a.n_heads + h * a.group + h0 + i) * a.score_stride + pos);
+        const float2 r = hml[i];
+        acc[0] = fmaf(__builtin_amdgcn_exp2f(sc.x - r.x), r.y, acc[0]);
+        acc[1] = fmaf(__builtin_amdgcn_exp2f(sc.y - r.x), r.y, acc[1]);
+        acc[2] = fmaf(__builtin_amdgcn_exp2f(sc.z - r.x), r.y, acc[2]);
+        acc[3] = fmaf(__builtin_amdgcn_exp2f(sc.w - r.x), r.y, acc[3]);
+      }
+    }
+  }
+  if (pos >= n) return;
+  const int32_t page = kv_page(a.table + (int64_t)s * a.table_stride, pos >> a.c.shift, a.table_stride, a.c.n_pages);
+  if (page < 0) return;
+  float* w = a.c.weight + kv_slot_at(a.c, page, h, pos & (a.c.ps - 1));
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (pos + j >= first && pos + j < n) w[j] += acc[j];
+}
+
+}  // namespace gqk

@@ -1,0 +1,510 @@
+// Kernels that write the paged key-value cache: append and the moves of an
+// eviction, and the eviction's selection.
+#pragma once
+
+#include "device_common.hpp"
+#include "kv_layout.hpp"
+
+namespace gqk {
+
+enum KvKind { kKvF16 = 0, kKvBF16 = 1, kKvQ80 = 2 };
+
+// ------------------------------------------------------------------ append
+
+struct AppendArgs {
+  KvView c;
+  const void* k;
+  const void* v;
+  const int32_t* seq;
+  const int32_t* slot;
+  const int32_t* pos;
+  const int32_t* table;
+  int64_t row_stride, table_stride, n_tokens, n_seqs;
+  int32_t tile;   // tokens per block: 8, 16, 32 or 64
+};
+
+constexpr int kAppendThreads = 256;
+constexpr int kAppendTile = 64;
+
+// Eight input values from element `i` of a row.
+template <bool BF16SRC>
+__device__ __forceinline__ void append_load8(const void* base, int64_t i, float (&x)[8]) {
+  if constexpr (BF16SRC) {
+    const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[2 * j] = __uint_as_float(u[j] << 16);
+      x[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+    }
+  } else {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
+    const float4 a = p[0], b = p[1];
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+}
+
+// Rounds eight values to their cache form: 16-bit patterns, or Q8_0 codes (in
+// the low bytes) with the scale of the 32-dim block, whose other values the
+// lanes differing in the two low bits of `lane` hold.
+template <int KIND>
+__device__ __forceinline__ void append_round8(const float (&x)[8], uint16_t (&o)[8], uint16_t* scale) {
+  if constexpr (KIND == kKvF16) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = __builtin_bit_cast(uint16_t, (_Float16)x[j]);
+  } else if constexpr (KIND == kKvBF16) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = to_bf16(x[j]);
+  } else {
+    float amax = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[j]));
+    amax = fmaxf(amax, __shfl_xor(amax, 1));
+    amax = fmaxf(amax, __shfl_xor(amax, 2));
+    const _Float16 d16 = (_Float16)(amax / 127.0f);
+    const float d = (float)d16;
+    *scale = __builtin_bit_cast(uint16_t, d16);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float q = d == 0.f ? 0.f : rintf(x[j] / d);
+      o[j] = (uint8_t)(int8_t)(int)fminf(fmaxf(q, -127.f), 127.f);
+    }
+  }
+}
+
+__device__ __forceinline__ uint4 pack8x16(const uint16_t (&o)[8]) {
+  return make_uint4(o[0] | (uint32_t)o[1] << 16, o[2] | (uint32_t)o[3] << 16, o[4] | (uint32_t)o[5] << 16,
+                    o[6] | (uint32_t)o[7] << 16);
+}
+__device__ __forceinline__ uint2 pack8x8(const uint16_t (&o)[8]) {
+  return make_uint2((o[0] & 255u) | (o[1] & 255u) << 8 | (o[2] & 255u) << 16 | (uint32_t)o[3] << 24,
+                    (o[4] & 255u) | (o[5] & 255u) << 8 | (o[6] & 255u) << 16 | (uint32_t)o[7] << 24);
+}
+
+// One block: `tile` consecutive tokens of one kv head. K rows go out as they
+// are; V goes through LDS to be written along the positions, eight consecutive
+// slots per 16-byte store where the tile holds a whole aligned group of them,
+// single slots elsewhere. Bound by the bytes read and written (a prompt) or by
+// its two dependent loads (a token).
+template <int KIND, bool BF16SRC, int DIM>
+__global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(const AppendArgs a) {
+  constexpr int kOct = DIM / 8;             // 8-value groups of a row
+  constexpr int kLdsRow = DIM + 2;          // uint16; odd words: a column's reads spread over the banks
+  __shared__ __align__(16) uint16_t vt[kAppendTile * kLdsRow];
+  __shared__ uint16_t vs[KIND == kKvQ80 ? kAppendTile * (DIM / 32) : 1];
+  __shared__ int64_t head_at[kAppendTile];  // byte offset of the token's page and head; -1: dropped
+  __shared__ int32_t slot_of[kAppendTile];  // slot within the page
+  __shared__ uint8_t unit[kAppendTile];     // 1: leads a whole group, 2: single, 0: in a group or dropped
+  const int h = blockIdx.y, tid = threadIdx.x;
+  const int64_t t0 = (int64_t)blockIdx.x * a.tile;
+  if (tid < kAppendTile) {   // one wave
+    const int64_t t = t0 + tid;
+    int64_t at = -1;
+    int32_t in_page = 0;
+    if (tid < a.tile && t < a.n_tokens) {
+      const int64_t s = a.seq ? a.seq[t] : t;
+      const int32_t slot = a.slot[t];
+      if (s >= 0 && s < a.n_seqs && slot >= 0) {
+        const int32_t page = kv_page(a.table + s * a.table_stride, slot >> a.c.shift, a.table_stride, a.c.n_pages);
+        in_page = slot & (a.c.ps - 1);
+        if (page >= 0) {
+          at = kv_head_at(a.c, page, h);
+          const int64_t i = kv_slot_at(a.c, page, h, in_page);
+          if (a.c.weight) a.c.weight[i] = 0.f;
+          if (a.c.pos) a.c.pos[i] = a.pos ? a.pos[t] : slot;
+        }
+      }
+    }
+    head_at[tid] = at;
+    slot_of[tid] = in_page;
+    // whole groups: token tid on a slot that is a multiple of 8, the seven
+    // tokens behind it on the seven slots behind it
+    bool lead = at >= 0 && (in_page & 7) == 0 && tid + 8 <= kAppendTile;
+#pragma unroll
+    for (int j = 1; j < 8; ++j) {
+      const int64_t at_j = __shfl(at, (tid + j) & 63);
+      const int32_t slot_j = __shfl(in_page, (tid + j) & 63);
+      lead = lead && at_j == at && slot_j == in_page + j;
+    }
+    // the same pages named again by an overlapping run of tokens would be two
+    // tokens on one slot, which the contract excludes
+    bool covered = false;
+    const uint64_t leads = __ballot(lead);
+#pragma unroll
+    for (int j = 1; j < 8; ++j) covered = covered || (tid >= j && (leads >> (tid - j) & 1));
+    unit[tid] = at < 0 ? 0 : lead ? 1 : covered ? 0 : 2;
+  }
+  __syncthreads();
+  const int rows = a.tile;
+  constexpr int kRowStep = kAppendThreads / kOct;   // rows per pass (threads past the last whole row idle)
+  const int oct = tid % kOct, r0 = tid / kOct;
+  if (r0 < kRowStep) {
+    for (int r = r0; r < rows; r += kRowStep) {
+      const int64_t at = head_at[r];
+      if (at < 0) continue;   // whole rows drop: the lanes of a 32-dim block agree
+      const int64_t e = (t0 + r) * a.row_stride + (int64_t)h * DIM + oct * 8;
+      float x[8];
+      uint16_t o[8], sc = 0;
+      append_load8<BF16SRC>(a.k, e, x);
+      append_round8<KIND>(x, o, &sc);
+      uint8_t* kp = a.c.k + at;
+      if constexpr (KIND == kKvQ80) {
+        *reinterpret_cast<uint2*>(kp + slot_of[r] * DIM + oct * 8) = pack8x8(o);
+        if ((oct & 3) == 0)
+          reinterpret_cast<uint16_t*>(kp + a.c.ps * DIM)[slot_of[r] * (DIM / 32) + (oct >> 2)] = sc;
+      } else {
+        *reinterpret_cast<uint4*>(kp + (slot_of[r] * DIM + oct * 8) * 2) = pack8x16(o);
+      }
+      append_load8<BF16SRC>(a.v, e, x);
+      append_round8<KIND>(x, o, &sc);
+      uint32_t* dst = reinterpret_cast<uint32_t*>(vt + r * kLdsRow + oct * 8);
+      const uint4 w = pack8x16(o);
+      dst[0] = w.x; dst[1] = w.y; dst[2] = w.z; dst[3] = w.w;
+      if constexpr (KIND == kKvQ80)
+        if ((oct & 3) == 0) vs[r * (DIM / 32) + (oct >> 2)] = sc;
+    }
+  }
+  __syncthreads();
+  // V: each wave takes a token's unit for 64 dims at a time
+  for (int i = tid; i < rows * DIM; i += kAppendThreads) {
+    const int r = i / DIM, d = i % DIM;
+    const int u = unit[r];
+    if (u == 0) continue;
+    uint8_t* vp = a.c.v + head_at[r];
+    const int at = d * a.c.ps + slot_of[r];
+    if (u == 1) {
+      uint16_t o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = vt[(r + j) * kLdsRow + d];
+      if constexpr (KIND == kKvQ80) *reinterpret_cast<uint2*>(vp + at) = pack8x8(o);
+      else *reinterpret_cast<uint4*>(vp + at * 2) = pack8x16(o);
+    } else {
+      if constexpr (KIND == kKvQ80) vp[at] = (uint8_t)vt[r * kLdsRow + d];
+      else reinterpret_cast<uint16_t*>(vp)[at] = vt[r * kLdsRow + d];
+    }
+  }
+  if constexpr (KIND == kKvQ80) {
+    for (int i = tid; i < rows * (DIM / 32); i += kAppendThreads) {
+      const int r = i / (DIM / 32), b = i % (DIM / 32);
+      if (head_at[r] < 0) continue;
+      reinterpret_cast<uint16_t*>(a.c.v + head_at[r] + a.c.ps * DIM)[b * a.c.ps + slot_of[r]] =
+          vs[r * (DIM / 32) + b];
+    }
+  }
+}
+
+// ------------------------------------------------------------------ eviction
+
+struct EvictArgs {
+  KvView c;
+  const int32_t* table;
+  int32_t* lengths;
+  int32_t* count;     // [n_seqs][hkv] moves
+  int32_t* src;       // [n_seqs][hkv][max_moves] slots of the sequence, ascending
+  int32_t* dst;       // the same: the vacated slots
+  int64_t table_stride, max_len, budget, recent, max_moves;
+};
+
+constexpr int kEvictThreads = 1024;
+constexpr int kEvictWaves = kEvictThreads / 64;
+constexpr int kHistCopies = 16;   // copies of a digit's histogram, lane & 15: a few shared leading
+                                  // digits (weights have few exponents) would queue on one LDS word
+
+// A weight as an unsigned key of the same order; zeros of either sign equal,
+// every NaN above the infinities, below the protected slots' key.
+constexpr uint32_t kKeyProtected = 0xFFFFFFFFu;
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  if (w != w) return 0xFFFFFFFEu;
+  const uint32_t b = __float_as_uint(w + 0.0f);
+  return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+
+// Exclusive prefix sum over the block's threads; *total: the sum. Two barriers.
+__device__ __forceinline__ int block_scan(int v, int* lds /* kEvictWaves + 1 */, int* total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int x = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int y = __shfl_up(x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 63) lds[wave] = x;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kEvictWaves; ++w) {
+    const int s = lds[w];
+    before += w < wave ? s : 0;
+    all += s;
+  }
+  __syncthreads();
+  *total = all;
+  return before + x - v;
+}
+
+// One block per (kv head, sequence): the budget-th greatest key by radix
+// select, eight bits at a time from the top (keys in registers for R > 0, up
+// to R per thread; read again per pass for R == 0), then the lists of the
+// vacated slots before the budget and of the kept ones behind it, both in
+// slot order. Thread t holds slots [t S, (t + 1) S): prefix sums over threads
+// are prefix sums over slots.
+template <int R>
+__global__ __launch_bounds__(kEvictThreads) void kv_evict_select_kernel(const EvictArgs a) {
+  __shared__ int hist[256 * kHistCopies];
+  __shared__ int digit_sum[256];
+  __shared__ int scan[kEvictWaves + 1];
+  __shared__ int pick[2];
+  const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
+  const int64_t pair = (int64_t)s * a.c.hkv + h;
+  const int n = (int)kv_length(a.lengths[s], a.max_len, a.table_stride, a.c.shift);
+  const int budget = (int)a.budget;
+  if (a.budget >= n) {   // nothing to evict
+    if (tid == 0) a.count[pair] = 0;
+    return;
+  }
+  const int32_t* row = a.table + (int64_t)s * a.table_stride;
+  int S = ((n + kEvictThreads - 1) / kEvictThreads + 3) & ~3;   // slots per thread
+  const int first = tid * S;   // 1024 * S < 2^31: n is
+  // four consecutive slots share a page
+  auto page4 = [&](int slot) { return kv_page(row, slot >> a.c.shift, a.table_stride, a.c.n_pages); };
+  int newest = -1;
+  if (a.recent > 0) {
+    int m = INT32_MIN;
+    for (int r = 0; r < S; r += 4) {
+      const int slot = first + r;
+      if (slot >= n) break;
+      const int32_t page = page4(slot);
+      if (page < 0) continue;
+      const int4 p = *reinterpret_cast<const int4*>(a.c.pos + kv_slot_at(a.c, page, h, slot & (a.c.ps - 1)));
+      const int q[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (slot + j < n) m = q[j] > m ? q[j] : m;
+    }
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) {
+      const int o = __shfl_xor(m, d);
+      m = o > m ? o : m;
+    }
+    if (lane == 0) scan[tid >> 6] = m;
+    __syncthreads();
+    newest = INT32_MIN;
+#pragma unroll
+    for (int w = 0; w < kEvictWaves; ++w) newest = scan[w] > newest ? scan[w] : newest;
+    __syncthreads();
+  }
+  auto load4 = [&](int slot, uint32_t (&k)[4]) {
+    const int32_t page = slot < n ? page4(slot) : -1;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) k[j] = 0u;   // a slot without a page goes first
+    if (page < 0) return;
+    const int64_t at = kv_slot_at(a.c, page, h, slot & (a.c.ps - 1));
+    const float4 w = *reinterpret_cast<const float4*>(a.c.weight + at);
+    const float f[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) k[j] = weight_key(f[j]);
+    if (a.recent > 0) {
+      const int4 p = *reinterpret_cast<const int4*>(a.c.pos + at);
+      const int q[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if ((int64_t)q[j] > (int64_t)newest - a.recent) k[j] = kKeyProtected;
+    }
+  };
+  constexpr int kRegs = R > 0 ? R : 4;
+  uint32_t key[kRegs];
+  if constexpr (R > 0) {
+#pragma unroll
+    for (int r = 0; r < R; r += 4) {
+      uint32_t k4[4] = {0u, 0u, 0u, 0u};
+      if (r < S) load4(first + r, k4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) key[r + j] = k4[j];
+    }
+  }
+  // calls fn(slot, key) for the thread's slots in order
+  auto each = [&](auto&& fn) {
+    if constexpr (R > 0) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (r < S && first + r < n) fn(first + r, key[r]);
+    } else {
+      for (int r = 0; r < S && first + r < n; r += 4) {
+        load4(first + r, key);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (first + r + j < n) fn(first + r + j, key[j]);
+      }
+    }
+  };
+  uint32_t prefix = 0;   // digits chosen so far
+  int want = budget;     // rank (from the top) still to place among keys with the prefix
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int i = tid; i < 256 * kHistCopies; i += kEvictThreads) hist[i] = 0;
+    __syncthreads();
+    const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
+    each([&](int, uint32_t k) {
+      if ((k & mask) == prefix) atomicAdd(&hist[((k >> shift) & 255u) * kHistCopies + (lane & (kHistCopies - 1))], 1);
+    });
+    __syncthreads();
+    if (tid < 256) {
+      int sum = 0;
+#pragma unroll
+      for (int c = 0; c < kHistCopies; ++c) sum += hist[tid * kHistCopies + ((c + lane) & (kHistCopies - 1))];
+      digit_sum[tid] = sum;
+    }
+    __syncthreads();
+    if (tid < 64) {   // one wave: lane l holds digits 255 - 4 l down to 252 - 4 l
+      int part[4], sum = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        part[j] = digit_sum[255 - 4 * lane - j];
+        sum += part[j];
+      }
+      int x = sum;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int y = __shfl_up(x, d);
+        if (lane >= d) x += y;
+      }
+      int above = x - sum;   // keys of greater digits
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (above < want && want <= above + part[j]) {
+          pick[0] = 255 - 4 * lane - j;
+          pick[1] = want - above;
+        }
+        above += part[j];
+      }
+    }
+    __syncthreads();
+    prefix |= (uint32_t)pick[0] << shift;
+    want = pick[1];
+    __syncthreads();
+  }
+  // `want` of the keys equal to the threshold stay, lowest slots first
+  int equal = 0;
+  each([&](int, uint32_t k) { equal += k == prefix; });
+  int all;
+  int eq_rank = block_scan(equal, scan, &all);
+  int holes = 0, tails = 0, e = eq_rank;
+  each([&](int slot, uint32_t k) {
+    bool keep = k > prefix;
+    if (k == prefix) keep = e++ < want;
+    holes += slot < budget && !keep;
+    tails += slot >= budget && keep;
+  });
+  int hole_at = block_scan(holes, scan, &all);
+  int tail_at = block_scan(tails, scan, &all);
+  e = eq_rank;
+  int32_t* dst = a.dst + pair * a.max_moves;
+  int32_t* src = a.src + pair * a.max_moves;
+  each([&](int slot, uint32_t k) {
+    bool keep = k > prefix;
+    if (k == prefix) keep = e++ < want;
+    if (slot < budget && !keep) dst[hole_at++] = slot;
+    if (slot >= budget && keep) src[tail_at++] = slot;
+  });
+  if (tid == 0) a.count[pair] = all;
+}
+
+constexpr int kMoveTile = 64;
+constexpr int kMoveThreads = 256;
+
+// One block: up to 64 moves of one kv head of one sequence. Sources lie at or
+// behind the budget and destinations before it, so no block reads what another
+// writes. K rows move as 16-byte (Q8_0: 8-byte) pieces; V moves lane per
+// move, row of a dim by row, so that the ascending slots of a wave share lines.
+// Block (0, 0, s) also cuts the length (the selection has read it).
+template <int KIND, int DIM>
+__global__ __launch_bounds__(kMoveThreads) void kv_evict_move_kernel(const EvictArgs a) {
+  __shared__ int64_t sp[kMoveTile], dp[kMoveTile];   // byte offset of page and head
+  __shared__ int32_t ss[kMoveTile], ds[kMoveTile];   // slot within the page; ss -1: no move
+  const int h = blockIdx.y, s = blockIdx.z, tid = threadIdx.x, lane = tid & 63;
+  if (blockIdx.x == 0 && h == 0 && tid == 0 && (int64_t)a.lengths[s] > a.budget) a.lengths[s] = (int32_t)a.budget;
+  if (a.max_moves == 0) return;
+  const int64_t pair = (int64_t)s * a.c.hkv + h;
+  const int count = a.count[pair];
+  const int j0 = blockIdx.x * kMoveTile;
+  if (j0 >= count) return;
+  const int32_t* row = a.table + (int64_t)s * a.table_stride;
+  if (tid < kMoveTile) {
+    ss[tid] = -1;
+    if (j0 + tid < count) {
+      const int from = a.src[pair * a.max_moves + j0 + tid], to = a.dst[pair * a.max_moves + j0 + tid];
+      const int32_t fp = kv_page(row, from >> a.c.shift, a.table_stride, a.c.n_pages);
+      const int32_t tp = kv_page(row, to >> a.c.shift, a.table_stride, a.c.n_pages);
+      if (fp >= 0 && tp >= 0) {
+        const int m = a.c.ps - 1;
+        sp[tid] = kv_head_at(a.c, fp, h);
+        dp[tid] = kv_head_at(a.c, tp, h);
+        ss[tid] = from & m;
+        ds[tid] = to & m;
+        const int64_t i = kv_slot_at(a.c, fp, h, from & m), o = kv_slot_at(a.c, tp, h, to & m);
+        a.c.weight[o] = a.c.weight[i];
+        if (a.c.pos) a.c.pos[o] = a.c.pos[i];
+      }
+    }
+  }
+  __syncthreads();
+  const int rows = count - j0 < kMoveTile ? count - j0 : kMoveTile;
+  constexpr int kOct = DIM / 8;
+  for (int i = tid; i < rows * kOct; i += kMoveThreads) {
+    const int r = i / kOct, o = i % kOct;
+    if (ss[r] < 0) continue;
+    if constexpr (KIND == kKvQ80)
+      *reinterpret_cast<uint2*>(a.c.k + dp[r] + ds[r] * DIM + o * 8) =
+          *reinterpret_cast<const uint2*>(a.c.k + sp[r] + ss[r] * DIM + o * 8);
+    else
+      *reinterpret_cast<uint4*>(a.c.k + dp[r] + (ds[r] * DIM + o * 8) * 2) =
+          *reinterpret_cast<const uint4*>(a.c.k + sp[r] + (ss[r] * DIM + o * 8) * 2);
+  }
+  if (rows >= 16) {
+    // lane per move, eight dims of a wave in flight
+    if (lane < rows && ss[lane] >= 0) {
+      const uint8_t* from = a.c.v + sp[lane];
+      uint8_t* to = a.c.v + dp[lane];
+      const int f = ss[lane], t = ds[lane];
+      for (int d0 = (tid >> 6) * 8; d0 < DIM; d0 += (kMoveThreads / 64) * 8) {
+        if constexpr (KIND == kKvQ80) {
+          uint8_t x[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = from[(d0 + j) * a.c.ps + f];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) to[(d0 + j) * a.c.ps + t] = x[j];
+        } else {
+          uint16_t x[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = reinterpret_cast<const uint16_t*>(from)[(d0 + j) * a.c.ps + f];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) reinterpret_cast<uint16_t*>(to)[(d0 + j) * a.c.ps + t] = x[j];
+        }
+      }
+    }
+  } else {
+    // few moves: thread per dim
+    for (int i = tid; i < rows * DIM; i += kMoveThreads) {
+      const int r = i / DIM, d = i % DIM;
+      if (ss[r] < 0) continue;
+      if constexpr (KIND == kKvQ80)
+        a.c.v[dp[r] + d * a.c.ps + ds[r]] = a.c.v[sp[r] + d * a.c.ps + ss[r]];
+      else
+        reinterpret_cast<uint16_t*>(a.c.v + dp[r])[d * a.c.ps + ds[r]] =
+            reinterpret_cast<const uint16_t*>(a.c.v + sp[r])[d * a.c.ps + ss[r]];
+    }
+  }
+  if constexpr (KIND == kKvQ80) {   // the scales behind the codes
+    constexpr int NB = DIM / 32;
+    for (int i = tid; i < rows * NB; i += kMoveThreads) {
+      const int r = i / NB, b = i % NB;
+      if (ss[r] < 0) continue;
+      reinterpret_cast<uint16_t*>(a.c.k + dp[r] + a.c.ps * DIM)[ds[r] * NB + b] =
+          reinterpret_cast<const uint16_t*>(a.c.k + sp[r] + a.c.ps * DIM)[ss[r] * NB + b];
+      reinterpret_cast<uint16_t*>(a.c.v + dp[r] + a.c.ps * DIM)[b * a.c.ps + ds[r]] =
+          reinterpret_cast<const uint16_t*>(a.c.v + sp[r] + a.c.ps * DIM)[b * a.c.ps + ss[r]];
+    }
+  }
+}
+
+}  // namespace gqk
