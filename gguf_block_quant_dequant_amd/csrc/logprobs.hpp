@@ -6,14 +6,14 @@
 // top k. With M, L, T the joined ones (T = sum of f (t + l (m - M)), f = e^(m -
 // M)): log p_i = x_i - M - log L and the entropy is log L - T / L.
 //
-// The top k of a split: the least of the four waves' ceil(k / 4)-th greatest
-// lane maxima bounds the split's k-th value from below; the values
-// at or above that bound (about twice k of them on ordinary logits) are put in
-// order by counting, per value, the greater ones. Where ties make them too
-// many to hold, k block-wide maxima take their place.
+// The top k of a split: the k-th greatest of its lanes' maxima (of four lanes'
+// for few alternatives) bounds its k-th value from below, and little more than k
+// values reach that bound. They are put in order by counting, per value, the
+// greater ones. Where ties make them too many to hold, or NaN is among the
+// values, k block-wide maxima take their place.
 #pragma once
 
-#include "device_common.hpp"
+#include "wave_ops.hpp"
 
 namespace gqk {
 
@@ -35,7 +35,9 @@ constexpr int kLpWaves = kLpThreads / 64;
 constexpr int kLpPer = 32;                          // values per thread
 constexpr int kLpSplit = kLpThreads * kLpPer;
 constexpr int kLpMaxTop = 64;
+constexpr int kLpQuadTop = 16;
 constexpr int kLpCand = 512;                        // values held for the ordering
+constexpr int kLpWaveCand = kLpCand / kLpWaves;     // of one wave
 
 // An unsigned key of a float's order: zeros of either sign equal, NaN greatest
 // (and below all ones, so that no candidate is the greatest 64-bit value).
@@ -56,24 +58,6 @@ __device__ __forceinline__ uint64_t logit_order(uint32_t key, uint32_t index) {
 
 __device__ __forceinline__ float lp_exp(float d) { return __builtin_amdgcn_exp2f(d * 1.44269504088896340736f); }
 
-__device__ __forceinline__ float lp_wave_max(float v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
-  return v;
-}
-__device__ __forceinline__ float lp_wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
-  return v;
-}
-__device__ __forceinline__ uint32_t lp_wave_max_key(uint32_t v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) {
-    const uint32_t o = __shfl_xor(v, d);
-    v = o > v ? o : v;
-  }
-  return v;
-}
 __device__ __forceinline__ uint64_t lp_wave_max_order(uint64_t v) {
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) {
@@ -114,7 +98,7 @@ __device__ __forceinline__ void lp_order(const uint64_t* cand, int count, int to
 }
 
 template <bool BF16>
-__global__ __launch_bounds__(kLpThreads) void logprobs_split_kernel(const LogprobArgs a) {
+__global__ __launch_bounds__(kLpThreads, BF16 ? 6 : 4) void logprobs_split_kernel(const LogprobArgs a) {
   constexpr int ES = BF16 ? 2 : 4, VE = 16 / ES, NV = kLpPer / VE;   // values per load, loads per thread
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int split = blockIdx.x;
@@ -124,104 +108,177 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_split_kernel(const Logpro
   // 16-byte words from the aligned address at or below the row's start; a word
   // that reaches outside the row is read value by value
   const int shift = (int)(reinterpret_cast<uintptr_t>(row) & 15) / ES;
+  __shared__ float red[kLpWaves][3];
+  __shared__ uint32_t maxima[kLpThreads];   // keys
+  __shared__ int counts[kLpWaves];
+  __shared__ uint64_t cand[kLpCand];
   float x[kLpPer];
   int idx0[NV];   // index of a word's first value
+  uint4 words_in[NV];
+  auto take = [&](int v) {
+    const uint4& w = words_in[v];
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int64_t first = ((int64_t)split * (kLpSplit / VE) + v * kLpThreads + tid) * VE - shift;
-    idx0[v] = first >= a.vocab ? a.vocab : (int)first;
-    if (first >= 0 && first + VE <= a.vocab) {
-      const uint4 w = *reinterpret_cast<const uint4*>(row + first * ES);
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (BF16) {
+        x[v * VE + 2 * j] = __uint_as_float(u[j] << 16);
+        x[v * VE + 2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+      } else {
+        x[v * VE + j] = __uint_as_float(u[j]);
+      }
+    }
+  };
+  const int64_t start = (int64_t)split * kLpSplit - shift;   // of the split's first value
+  const bool within = start >= 0 && start + kLpSplit <= a.vocab;
+  if (within) {
+    // all loads in flight before the first is used
+    const uint4* p = reinterpret_cast<const uint4*>(row + start * ES) + tid;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (BF16) {
-          x[v * VE + 2 * j] = __uint_as_float(u[j] << 16);
-          x[v * VE + 2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
-        } else {
-          x[v * VE + j] = __uint_as_float(u[j]);
-        }
+    for (int v = 0; v < NV; ++v) words_in[v] = p[v * kLpThreads];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      idx0[v] = (int)start + (v * kLpThreads + tid) * VE;
+      take(v);
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int64_t first = start + (v * kLpThreads + tid) * VE;
+      idx0[v] = first >= a.vocab ? a.vocab : (int)first;
+      if (first >= 0 && first + VE <= a.vocab) words_in[v] = *reinterpret_cast<const uint4*>(row + first * ES);
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int first = idx0[v];
+      if (first >= 0 && first <= a.vocab - VE) {
+        take(v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < VE; ++j)
+          x[v * VE + j] = first + j >= 0 && first + j < a.vocab ? lp_at<BF16>(row, first + j) : -__builtin_inff();
+      }
+    }
+  }
+  float quad_max[kLpPer / 4], m = -__builtin_inff();   // maxima pass NaN over; the sums do not
+#pragma unroll
+  for (int i = 0; i < kLpPer / 4; ++i) {
+    quad_max[i] = fmaxf(fmaxf(x[4 * i], x[4 * i + 1]), fmaxf(x[4 * i + 2], x[4 * i + 3]));
+    m = fmaxf(m, quad_max[i]);
+  }
+  const float lane_max = m;
+  m = wave_max(m);
+  // Sums relative to the wave's own maximum: no barrier before the last value.
+  float l = 0.f, t = 0.f;
+  if (fabsf(m) < 4096.f) {
+    // In the log2 domain, one fma per value: y = x log2(e) - c with c the
+    // rounded m log2(e). What c lacks (gap, exact by fma, below 2^-11) is
+    // taken out of the sums.
+    constexpr float kLog2e = 1.44269504088896340736f;
+    const float c = m * kLog2e, gap = fmaf(m, kLog2e, -c);
+#pragma unroll
+    for (int i = 0; i < kLpPer; ++i) {
+      const float y = fmaf(x[i], kLog2e, -c), e = __builtin_amdgcn_exp2f(y);
+      l += e;
+      t = fmaf(e, fmaxf(y, -2000.f), t);   // e is 0 there: 0 for -inf, too
+    }
+    const float f = __builtin_amdgcn_exp2f(-gap);
+    t = (t - gap * l) * (f * 0.693147180559945309417f);
+    l *= f;
+  } else {
+    const float base = m == -__builtin_inff() ? 0.f : m;   // nothing but -inf: sums of 0
+#pragma unroll
+    for (int i = 0; i < kLpPer; ++i) {
+      const float d = x[i] - base, e = lp_exp(d);
+      l += e;
+      t = fmaf(e, fmaxf(d, -1000.f), t);
+    }
+  }
+  l = wave_sum(l);
+  t = wave_sum(t);
+  if (lane == 0) {
+    red[wave][0] = m;
+    red[wave][1] = l;
+    red[wave][2] = t;
+  }
+  // few alternatives of many values: the maxima of four lanes serve as well as
+  // the lanes' own
+  const bool quads = a.top_k <= kLpQuadTop && a.vocab - start >= kLpThreads / 2 * VE;
+  if (a.top_k > 0) {
+    if (quads) {
+      float v = fmaxf(lane_max, dpp_float<0xB1>(lane_max));
+      v = fmaxf(v, dpp_float<0x4E>(v));
+      if ((lane & 3) == 0) maxima[tid >> 2] = logit_key(v);
+    } else {
+      maxima[tid] = logit_key(lane_max);
+    }
+  }
+  __syncthreads();
+  if (a.top_k > 0) {
+    // the top 16 bits of the k-th greatest maximum, by bisection
+    uint32_t bits = 0;
+    if (quads) {
+      const uint32_t v = maxima[lane];
+#pragma unroll
+      for (int bit = 31; bit >= 16; --bit) {
+        const uint32_t trial = bits | 1u << bit;
+        if (__popcll((unsigned long long)__ballot(v >= trial)) >= a.top_k) bits = trial;
       }
     } else {
+      uint32_t v[4];
 #pragma unroll
-      for (int j = 0; j < VE; ++j) {
-        const int64_t i = first + j;
-        x[v * VE + j] = i >= 0 && i < a.vocab ? lp_at<BF16>(row, i) : -__builtin_inff();
+      for (int i = 0; i < 4; ++i) v[i] = maxima[lane + 64 * i];
+#pragma unroll
+      for (int bit = 31; bit >= 16; --bit) {
+        const uint32_t trial = bits | 1u << bit;
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) n += __popcll((unsigned long long)__ballot(v[i] >= trial));
+        if (n >= a.top_k) bits = trial;
       }
     }
-  }
-  // waves whose every lane holds a value of the row; with none the split has
-  // fewer than 64 words, all of which can be held
-  const int64_t words = (a.vocab + shift + VE - 1) / VE - (int64_t)split * (kLpSplit / VE);
-  const int full = words >= kLpThreads ? kLpWaves : words < 0 ? 0 : (int)(words / 64);
-  __shared__ float red[kLpWaves][2];
-  __shared__ uint32_t bound[kLpWaves];
-  __shared__ int count;
-  __shared__ uint64_t cand[kLpCand];
-  float m = -__builtin_inff();
+    // keys below the one of -inf (no maximum there) are NaN patterns
+    const float low = bits < 0x00800000u ? -__builtin_inff() : key_logit(bits);
+    // each wave's values at or above the bound, in a list of its own
+    int n = 0;
+    uint64_t* list = cand + wave * kLpWaveCand;   // (bits, index), not yet in order
 #pragma unroll
-  for (int i = 0; i < kLpPer; ++i) m = fmaxf(m, x[i]);
-  uint32_t lane_key = 0;   // of this lane's maximum, NaN above all
-  if (a.top_k > 0) {
-    bool nan = false;
+    for (int q = 0; q < kLpPer / 4; ++q) {
+      if (!__ballot(quad_max[q] >= low)) continue;
 #pragma unroll
-    for (int i = 0; i < kLpPer; ++i) nan = nan || x[i] != x[i];
-    lane_key = nan ? kNanKey : logit_key(m);
-  }
-  m = lp_wave_max(m);
-  if (lane == 0) red[wave][0] = m;
-  if (a.top_k > 0) {
-    // the ceil(k / full)-th greatest lane maximum of this wave
-    uint32_t k = lane_key, b = 0;
-    const int need = full > 0 ? (a.top_k + full - 1) / full : 0;
-    for (int i = 0; i < need; ++i) {
-      b = lp_wave_max_key(k);
-      const uint64_t at = __ballot(k == b);
-      if (lane == __ffsll((unsigned long long)at) - 1) k = 0;
-    }
-    if (lane == 0) bound[wave] = b;
-    if (tid == 0) count = 0;
-  }
-  __syncthreads();
-  m = fmaxf(fmaxf(red[0][0], red[1][0]), fmaxf(red[2][0], red[3][0]));
-  __syncthreads();
-  const float base = m == -__builtin_inff() ? 0.f : m;   // nothing but -inf: sums of 0
-  float l = 0.f, t = 0.f;
-#pragma unroll
-  for (int i = 0; i < kLpPer; ++i) {
-    const float d = x[i] - base, e = lp_exp(d);
-    l += e;
-    t += e > 0.f ? e * d : 0.f;
-  }
-  l = lp_wave_sum(l);
-  t = lp_wave_sum(t);
-  if (lane == 0) {
-    red[wave][0] = l;
-    red[wave][1] = t;
-  }
-  uint32_t low = 0;
-  if (a.top_k > 0) {
-    low = full > 0 ? bound[0] : 0;
-    for (int w = 1; w < full; ++w) low = bound[w] < low ? bound[w] : low;
-    if (lane_key >= low) {
-#pragma unroll
-      for (int i = 0; i < kLpPer; ++i) {
+      for (int i = 4 * q; i < 4 * q + 4; ++i) {
+        uint64_t at = __ballot(x[i] >= low);
+        if (!at) continue;
         const int index = idx0[i / VE] + i % VE;
-        const uint32_t key = logit_key(x[i]);
-        if (key >= low && index >= 0 && index < a.vocab) {
-          const int at = atomicAdd(&count, 1);
-          if (at < kLpCand) cand[at] = logit_order(key, (uint32_t)index);
-        }
+        if (!within) at &= __ballot(index >= 0 && index < a.vocab);   // not what fills up an edge split
+        const int rank = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(at >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)at, 0));
+        if ((at >> lane & 1) && rank < kLpWaveCand) list[rank] = (uint64_t)__float_as_uint(x[i]) << 32 | (uint32_t)index;
+        n += __popcll((unsigned long long)at);
       }
     }
+    if (lane == 0) counts[wave] = n;
+    __syncthreads();
   }
-  __syncthreads();
-  l = (red[0][0] + red[1][0]) + (red[2][0] + red[3][0]);
-  t = (red[0][1] + red[1][1]) + (red[2][1] + red[3][1]);
   const bool whole = a.splits == 1;
+  // the split's sums; the first wave needs them, and every wave where the row
+  // ends here
+  float nan_sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kLpWaves; ++w) nan_sum += red[w][1];
+  float base = 0.f;
+  if (wave == 0 || whole) {
+    m = fmaxf(fmaxf(red[0][0], red[1][0]), fmaxf(red[2][0], red[3][0]));
+    base = m == -__builtin_inff() ? 0.f : m;
+    l = t = 0.f;
+#pragma unroll
+    for (int w = 0; w < kLpWaves; ++w) {
+      const float wm = red[w][0], d = wm == -__builtin_inff() ? 0.f : wm - base, f = lp_exp(d);
+      l = fmaf(f, red[w][1], l);
+      t = fmaf(f, fmaf(red[w][1], fmaxf(d, -1000.f), red[w][2]), t);
+    }
+  }
   if (tid == 0 && !whole) *reinterpret_cast<float4*>(a.part + (r * a.splits + split) * 4) = make_float4(base, l, t, m);
   if (a.top_k > 0) {
-    const float logl = logf(l);
+    const float logl = whole ? logf(l) : 0.f;
     auto put = [&](int rank, uint64_t c) {
       if (whole) {
         a.top_id[r * a.top_k + rank] = (int32_t)~(uint32_t)c;
@@ -230,20 +287,64 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_split_kernel(const Logpro
         a.cand[(r * a.splits + split) * a.top_k + rank] = c;
       }
     };
-    const int have = count;
-    if (have <= kLpCand) {
-      lp_order(cand, have, a.top_k, tid, put);
+    int have = 0;
+    bool fits = nan_sum == nan_sum;   // NaN passed the maxima over
+#pragma unroll
+    for (int w = 0; w < kLpWaves; ++w) {
+      have += counts[w];
+      fits = fits && counts[w] <= kLpWaveCand;
+    }
+    if (fits) {
+      if (have <= 64) {
+        // one wave, a value per lane, read out lane by lane
+        if (wave == 0) {
+          int w = 0, before = 0;
+#pragma unroll
+          for (int v = 0; v < kLpWaves - 1; ++v) {
+            if (lane >= before + counts[v] && w == v) {
+              before += counts[v];
+              w = v + 1;
+            }
+          }
+          uint64_t c = 0;
+          if (lane < have) {
+            const uint64_t v = cand[w * kLpWaveCand + lane - before];
+            c = logit_order(logit_key(__uint_as_float((uint32_t)(v >> 32))), (uint32_t)v);
+          }
+          int rank = 0;
+          for (int j = 0; j < have; ++j)
+            rank += ((uint64_t)lane_word((uint32_t)(c >> 32), j) << 32 | lane_word((uint32_t)c, j)) > c;
+          if (lane < have && rank < a.top_k) put(rank, c);
+        }
+      } else {
+        for (int i = tid; i < kLpCand; i += kLpThreads) {
+          const uint64_t v = cand[i];
+          if (i % kLpWaveCand < counts[i / kLpWaveCand])
+            cand[i] = logit_order(logit_key(__uint_as_float((uint32_t)(v >> 32))), (uint32_t)v);
+        }
+        __syncthreads();
+        for (int i = tid; i < kLpCand; i += kLpThreads) {
+          const int w = i / kLpWaveCand;
+          if (i % kLpWaveCand >= counts[w]) continue;
+          const uint64_t c = cand[i];
+          int rank = 0;
+          for (int v = 0; v < kLpWaves; ++v)
+            for (int j = 0; j < counts[v]; ++j) rank += cand[v * kLpWaveCand + j] > c;
+          if (rank < a.top_k) put(rank, c);
+        }
+      }
       // a split of fewer values than k
       if (!whole && tid >= have && tid < a.top_k) put(tid, 0);
     } else {
-      // more ties than fit: k times the greatest value below the last one
+      // more ties than fit, or NaN: k times the greatest value below the last
+      // one, the split read again for each
+      const int64_t first = start < 0 ? 0 : start;
+      const int64_t past = start + kLpSplit < a.vocab ? start + kLpSplit : a.vocab;
       uint64_t last = ~0ull;
       for (int k = 0; k < a.top_k; ++k) {
         uint64_t best = 0;
-#pragma unroll
-        for (int i = 0; i < kLpPer; ++i) {
-          const int index = idx0[i / VE] + i % VE;
-          const uint64_t c = index >= 0 && index < a.vocab ? logit_order(logit_key(x[i]), (uint32_t)index) : 0;
+        for (int64_t i = first + tid; i < past; i += kLpThreads) {
+          const uint64_t c = logit_order(logit_key(lp_at<BF16>(row, i)), (uint32_t)i);
           if (c < last && c > best) best = c;
         }
         best = lp_wave_max_order(best);
@@ -270,7 +371,7 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_join_kernel(const Logprob
   const float4* part = reinterpret_cast<const float4*>(a.part) + r * a.splits;
   float M = -__builtin_inff();
   for (int i = lane; i < a.splits; i += 64) M = fmaxf(M, part[i].w);
-  M = lp_wave_max(M);
+  M = wave_max(M);
   const float base = M == -__builtin_inff() ? 0.f : M;
   float L = 0.f, T = 0.f;
   for (int i = lane; i < a.splits; i += 64) {
@@ -283,17 +384,65 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_join_kernel(const Logprob
     L += p.y * f;
     T += f > 0.f ? f * (p.z + p.y * d) : 0.f;
   }
-  L = lp_wave_sum(L);
-  T = lp_wave_sum(T);
+  L = wave_sum(L);
+  T = wave_sum(T);
   const uint8_t* row = a.x + r * a.row_stride * (BF16 ? 2 : 4);
   lp_finish<BF16>(a, r, row, M, L, T, tid);
   if (a.top_k == 0) return;
   const float logl = logf(L);
-  // Candidates: the splits' lists, in rounds that fit (the best so far ahead).
+  // Candidates: the splits' lists, each in order. The q-th greatest of the
+  // lists' r-th values, q r >= k, bounds the row's k-th value from below; r is
+  // chosen to make q about half of the lists. What reaches the bound (a few
+  // more than k) is put in order by counting.
   __shared__ uint64_t cand[kLpCand];
   __shared__ uint64_t best[kLpMaxTop];
+  __shared__ uint64_t low;
+  __shared__ int count;
   const uint64_t* lists = a.cand + r * a.splits * a.top_k;
   const int64_t total = (int64_t)a.splits * a.top_k;
+  auto put = [&](int rank, uint64_t c) {
+    a.top_id[r * a.top_k + rank] = (int32_t)~(uint32_t)c;
+    a.top_lp[r * a.top_k + rank] = (key_logit((uint32_t)(c >> 32)) - M) - logl;
+  };
+  if (total <= 16 * kLpThreads) {
+    uint64_t mine[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) mine[i] = tid + i * kLpThreads < total ? lists[tid + i * kLpThreads] : 0;
+    const int heads = a.splits < 64 ? a.splits : 64;
+    int at = (2 * a.top_k + heads - 1) / heads;   // r
+    if (at > a.top_k) at = a.top_k;
+    const int q = (a.top_k + at - 1) / at;        // <= heads: at >= 2 k / heads, or at = k
+    if (tid == 0) {
+      low = 0;
+      count = 0;
+    }
+    if (tid < heads) cand[tid] = lists[(int64_t)tid * a.top_k + at - 1];
+    __syncthreads();
+    if (tid < heads) {
+      const uint64_t c = cand[tid];
+      int rank = 0;
+      for (int j = 0; j < heads; ++j) rank += cand[j] > c;
+      if (rank == q - 1 && c) low = c;   // values differ; 0 stands for a list too short
+    }
+    __syncthreads();
+    const uint64_t bound = low;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (mine[i] && mine[i] >= bound) {
+        const int w = atomicAdd(&count, 1);
+        if (w < kLpCand) cand[w] = mine[i];
+      }
+    }
+    __syncthreads();
+    const int have = count;
+    if (have <= kLpCand) {
+      lp_order(cand, have, a.top_k, tid, put);
+      return;
+    }
+    __syncthreads();
+  }
+  // too many to hold: in rounds that fit, the best so far ahead
   int held = 0;   // best so far, in cand[0 .. held)
   for (int64_t at = 0; at < total;) {
     const int64_t room = kLpCand - held;
@@ -305,10 +454,7 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_join_kernel(const Logprob
     const bool done = at >= total;
     lp_order(cand, count, a.top_k, tid, [&](int rank, uint64_t c) {
       if (!done) best[rank] = c;
-      else if (c) {
-        a.top_id[r * a.top_k + rank] = (int32_t)~(uint32_t)c;
-        a.top_lp[r * a.top_k + rank] = (key_logit((uint32_t)(c >> 32)) - M) - logl;
-      }
+      else if (c) put(rank, c);
     });
     if (done) break;
     __syncthreads();
