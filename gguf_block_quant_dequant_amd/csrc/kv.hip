@@ -210,6 +210,7 @@ int gguf_kv_evict(const gguf_kv_cache* cache, int64_t n_seqs, const int32_t* pag
     const int64_t per = ((max_len + kEvictThreads - 1) / kEvictThreads + 3) / 4 * 4;   // slots per thread
     if (per <= 4) hipLaunchKernelGGL(kv_evict_select_kernel<4>, grid, block, 0, stream, a);
     else if (per <= 8) hipLaunchKernelGGL(kv_evict_select_kernel<8>, grid, block, 0, stream, a);
+    else if (per <= 16) hipLaunchKernelGGL(kv_evict_select_kernel<16>, grid, block, 0, stream, a);
     else if (per <= 32) hipLaunchKernelGGL(kv_evict_select_kernel<32>, grid, block, 0, stream, a);
     else hipLaunchKernelGGL(kv_evict_select_kernel<0>, grid, block, 0, stream, a);
     st = abi_launched();

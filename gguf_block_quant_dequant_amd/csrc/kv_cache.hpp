@@ -208,6 +208,7 @@ struct EvictArgs {
 
 constexpr int kEvictThreads = 1024;
 constexpr int kEvictWaves = kEvictThreads / 64;
+constexpr int kEvictFew = 4;      // slots past the budget up to which they are picked one by one
 constexpr int kHistCopies = 16;   // copies of a digit's histogram, lane & 15: a few shared leading
                                   // digits (weights have few exponents) would queue on one LDS word
 
@@ -251,7 +252,7 @@ __device__ __forceinline__ int block_scan(int v, int* lds /* kEvictWaves + 1 */,
 // are prefix sums over slots.
 template <int R>
 __global__ __launch_bounds__(kEvictThreads) void kv_evict_select_kernel(const EvictArgs a) {
-  __shared__ int hist[256 * kHistCopies];
+  __shared__ __align__(16) int hist[256 * kHistCopies + 1024];
   __shared__ int digit_sum[256];
   __shared__ int scan[kEvictWaves + 1];
   __shared__ int pick[2];
@@ -264,24 +265,31 @@ __global__ __launch_bounds__(kEvictThreads) void kv_evict_select_kernel(const Ev
     return;
   }
   const int32_t* row = a.table + (int64_t)s * a.table_stride;
-  int S = ((n + kEvictThreads - 1) / kEvictThreads + 3) & ~3;   // slots per thread
+  const int S = R > 0 ? R : ((n + kEvictThreads - 1) / kEvictThreads + 3) & ~3;   // slots per thread
   const int first = tid * S;   // 1024 * S < 2^31: n is
-  // four consecutive slots share a page
-  auto page4 = [&](int slot) { return kv_page(row, slot >> a.c.shift, a.table_stride, a.c.n_pages); };
-  int newest = -1;
-  if (a.recent > 0) {
-    int m = INT32_MIN;
-    for (int r = 0; r < S; r += 4) {
-      const int slot = first + r;
-      if (slot >= n) break;
-      const int32_t page = page4(slot);
-      if (page < 0) continue;
-      const int4 p = *reinterpret_cast<const int4*>(a.c.pos + kv_slot_at(a.c, page, h, slot & (a.c.ps - 1)));
-      const int q[4] = {p.x, p.y, p.z, p.w};
+  // Four consecutive slots share a page. Every load goes out, from page 0 where
+  // there is none (the value is then not used), so that none waits for another.
+  auto page4 = [&](int slot) { return slot < n ? kv_page(row, slot >> a.c.shift, a.table_stride, a.c.n_pages) : -1; };
+  auto at4 = [&](int32_t page, int slot) { return kv_slot_at(a.c, page < 0 ? 0 : page, h, slot & (a.c.ps - 1)); };
+  constexpr int kRegs = R > 0 ? R : 4;
+  uint32_t key[kRegs];
+  // the keys of four slots, a slot without a page below all others
+  int newest = 0;   // position; protected: within `recent` of it (the difference fits 32 bits unsigned)
+  const uint32_t recent = (uint32_t)a.recent;
+  auto keys4 = [&](int32_t page, const float4& w, const int4& p, uint32_t* k) {
+    const float f[4] = {w.x, w.y, w.z, w.w};
+    const int q[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (slot + j < n) m = q[j] > m ? q[j] : m;
-    }
+    for (int j = 0; j < 4; ++j)
+      k[j] = page < 0 ? 0u : (uint32_t)newest - (uint32_t)q[j] < recent ? kKeyProtected : weight_key(f[j]);
+  };
+  auto newest4 = [&](int32_t page, int slot, const int4& p, int m) {
+    const int q[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = page >= 0 && slot + j < n && q[j] > m ? q[j] : m;
+    return m;
+  };
+  auto block_max = [&](int m) {
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) {
       const int o = __shfl_xor(m, d);
@@ -289,55 +297,135 @@ __global__ __launch_bounds__(kEvictThreads) void kv_evict_select_kernel(const Ev
     }
     if (lane == 0) scan[tid >> 6] = m;
     __syncthreads();
-    newest = INT32_MIN;
+    m = INT32_MIN;
 #pragma unroll
-    for (int w = 0; w < kEvictWaves; ++w) newest = scan[w] > newest ? scan[w] : newest;
+    for (int w = 0; w < kEvictWaves; ++w) m = scan[w] > m ? scan[w] : m;
     __syncthreads();
-  }
-  auto load4 = [&](int slot, uint32_t (&k)[4]) {
-    const int32_t page = slot < n ? page4(slot) : -1;
+    return m;
+  };
+  if constexpr (R > 0) {
+    // A wave's 64 R slots as they lie in memory, 256 per load (a thread's own R
+    // would cost a cache line per lane and load); through LDS they then go to
+    // their threads.
+    const int base = (tid >> 6) * 64 * R + lane * 4;
+    int32_t page[R / 4];
+    float4 w[R / 4];
+    int4 p[R / 4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) k[j] = 0u;   // a slot without a page goes first
-    if (page < 0) return;
-    const int64_t at = kv_slot_at(a.c, page, h, slot & (a.c.ps - 1));
-    const float4 w = *reinterpret_cast<const float4*>(a.c.weight + at);
-    const float f[4] = {w.x, w.y, w.z, w.w};
+    for (int r = 0; r < R / 4; ++r) page[r] = page4(base + 256 * r);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) k[j] = weight_key(f[j]);
+    for (int r = 0; r < R / 4; ++r) {
+      const int64_t at = at4(page[r], base + 256 * r);
+      w[r] = *reinterpret_cast<const float4*>(a.c.weight + at);
+      p[r] = a.recent > 0 ? *reinterpret_cast<const int4*>(a.c.pos + at) : make_int4(0, 0, 0, 0);
+    }
     if (a.recent > 0) {
-      const int4 p = *reinterpret_cast<const int4*>(a.c.pos + at);
-      const int q[4] = {p.x, p.y, p.z, p.w};
+      int m = INT32_MIN;
+#pragma unroll
+      for (int r = 0; r < R / 4; ++r) m = newest4(page[r], base + 256 * r, p[r], m);
+      newest = block_max(m);
+    }
+    // 256 slots in rows of R, one row per thread; padded against bank conflicts
+    constexpr int kRow = R >= 16 ? R + 4 : R, kRows = 256 / R;
+    uint32_t* const tile = reinterpret_cast<uint32_t*>(hist) + (tid >> 6) * (kRows * kRow);
+    static_assert(kEvictWaves * kRows * kRow <= 256 * kHistCopies + 1024, "the tiles fit the histogram's memory");
+#pragma unroll
+    for (int r = 0; r < R / 4; ++r) {
+      uint32_t k4[4];
+      keys4(page[r], w[r], p[r], k4);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if ((int64_t)q[j] > (int64_t)newest - a.recent) k[j] = kKeyProtected;
-    }
-  };
-  constexpr int kRegs = R > 0 ? R : 4;
-  uint32_t key[kRegs];
-  if constexpr (R > 0) {
+        if (base + 256 * r + j >= n) k4[j] = 0u;   // behind the end: after every slot in every order
+      *reinterpret_cast<uint4*>(tile + 4 * lane / R * kRow + 4 * lane % R) = make_uint4(k4[0], k4[1], k4[2], k4[3]);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      if (lane / kRows == r) {
 #pragma unroll
-    for (int r = 0; r < R; r += 4) {
-      uint32_t k4[4] = {0u, 0u, 0u, 0u};
-      if (r < S) load4(first + r, k4);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) key[r + j] = k4[j];
+        for (int j = 0; j < R; j += 4) {
+          const uint4 v = *reinterpret_cast<const uint4*>(tile + lane % kRows * kRow + j);
+          key[j] = v.x; key[j + 1] = v.y; key[j + 2] = v.z; key[j + 3] = v.w;
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
+    __syncthreads();   // the memory becomes the histogram
+  } else if (a.recent > 0) {
+    int m = INT32_MIN;
+    for (int r = 0; r < S; r += 4) {
+      const int32_t page = page4(first + r);
+      m = newest4(page, first + r, *reinterpret_cast<const int4*>(a.c.pos + at4(page, first + r)), m);
+    }
+    newest = block_max(m);
   }
-  // calls fn(slot, key) for the thread's slots in order
+  // Calls fn(index, key) for the thread's slots first + index in order. With
+  // keys in registers also for those behind the end: key 0 and the highest
+  // slots, they are never among the kept, nor before the budget.
   auto each = [&](auto&& fn) {
     if constexpr (R > 0) {
 #pragma unroll
       for (int r = 0; r < R; ++r)
-        if (r < S && first + r < n) fn(first + r, key[r]);
+        fn(r, key[r]);
     } else {
       for (int r = 0; r < S && first + r < n; r += 4) {
-        load4(first + r, key);
+        const int32_t page = page4(first + r);
+        const int64_t at = at4(page, first + r);
+        keys4(page, *reinterpret_cast<const float4*>(a.c.weight + at),
+              a.recent > 0 ? *reinterpret_cast<const int4*>(a.c.pos + at) : make_int4(0, 0, 0, 0), key);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (first + r + j < n) fn(first + r + j, key[j]);
+          if (first + r + j < n) fn(r + j, key[j]);
       }
     }
   };
+  const int over = n - budget;
+  if (over <= kEvictFew) {
+    // A sequence that grew past its budget by a few slots (one, step by step):
+    // the least key, of equal ones the highest slot, goes, `over` times.
+    __shared__ uint64_t least[kEvictWaves];
+    uint64_t gone = 0;   // keys up to this one are out
+    int out[kEvictFew];
+    for (int i = 0; i < over; ++i) {
+      uint64_t best = ~0ull;
+      each([&](int r, uint32_t k) {
+        const uint64_t c = (uint64_t)k << 32 | (uint32_t)(INT32_MAX - first - r);   // above 0, and distinct
+        if (first + r < n && c > gone && c < best) best = c;
+      });
+#pragma unroll
+      for (int d = 32; d >= 1; d >>= 1) {
+        const uint64_t o = __shfl_xor((unsigned long long)best, d);
+        best = o < best ? o : best;
+      }
+      if (lane == 0) least[tid >> 6] = best;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kEvictWaves; ++w) best = least[w] < best ? least[w] : best;
+      __syncthreads();
+      gone = best;
+#pragma unroll
+      for (int j = 0; j < kEvictFew; ++j)
+        if (j == i) out[j] = INT32_MAX - (int)(uint32_t)best;
+    }
+    if (tid == 0) {
+      int32_t* dst = a.dst + pair * a.max_moves;
+      int32_t* src = a.src + pair * a.max_moves;
+      int moves = 0, tails = 0;
+      // kept slots behind the budget, and the vacated ones before it, ascending
+      for (int slot = budget; slot < n; ++slot) {
+        bool keep = true;
+#pragma unroll
+        for (int j = 0; j < kEvictFew; ++j) keep = keep && !(j < over && out[j] == slot);
+        if (keep) src[tails++] = slot;
+      }
+      for (int last = -1; moves < tails; ++moves) {
+        int next = INT32_MAX;
+#pragma unroll
+        for (int j = 0; j < kEvictFew; ++j)
+          if (j < over && out[j] > last && out[j] < next) next = out[j];
+        dst[moves] = last = next;
+      }
+      a.count[pair] = moves;
+    }
+    return;
+  }
   uint32_t prefix = 0;   // digits chosen so far
   int want = budget;     // rank (from the top) still to place among keys with the prefix
   for (int shift = 24; shift >= 0; shift -= 8) {
@@ -388,24 +476,52 @@ __global__ __launch_bounds__(kEvictThreads) void kv_evict_select_kernel(const Ev
   each([&](int, uint32_t k) { equal += k == prefix; });
   int all;
   int eq_rank = block_scan(equal, scan, &all);
+  const int cut = budget - first;   // the thread's slots from this index on are behind the budget
   int holes = 0, tails = 0, e = eq_rank;
-  each([&](int slot, uint32_t k) {
-    bool keep = k > prefix;
-    if (k == prefix) keep = e++ < want;
-    holes += slot < budget && !keep;
-    tails += slot >= budget && keep;
-  });
-  int hole_at = block_scan(holes, scan, &all);
-  int tail_at = block_scan(tails, scan, &all);
-  e = eq_rank;
-  int32_t* dst = a.dst + pair * a.max_moves;
-  int32_t* src = a.src + pair * a.max_moves;
-  each([&](int slot, uint32_t k) {
-    bool keep = k > prefix;
-    if (k == prefix) keep = e++ < want;
-    if (slot < budget && !keep) dst[hole_at++] = slot;
-    if (slot >= budget && keep) src[tail_at++] = slot;
-  });
+  if constexpr (R > 0) {
+    uint32_t keep = 0;   // bit per slot
+    each([&](int r, uint32_t k) {
+      const bool same = k == prefix;
+      keep |= (uint32_t)(k > prefix || (same && e < want)) << r;
+      e += same;
+    });
+    const uint32_t before = cut <= 0 ? 0u : cut >= R ? (uint32_t)((uint64_t(1) << R) - 1) : (1u << cut) - 1u;
+    uint32_t hole = ~keep & before, tail = keep & ~before;
+    holes = __popc(hole);
+    tails = __popc(tail);
+    int hole_at = block_scan(holes, scan, &all);
+    int tail_at = block_scan(tails, scan, &all);
+    int32_t* dst = a.dst + pair * a.max_moves + hole_at;
+    int32_t* src = a.src + pair * a.max_moves + tail_at;
+    while (hole) {
+      const int r = __ffs(hole) - 1;
+      hole &= hole - 1;
+      *dst++ = first + r;
+    }
+    while (tail) {
+      const int r = __ffs(tail) - 1;
+      tail &= tail - 1;
+      *src++ = first + r;
+    }
+  } else {
+    each([&](int r, uint32_t k) {
+      bool keep = k > prefix;
+      if (k == prefix) keep = e++ < want;
+      holes += r < cut && !keep;
+      tails += r >= cut && keep;
+    });
+    int hole_at = block_scan(holes, scan, &all);
+    int tail_at = block_scan(tails, scan, &all);
+    e = eq_rank;
+    int32_t* dst = a.dst + pair * a.max_moves;
+    int32_t* src = a.src + pair * a.max_moves;
+    each([&](int r, uint32_t k) {
+      bool keep = k > prefix;
+      if (k == prefix) keep = e++ < want;
+      if (r < cut && !keep) dst[hole_at++] = first + r;
+      if (r >= cut && keep) src[tail_at++] = first + r;
+    });
+  }
   if (tid == 0) a.count[pair] = all;
 }
 
@@ -461,24 +577,25 @@ __global__ __launch_bounds__(kMoveThreads) void kv_evict_move_kernel(const Evict
           *reinterpret_cast<const uint4*>(a.c.k + sp[r] + (ss[r] * DIM + o * 8) * 2);
   }
   if (rows >= 16) {
-    // lane per move, eight dims of a wave in flight
+    // lane per move, kBatch dims of a wave in flight
+    constexpr int kBatch = 16;
     if (lane < rows && ss[lane] >= 0) {
       const uint8_t* from = a.c.v + sp[lane];
       uint8_t* to = a.c.v + dp[lane];
       const int f = ss[lane], t = ds[lane];
-      for (int d0 = (tid >> 6) * 8; d0 < DIM; d0 += (kMoveThreads / 64) * 8) {
+      for (int d0 = (tid >> 6) * kBatch; d0 < DIM; d0 += (kMoveThreads / 64) * kBatch) {
         if constexpr (KIND == kKvQ80) {
-          uint8_t x[8];
+          uint8_t x[kBatch];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = from[(d0 + j) * a.c.ps + f];
+          for (int j = 0; j < kBatch; ++j) x[j] = from[(d0 + j) * a.c.ps + f];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) to[(d0 + j) * a.c.ps + t] = x[j];
+          for (int j = 0; j < kBatch; ++j) to[(d0 + j) * a.c.ps + t] = x[j];
         } else {
-          uint16_t x[8];
+          uint16_t x[kBatch];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = reinterpret_cast<const uint16_t*>(from)[(d0 + j) * a.c.ps + f];
+          for (int j = 0; j < kBatch; ++j) x[j] = reinterpret_cast<const uint16_t*>(from)[(d0 + j) * a.c.ps + f];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) reinterpret_cast<uint16_t*>(to)[(d0 + j) * a.c.ps + t] = x[j];
+          for (int j = 0; j < kBatch; ++j) reinterpret_cast<uint16_t*>(to)[(d0 + j) * a.c.ps + t] = x[j];
         }
       }
     }

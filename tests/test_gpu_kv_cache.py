@@ -225,7 +225,7 @@ def test_evict_types_and_dims(kind, dim):
 @pytest.mark.parametrize("lengths,budget,recent", [
     ([1], 1, 1), ([2], 1, 0), ([2], 1, 1), ([33, 32, 31], 32, 0), ([33], 32, 32), ([500, 10], 499, 0), ([500], 1, 1),
     ([500], 250, 250), ([4096], 4095, 100), ([4097], 4096, 0), ([5000, 4000], 1000, 64), ([8192], 4096, 128),
-    ([8193], 100, 0), ([20000], 6000, 500), ([33000], 9000, 1000), ([70000], 65000, 10)])
+    ([8193], 100, 0), ([12000, 16384], 5000, 64), ([16385], 16000, 9), ([20000], 6000, 500), ([33000], 9000, 1000), ([70000], 65000, 10)])
 def test_evict_lengths(lengths, budget, recent):
     # each way of holding the keys (4, 8 and 32 per thread, and none), budgets at the edges
     rng = np.random.default_rng([lengths[0], budget])
@@ -322,3 +322,17 @@ def test_evict_refusals():
     with pytest.raises(ValueError):
         g.gguf_kv_evict(d["cache"], t, n.long(), 64, 10)
     assert host(n).tolist() == [64]
+
+
+@pytest.mark.parametrize("over", [1, 2, 3, 4, 5, 6])
+@pytest.mark.parametrize("budget", [1, 3, 16, 300, 4096, 33000])
+def test_evict_few_slots_past_the_budget(budget, over):
+    # a sequence that grows token by token; ties, weights of zero, holes that
+    # are the newest slots themselves
+    rng = np.random.default_rng([budget, over])
+    d = evict_case(rng, "bf16", [budget + over, max(1, budget - 1), budget + max(1, over - 1)], 64, hkv=2)
+    check_evict(d, budget, min(2, budget))
+    d = evict_case(rng, "f16", [budget + over], 16, hkv=1)
+    d["weight"][...] = 0.0
+    d["cache"].weight.copy_(dev(d["weight"]))
+    check_evict(d, budget, 0)
