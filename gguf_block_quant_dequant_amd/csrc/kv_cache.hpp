@@ -26,24 +26,34 @@ struct AppendArgs {
 constexpr int kAppendThreads = 256;
 constexpr int kAppendTile = 64;
 
-// Eight input values from element `i` of a row.
+// Eight input values from element `i` of a row, as loaded.
 template <bool BF16SRC>
-__device__ __forceinline__ void append_load8(const void* base, int64_t i, float (&x)[8]) {
-  if constexpr (BF16SRC) {
-    const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+struct Raw8 {
+  uint4 w[BF16SRC ? 1 : 2];
+  __device__ __forceinline__ void load(const void* base, int64_t i) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + i * (BF16SRC ? 2 : 4));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[2 * j] = __uint_as_float(u[j] << 16);
-      x[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
-    }
-  } else {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
-    const float4 a = p[0], b = p[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    for (int j = 0; j < (BF16SRC ? 1 : 2); ++j) w[j] = p[j];
   }
-}
+  __device__ __forceinline__ void values(float (&x)[8]) const {
+    if constexpr (BF16SRC) {
+      const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[2 * j] = __uint_as_float(u[j] << 16);
+        x[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        x[4 * j] = __uint_as_float(w[j].x);
+        x[4 * j + 1] = __uint_as_float(w[j].y);
+        x[4 * j + 2] = __uint_as_float(w[j].z);
+        x[4 * j + 3] = __uint_as_float(w[j].w);
+      }
+    }
+  }
+};
 
 // Rounds eight values to their cache form: 16-bit patterns, or Q8_0 codes (in
 // the low bytes) with the scale of the 32-dim block, whose other values the
@@ -84,9 +94,10 @@ __device__ __forceinline__ uint2 pack8x8(const uint16_t (&o)[8]) {
 
 // One block: `tile` consecutive tokens of one kv head. K rows go out as they
 // are; V goes through LDS to be written along the positions, eight consecutive
-// slots per 16-byte store where the tile holds a whole aligned group of them,
-// single slots elsewhere. Bound by the bytes read and written (a prompt) or by
-// its two dependent loads (a token).
+// slots per 16-byte store where the tile holds a whole aligned group of them
+// (the groups of a dim side by side: 128 bytes of 64 positions), single slots
+// elsewhere. Bound by the bytes read and written (a prompt) or by its dependent
+// loads (a token).
 template <int KIND, bool BF16SRC, int DIM>
 __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(const AppendArgs a) {
   constexpr int kOct = DIM / 8;             // 8-value groups of a row
@@ -95,7 +106,8 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(const AppendA
   __shared__ uint16_t vs[KIND == kKvQ80 ? kAppendTile * (DIM / 32) : 1];
   __shared__ int64_t head_at[kAppendTile];  // byte offset of the token's page and head; -1: dropped
   __shared__ int32_t slot_of[kAppendTile];  // slot within the page
-  __shared__ uint8_t unit[kAppendTile];     // 1: leads a whole group, 2: single, 0: in a group or dropped
+  __shared__ uint8_t leads_at[kAppendTile], single_at[kAppendTile];   // tokens that lead a whole group, single ones
+  __shared__ int n_lead, n_single;
   const int h = blockIdx.y, tid = threadIdx.x;
   const int64_t t0 = (int64_t)blockIdx.x * a.tile;
   if (tid < kAppendTile) {   // one wave
@@ -133,56 +145,75 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(const AppendA
     const uint64_t leads = __ballot(lead);
 #pragma unroll
     for (int j = 1; j < 8; ++j) covered = covered || (tid >= j && (leads >> (tid - j) & 1));
-    unit[tid] = at < 0 ? 0 : lead ? 1 : covered ? 0 : 2;
+    const bool single = at >= 0 && !lead && !covered;
+    const uint64_t singles = __ballot(single), below = (uint64_t(1) << tid) - 1;
+    if (lead) leads_at[__popcll((unsigned long long)(leads & below))] = (uint8_t)tid;
+    if (single) single_at[__popcll((unsigned long long)(singles & below))] = (uint8_t)tid;
+    if (tid == 0) {
+      n_lead = __popcll((unsigned long long)leads);
+      n_single = __popcll((unsigned long long)singles);
+    }
   }
   __syncthreads();
   const int rows = a.tile;
   constexpr int kRowStep = kAppendThreads / kOct;   // rows per pass (threads past the last whole row idle)
+  constexpr int kPasses = (kAppendTile + kRowStep - 1) / kRowStep;
   const int oct = tid % kOct, r0 = tid / kOct;
-  if (r0 < kRowStep) {
-    for (int r = r0; r < rows; r += kRowStep) {
-      const int64_t at = head_at[r];
-      if (at < 0) continue;   // whole rows drop: the lanes of a 32-dim block agree
+  Raw8<BF16SRC> rk[kPasses], rv[kPasses];
+  int64_t at[kPasses];   // all loads in flight before the first is used
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int r = r0 + i * kRowStep;
+    at[i] = r0 < kRowStep && r < rows ? head_at[r] : -1;
+    if (at[i] >= 0) {
       const int64_t e = (t0 + r) * a.row_stride + (int64_t)h * DIM + oct * 8;
-      float x[8];
-      uint16_t o[8], sc = 0;
-      append_load8<BF16SRC>(a.k, e, x);
-      append_round8<KIND>(x, o, &sc);
-      uint8_t* kp = a.c.k + at;
-      if constexpr (KIND == kKvQ80) {
-        *reinterpret_cast<uint2*>(kp + slot_of[r] * DIM + oct * 8) = pack8x8(o);
-        if ((oct & 3) == 0)
-          reinterpret_cast<uint16_t*>(kp + a.c.ps * DIM)[slot_of[r] * (DIM / 32) + (oct >> 2)] = sc;
-      } else {
-        *reinterpret_cast<uint4*>(kp + (slot_of[r] * DIM + oct * 8) * 2) = pack8x16(o);
-      }
-      append_load8<BF16SRC>(a.v, e, x);
-      append_round8<KIND>(x, o, &sc);
-      uint32_t* dst = reinterpret_cast<uint32_t*>(vt + r * kLdsRow + oct * 8);
-      const uint4 w = pack8x16(o);
-      dst[0] = w.x; dst[1] = w.y; dst[2] = w.z; dst[3] = w.w;
-      if constexpr (KIND == kKvQ80)
-        if ((oct & 3) == 0) vs[r * (DIM / 32) + (oct >> 2)] = sc;
+      rk[i].load(a.k, e);
+      rv[i].load(a.v, e);
     }
   }
-  __syncthreads();
-  // V: each wave takes a token's unit for 64 dims at a time
-  for (int i = tid; i < rows * DIM; i += kAppendThreads) {
-    const int r = i / DIM, d = i % DIM;
-    const int u = unit[r];
-    if (u == 0) continue;
-    uint8_t* vp = a.c.v + head_at[r];
-    const int at = d * a.c.ps + slot_of[r];
-    if (u == 1) {
-      uint16_t o[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = vt[(r + j) * kLdsRow + d];
-      if constexpr (KIND == kKvQ80) *reinterpret_cast<uint2*>(vp + at) = pack8x8(o);
-      else *reinterpret_cast<uint4*>(vp + at * 2) = pack8x16(o);
+  for (int i = 0; i < kPasses; ++i) {
+    if (at[i] < 0) continue;   // whole rows drop: the lanes of a 32-dim block agree
+    const int r = r0 + i * kRowStep;
+    float x[8];
+    uint16_t o[8], sc = 0;
+    rk[i].values(x);
+    append_round8<KIND>(x, o, &sc);
+    uint8_t* kp = a.c.k + at[i];
+    if constexpr (KIND == kKvQ80) {
+      *reinterpret_cast<uint2*>(kp + slot_of[r] * DIM + oct * 8) = pack8x8(o);
+      if ((oct & 3) == 0)
+        reinterpret_cast<uint16_t*>(kp + a.c.ps * DIM)[slot_of[r] * (DIM / 32) + (oct >> 2)] = sc;
     } else {
-      if constexpr (KIND == kKvQ80) vp[at] = (uint8_t)vt[r * kLdsRow + d];
-      else reinterpret_cast<uint16_t*>(vp)[at] = vt[r * kLdsRow + d];
+      *reinterpret_cast<uint4*>(kp + (slot_of[r] * DIM + oct * 8) * 2) = pack8x16(o);
     }
+    rv[i].values(x);
+    append_round8<KIND>(x, o, &sc);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(vt + r * kLdsRow + oct * 8);
+    const uint4 w = pack8x16(o);
+    dst[0] = w.x; dst[1] = w.y; dst[2] = w.z; dst[3] = w.w;
+    if constexpr (KIND == kKvQ80)
+      if ((oct & 3) == 0) vs[r * (DIM / 32) + (oct >> 2)] = sc;
+  }
+  __syncthreads();
+  // V, a dim's groups side by side
+  const int nl = n_lead, ns = n_single;
+  for (int i = tid; i < nl * DIM; i += kAppendThreads) {
+    const int d = nl == 8 ? i >> 3 : i / nl, r = leads_at[i - d * nl];
+    uint8_t* vp = a.c.v + head_at[r];
+    const int to = d * a.c.ps + slot_of[r];
+    uint16_t o[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = vt[(r + j) * kLdsRow + d];
+    if constexpr (KIND == kKvQ80) *reinterpret_cast<uint2*>(vp + to) = pack8x8(o);
+    else *reinterpret_cast<uint4*>(vp + to * 2) = pack8x16(o);
+  }
+  for (int i = tid; i < ns * DIM; i += kAppendThreads) {
+    const int d = i / ns, r = single_at[i - d * ns];
+    uint8_t* vp = a.c.v + head_at[r];
+    const int to = d * a.c.ps + slot_of[r];
+    if constexpr (KIND == kKvQ80) vp[to] = (uint8_t)vt[r * kLdsRow + d];
+    else reinterpret_cast<uint16_t*>(vp)[to] = vt[r * kLdsRow + d];
   }
   if constexpr (KIND == kKvQ80) {
     for (int i = tid; i < rows * (DIM / 32); i += kAppendThreads) {
