@@ -5,7 +5,7 @@
 
 namespace gqk {
 
-constexpr int64_t kAttnMaxLen = int64_t(1) << 30;   // 32-bit position arithmetic
+constexpr int64_t kAttnMaxLen = int64_t(1) << 25;   // splits of at least 1024 positions lie along a grid axis of 65535
 constexpr int64_t kAttnBlocks = 1024;               // blocks a call aims for
 
 // How a call is cut and what its workspace holds.
@@ -36,7 +36,7 @@ static int attn_plan(const KvView& c, int64_t n_seqs, int64_t n_heads, int64_t m
   if (chunk < 2 * round) chunk = 2 * round;
   if (chunk > most) chunk = most;
   p->chunk = (int32_t)chunk;
-  p->splits = (int32_t)((p->span + chunk - 1) / chunk);   // <= 2^30 / 256
+  p->splits = (int32_t)((p->span + chunk - 1) / chunk);   // <= 2^25 / 1024 past the first 1024 blocks
   // No shorter span, as a window leaves, is cut into more splits than this
   // (the count itself may grow as the span shrinks past a rounding of the chunk).
   p->most_splits = (p->span + most - 1) / most;
@@ -144,8 +144,9 @@ int gguf_attn_decode(const gguf_kv_cache* cache, const float* q, int64_t q_strid
   a.head_tiles = p.head_tiles;
   a.splits = p.splits;
   a.chunk = p.chunk;
+  a.chunk_pages = (p.chunk + a.c.ps - 1) / a.c.ps + 1 < 64 ? (p.chunk + a.c.ps - 1) / a.c.ps + 1 : 64;
   a.qscale = scale * 1.44269504088896340736f;
-  const dim3 grid((unsigned)p.splits, (unsigned)(a.c.hkv * p.head_tiles), (unsigned)n_seqs);
+  const dim3 grid((unsigned)(a.c.hkv * p.head_tiles), (unsigned)n_seqs, (unsigned)p.splits);
   if (cache->type == GGUF_KV_TYPE_F16) launch_attn_f16(a, track != 0, grid, stream);
   else if (cache->type == GGUF_KV_TYPE_BF16) launch_attn_bf16(a, track != 0, grid, stream);
   else launch_attn_q8_0(a, track != 0, grid, stream);

@@ -34,7 +34,7 @@ struct AttnArgs {
   float* part_ml;   // [n_seqs][n_heads][splits][2]: maximum (log2 domain) and sum
   float* scores;    // [n_seqs][n_heads][score_stride] (track): log2-domain scores
   int64_t table_stride, q_stride, out_stride, max_len, window, score_stride;
-  int32_t n_heads, group, head_tiles, splits, chunk;
+  int32_t n_heads, group, head_tiles, splits, chunk, chunk_pages;
   float qscale;     // scale * log2(e)
 };
 
@@ -105,30 +105,55 @@ __device__ __forceinline__ uint4 codes_bf16(const uint2& q) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// The same as fp16: with the sign bit flipped a code is 0 .. 255, as the low
+// byte of an fp16 between 1024 and 1279 (one unit per code).
+__device__ __forceinline__ uint4 codes_f16(const uint2& q) {
+  typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+  const f16x2 off = {(_Float16)1152.0f, (_Float16)1152.0f};
+  const uint32_t a = q.x ^ 0x80808080u, b = q.y ^ 0x80808080u;
+  const uint32_t w[4] = {__builtin_amdgcn_perm(0x64646464u, a, 0x04010400u), __builtin_amdgcn_perm(0x64646464u, a, 0x04030402u),
+                         __builtin_amdgcn_perm(0x64646464u, b, 0x04010400u), __builtin_amdgcn_perm(0x64646464u, b, 0x04030402u)};
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o[j] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, w[j]) - off);
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 // A wave's 32 positions of K or V as loaded.
+// Q8_0: the 4 NB words of scales of a lane's eight positions (pairs of halves; K
+// [position][block], V [block][position]) are the same for the 16 lanes of its
+// group: lane c of the 16 holds words c and c + 16.
 template <int KIND, int NB>
 struct AttnK {
   uint4 x[2][KIND == kKvQ80 ? 1 : NB];
   uint2 c[2][KIND == kKvQ80 ? NB : 1];
-  uint4 d[KIND == kKvQ80 ? NB : 1];   // scales of the lane's eight positions, [position][block]
+  uint32_t d[(4 * NB + 15) / 16];
 };
 template <int KIND, int NB>
 struct AttnV {
   uint4 x[KIND == kKvQ80 ? 1 : 2 * NB];
   uint2 c[KIND == kKvQ80 ? 2 * NB : 1];
-  uint4 d[KIND == kKvQ80 ? NB : 1];   // scales of the lane's eight positions, [block][position]
+  uint32_t d[(4 * NB + 15) / 16];
 };
 
 __device__ __forceinline__ uint4 load16(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
 __device__ __forceinline__ uint2 load8(const uint8_t* p) { return *reinterpret_cast<const uint2*>(p); }
 
-// Half i of a run of 16-byte words.
-template <int N>
-__device__ __forceinline__ float half_of(const uint4 (&d)[N], int i) {
-  const uint4& w = d[i >> 3];
-  const int j = (i >> 1) & 3;
-  const uint32_t u = j == 0 ? w.x : j == 1 ? w.y : j == 2 ? w.z : w.w;
-  return (i & 1) ? half_hi(u) : half_lo(u);
+__device__ __forceinline__ uint32_t load4(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
+
+// The lanes' word I as an array of both halves, from the lane of the 16 that
+// holds it (a broadcast within rows of 16 lanes).
+template <int I, int N>
+__device__ __forceinline__ uint32_t scale_word(const uint32_t (&d)[N]) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)d[I / 16], 0x150 + I % 16, 0xF, 0xF, true);
+}
+// fn(integral constant I, word I) for every word.
+template <int I, int END, class Fn, int N>
+__device__ __forceinline__ void each_scale(const uint32_t (&d)[N], Fn&& fn) {
+  if constexpr (I < END) {
+    fn(I, scale_word<I>(d));
+    each_scale<I + 1, END>(d, fn);
+  }
 }
 
 // One block: a chunk of one sequence's positions, up to 16 query heads of one
@@ -137,14 +162,29 @@ template <int KIND, int NB, bool TRACK>
 __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArgs a) {
   constexpr int DIM = NB * 32;
   constexpr int NT = 2 * NB;   // 16-dim tiles of the output
+  // operand parts: fp16 pairs for Q K^T of the F16 and Q8_0 caches and for P V of
+  // F16; bf16 triples otherwise (a weight times a Q8_0 scale has any magnitude)
+  constexpr int QK = KIND == kKvBF16 ? kKvBF16 : kKvF16;
+  using Q = Parts<QK>;
   using P = Parts<KIND>;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, g = lane >> 4;
-  const int split = blockIdx.x, s = blockIdx.z;
-  const int h = blockIdx.y / a.head_tiles, ht = blockIdx.y % a.head_tiles;
-  const int n = (int)kv_length(a.lengths[s], a.max_len, a.table_stride, a.c.shift);
+  // Heads run fastest, splits slowest: consecutive blocks go to the eight XCDs
+  // in turn, and with the splits fastest the empty ones behind the sequences'
+  // ends would leave the same XCDs idle (8 splits, half of them empty: 315
+  // instead of 190 us for 1 GB).
+  const int split = blockIdx.z, s = blockIdx.y;
+  const int h = blockIdx.x / a.head_tiles, ht = blockIdx.x % a.head_tiles;
+  // The chunk's page ids, one per lane (a chunk spans at most 64 pages). Without
+  // a window they are asked for beside the length, not behind it.
+  const int32_t length = a.lengths[s];
+  int32_t pid = 0;
+  if (a.window == 0 && lane < a.chunk_pages)
+    pid = kv_page(a.table + (int64_t)s * a.table_stride, ((int64_t)split * a.chunk >> a.c.shift) + lane, a.table_stride,
+                  a.c.n_pages);
+  const int n = (int)kv_length(length, a.max_len, a.table_stride, a.c.shift);
   const int first = attn_first(n, a.window);
-  const int begin = (first & ~(kAttnTile - 1)) + split * a.chunk;   // < 2^31: max_len <= 2^30
+  const int begin = (first & ~(kAttnTile - 1)) + split * a.chunk;   // < 2^31: max_len <= 2^25
   const int heads = a.group - ht * 16 < 16 ? a.group - ht * 16 : 16;   // valid columns
   const int head0 = h * a.group + ht * 16;
   if (begin >= n) {
@@ -158,16 +198,12 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
   }
   const int end = n - begin < a.chunk ? n : begin + a.chunk;
 
-  // the chunk's page ids, one per lane (a chunk spans at most 64 pages)
   const int page0 = begin >> a.c.shift;
-  const int last_page = (end - 1) >> a.c.shift;
-  int32_t pid = 0;
-  bool bad = false;
-  if (page0 + lane <= last_page) {
+  const bool paged = page0 + lane <= (end - 1) >> a.c.shift;
+  if (a.window > 0 && paged)
     pid = kv_page(a.table + (int64_t)s * a.table_stride, page0 + lane, a.table_stride, a.c.n_pages);
-    bad = pid < 0;
-  }
-  const bool any_bad = __any(bad);
+  if (!paged) pid = 0;   // behind the sequence's last page: whatever the entry, not followed
+  const bool any_bad = __any(pid < 0);
 
   const int k_row = 8 * (col >> 2) + (col & 3);   // + 4 t: the position in the tile of this lane's K row
   const uint8_t* const kh = a.c.k + (int64_t)h * a.c.head_bytes;
@@ -179,12 +215,10 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
     const int id = __builtin_amdgcn_readlane(pid, local);
     return id < 0 ? 0 : id;
   };
-  AttnK<KIND, NB> K;
-  AttnV<KIND, NB> V;
   // A tile lies in one page, or in two of 16 positions; the second half of a
   // last tile may have no page: lanes past the table hold page 0, whose values
   // are then masked.
-  auto load_k = [&](int t0) {
+  auto load_k = [&](AttnK<KIND, NB>& K, int t0) {
     const int local = (t0 >> a.c.shift) - page0;
     int64_t base = page_at(local) * page_bytes;
     if (a.c.ps == 16 && k_row >= 16) base = page_at((local + 1) & 63) * page_bytes;
@@ -203,10 +237,13 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
       if (a.c.ps == 16 && g >= 2) dbase = page_at((local + 1) & 63) * page_bytes;
       const uint8_t* dp = kh + dbase + a.c.ps * DIM + ((t0 + 8 * g) & smask) * (NB * 2);
 #pragma unroll
-      for (int b = 0; b < NB; ++b) K.d[b] = load16(dp + 16 * b);
+      for (int j = 0; j < (4 * NB + 15) / 16; ++j) {
+        const int w = col + 16 * j;
+        K.d[j] = load4(dp + 4 * (w < 4 * NB ? w : 0));
+      }
     }
   };
-  auto load_v = [&](int t0) {
+  auto load_v = [&](AttnV<KIND, NB>& V, int t0) {
     const int local = (t0 >> a.c.shift) - page0;
     int64_t base = page_at(local) * page_bytes;
     if (a.c.ps == 16 && g >= 2) base = page_at((local + 1) & 63) * page_bytes;
@@ -219,7 +256,10 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
     }
     if constexpr (KIND == kKvQ80) {
 #pragma unroll
-      for (int b = 0; b < NB; ++b) V.d[b] = load16(p + a.c.ps * DIM + (b * a.c.ps + slot) * 2);
+      for (int j = 0; j < (4 * NB + 15) / 16; ++j) {
+        const int w = col + 16 * j < 4 * NB ? col + 16 * j : 0;
+        V.d[j] = load4(p + a.c.ps * DIM + ((w >> 2) * a.c.ps + slot) * 2 + (w & 3) * 4);
+      }
     }
   };
 
@@ -231,14 +271,21 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
   int t_lo = mine, t_hi = end & ~(kAttnTile - 1);
   if (t_lo < first) t_lo += step;
   if (any_bad) t_hi = t_lo;
-  if (t_lo < t_hi) {
-    load_k(t_lo);
-    load_v(t_lo);
+  // Q8_0 has half the bytes per tile: two tiles ahead instead of one.
+  constexpr int kSets = KIND == kKvQ80 && NB <= 4 ? 2 : 1;
+  AttnK<KIND, NB> K[kSets];
+  AttnV<KIND, NB> V[kSets];
+#pragma unroll
+  for (int i = 0; i < kSets; ++i) {
+    if (t_lo + i * step < t_hi) {
+      load_k(K[i], t_lo + i * step);
+      load_v(V[i], t_lo + i * step);
+    }
   }
 
   // q of this lane's head: the B operand, dims 32 b + 8 g .. + 7
-  P q[NB];
-  float sfac = 1.0f;   // undoes the row's power-of-two scale (F16)
+  Q q[NB];
+  float sfac = 1.0f;   // undoes the row's power-of-two scale (fp16 parts)
   {
     float x[NB][8];
     const bool live = col < heads;
@@ -255,7 +302,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
         amax = fmaxf(amax, fabsf(x[b][j]));
       }
     }
-    if constexpr (KIND == kKvF16) {
+    if constexpr (QK == kKvF16) {
       // the row's largest magnitude to [512, 1024): both fp16 parts of every
       // value that matters are normal numbers
       amax = fmaxf(amax, __shfl_xor(amax, 16));
@@ -283,27 +330,35 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
   float m = -__builtin_inff(), l = 0.f;   // of this lane's head; l over this lane's positions
 
   // Scores of positions t0 + 8 g + j of this lane's head, from the K loaded.
-  auto scores = [&](float (&sc)[8]) {
+  auto scores = [&](const AttnK<KIND, NB>& K, float (&sc)[8]) {
+    if constexpr (KIND == kKvQ80) {
+      f32x4 r[2][NB];   // per 32-dim block, before its scale
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      f32x4 acc = zero;
-      if constexpr (KIND == kKvQ80) {
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          const uint4 kc = codes_bf16(K.c[t][b]);
-          f32x4 r = zero;
+          const uint4 kc = codes_f16(K.c[t][b]);
+          r[t][b] = zero;
 #pragma unroll
-          for (int i = P::kN - 1; i >= 0; --i) r = attn_mfma<KIND>(kc, q[b].p[i], r);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[i] = fmaf(r[i], half_of(K.d, (4 * t + i) * NB + b), acc[i]);
+          for (int i = Q::kN - 1; i >= 0; --i) r[t][b] = attn_mfma<QK>(kc, q[b].p[i], r[t][b]);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sc[4 * t + i] = acc[i];
-      } else {
+      for (int j = 0; j < 8; ++j) sc[j] = 0.f;
+      each_scale<0, 4 * NB>(K.d, [&](int w, uint32_t d) {
+        const int j0 = 2 * w / NB, b0 = 2 * w % NB, j1 = (2 * w + 1) / NB, b1 = (2 * w + 1) % NB;
+        sc[j0] = fmaf(r[j0 >> 2][b0][j0 & 3], half_lo(d), sc[j0]);
+        sc[j1] = fmaf(r[j1 >> 2][b1][j1 & 3], half_hi(d), sc[j1]);
+      });
 #pragma unroll
-        for (int i = P::kN - 1; i >= 0; --i)
+      for (int j = 0; j < 8; ++j) sc[j] *= sfac;
+    } else {
 #pragma unroll
-          for (int b = 0; b < NB; ++b) acc = attn_mfma<KIND>(K.x[t][b], q[b].p[i], acc);
+      for (int t = 0; t < 2; ++t) {
+        f32x4 acc = zero;
+#pragma unroll
+        for (int i = Q::kN - 1; i >= 0; --i)
+#pragma unroll
+          for (int b = 0; b < NB; ++b) acc = attn_mfma<QK>(K.x[t][b], q[b].p[i], acc);
 #pragma unroll
         for (int i = 0; i < 4; ++i) sc[4 * t + i] = acc[i] * sfac;
       }
@@ -342,20 +397,22 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
   // O^T += V^T P^T, from the V given.
   auto accumulate = [&](const AttnV<KIND, NB>& v, float (&p)[8]) {
     if constexpr (KIND == kKvQ80) {
+      float pd[8];
+      each_scale<0, 4 * NB>(v.d, [&](int w, uint32_t d) {
+        const int j = 2 * (w % 4);
+        pd[j] = p[j] * half_lo(d);
+        pd[j + 1] = p[j + 1] * half_hi(d);
+        if (w % 4 == 3) {   // a block's eight weights
+          P pp;
+          pp.set(pd);
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        float pd[8];
+          for (int t = 2 * (w / 4); t < 2 * (w / 4) + 2; ++t) {
+            const uint4 vc = codes_bf16(v.c[t]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) pd[j] = p[j] * half_of(v.d, 8 * b + j);
-        P pp;
-        pp.set(pd);
-#pragma unroll
-        for (int t = 2 * b; t < 2 * b + 2; ++t) {
-          const uint4 vc = codes_bf16(v.c[t]);
-#pragma unroll
-          for (int i = P::kN - 1; i >= 0; --i) o[t] = attn_mfma<KIND>(vc, pp.p[i], o[t]);
+            for (int i = P::kN - 1; i >= 0; --i) o[t] = attn_mfma<KIND>(vc, pp.p[i], o[t]);
+          }
         }
-      }
+      });
     } else {
       if constexpr (KIND == kKvF16) {
 #pragma unroll
@@ -370,20 +427,27 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
     }
   };
 
-  for (int t0 = t_lo; t0 < t_hi; t0 += step) {
+  auto full_tile = [&](AttnK<KIND, NB>& K, AttnV<KIND, NB>& V, int t0) {
     float sc[8], p[8];
-    scores(sc);
-    const bool more = t0 + step < t_hi;   // uniform over the wave
-    if (more) load_k(t0 + step);
+    scores(K, sc);
+    const int next = t0 + kSets * step;   // uniform over the wave
+    if (next < t_hi) load_k(K, next);
     keep_scores(t0, sc);
     softmax(sc, p);
     accumulate(V, p);
-    if (more) load_v(t0 + step);
+    if (next < t_hi) load_v(V, next);
+  };
+  for (int t0 = t_lo; t0 < t_hi; t0 += kSets * step) {
+    full_tile(K[0], V[0], t0);
+    if constexpr (kSets == 2)
+      if (t0 + step < t_hi) full_tile(K[1], V[1], t0 + step);
   }
   for (int t0 = mine; t0 < end; t0 += step) {
     if (t0 >= t_lo && t0 < t_hi) continue;
-    load_k(t0);
-    load_v(t0);
+    AttnK<KIND, NB> ek;
+    AttnV<KIND, NB> ev;
+    load_k(ek, t0);
+    load_v(ev, t0);
     const int p0 = t0 + 8 * g;
     int hi = end - p0, lo = first - p0;
     hi = hi < 0 ? 0 : hi > 8 ? 8 : hi;
@@ -391,7 +455,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
     uint32_t live = ((1u << hi) - 1u) & ~((1u << lo) - 1u);   // of the lane's eight positions
     if (any_bad && __shfl(pid, ((p0 >> a.c.shift) - page0) & 63) < 0) live = 0u;
     float sc[8], p[8];
-    scores(sc);
+    scores(ek, sc);
 #pragma unroll
     for (int j = 0; j < 8; ++j) sc[j] = (live >> j & 1) ? sc[j] : -__builtin_inff();
     keep_scores(t0, sc);
@@ -402,15 +466,15 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
     const uint32_t w1 = ((live & 4) ? 0xFFFFu : 0u) | ((live & 8) ? 0xFFFF0000u : 0u);
     const uint32_t w2 = ((live & 16) ? 0xFFFFu : 0u) | ((live & 32) ? 0xFFFF0000u : 0u);
     const uint32_t w3 = ((live & 64) ? 0xFFFFu : 0u) | ((live & 128) ? 0xFFFF0000u : 0u);
-    AttnV<KIND, NB> mv = V;
+    AttnV<KIND, NB> mv = ev;
     if constexpr (KIND == kKvQ80) {
+      const uint32_t wd = (col & 3) == 0 ? w0 : (col & 3) == 1 ? w1 : (col & 3) == 2 ? w2 : w3;
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
-        mv.d[b] = make_uint4(V.d[b].x & w0, V.d[b].y & w1, V.d[b].z & w2, V.d[b].w & w3);
+      for (int j = 0; j < (4 * NB + 15) / 16; ++j) mv.d[j] = ev.d[j] & wd;
     } else {
 #pragma unroll
       for (int t = 0; t < NT; ++t)
-        mv.x[t] = make_uint4(V.x[t].x & w0, V.x[t].y & w1, V.x[t].z & w2, V.x[t].w & w3);
+        mv.x[t] = make_uint4(ev.x[t].x & w0, ev.x[t].y & w1, ev.x[t].z & w2, ev.x[t].w & w3);
     }
     accumulate(mv, p);
   }

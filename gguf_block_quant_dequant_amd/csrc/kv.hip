@@ -216,9 +216,12 @@ int gguf_kv_evict(const gguf_kv_cache* cache, int64_t n_seqs, const int32_t* pag
     st = abi_launched();
     if (st) return st;
   }
-  const int64_t tiles = p.moves > 0 ? (p.moves + kMoveTile - 1) / kMoveTile : 1;
+  // heads fastest, tiles slowest: tiles past a sequence's moves are empty, and
+  // consecutive blocks go to different XCDs
+  int64_t tiles = p.moves > 0 ? (p.moves + kMoveTile - 1) / kMoveTile : 1;
+  if (tiles > 1024) tiles = 1024;   // blocks step over the rest
   by_cache(kind_of(cache->type), a.c.dim,
-           LaunchMove{a, dim3((unsigned)tiles, p.moves > 0 ? (unsigned)a.c.hkv : 1u, (unsigned)n_seqs), stream});
+           LaunchMove{a, dim3(p.moves > 0 ? (unsigned)a.c.hkv : 1u, (unsigned)n_seqs, (unsigned)tiles), stream});
   return abi_launched();
 }
 

@@ -559,7 +559,7 @@ __global__ __launch_bounds__(kEvictThreads) void kv_evict_select_kernel(const Ev
 constexpr int kMoveTile = 64;
 constexpr int kMoveThreads = 256;
 
-// One block: up to 64 moves of one kv head of one sequence. Sources lie at or
+// Blocks of one kv head of one sequence, 64 moves at a time. Sources lie at or
 // behind the budget and destinations before it, so no block reads what another
 // writes. K rows move as 16-byte (Q8_0: 8-byte) pieces; V moves lane per
 // move, row of a dim by row, so that the ascending slots of a wave share lines.
@@ -568,14 +568,14 @@ template <int KIND, int DIM>
 __global__ __launch_bounds__(kMoveThreads) void kv_evict_move_kernel(const EvictArgs a) {
   __shared__ int64_t sp[kMoveTile], dp[kMoveTile];   // byte offset of page and head
   __shared__ int32_t ss[kMoveTile], ds[kMoveTile];   // slot within the page; ss -1: no move
-  const int h = blockIdx.y, s = blockIdx.z, tid = threadIdx.x, lane = tid & 63;
-  if (blockIdx.x == 0 && h == 0 && tid == 0 && (int64_t)a.lengths[s] > a.budget) a.lengths[s] = (int32_t)a.budget;
+  const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
+  if (blockIdx.z == 0 && h == 0 && tid == 0 && (int64_t)a.lengths[s] > a.budget) a.lengths[s] = (int32_t)a.budget;
   if (a.max_moves == 0) return;
   const int64_t pair = (int64_t)s * a.c.hkv + h;
   const int count = a.count[pair];
-  const int j0 = blockIdx.x * kMoveTile;
-  if (j0 >= count) return;
   const int32_t* row = a.table + (int64_t)s * a.table_stride;
+  for (int64_t j0 = (int64_t)blockIdx.z * kMoveTile; j0 < count; j0 += (int64_t)gridDim.z * kMoveTile) {
+  __syncthreads();   // the last tile's moves are read
   if (tid < kMoveTile) {
     ss[tid] = -1;
     if (j0 + tid < count) {
@@ -595,7 +595,7 @@ __global__ __launch_bounds__(kMoveThreads) void kv_evict_move_kernel(const Evict
     }
   }
   __syncthreads();
-  const int rows = count - j0 < kMoveTile ? count - j0 : kMoveTile;
+  const int rows = count - j0 < kMoveTile ? (int)(count - j0) : kMoveTile;
   constexpr int kOct = DIM / 8;
   for (int i = tid; i < rows * kOct; i += kMoveThreads) {
     const int r = i / kOct, o = i % kOct;
@@ -652,6 +652,7 @@ __global__ __launch_bounds__(kMoveThreads) void kv_evict_move_kernel(const Evict
       reinterpret_cast<uint16_t*>(a.c.v + dp[r] + a.c.ps * DIM)[b * a.c.ps + ds[r]] =
           reinterpret_cast<const uint16_t*>(a.c.v + sp[r] + a.c.ps * DIM)[b * a.c.ps + ss[r]];
     }
+  }
   }
 }
 

@@ -105,7 +105,7 @@ int gguf_kv_append(const gguf_kv_cache* cache, const void* k, const void* v, int
  * behind a sequence's length is not looked at, whatever it holds; keys and
  * values within the length have to be finite.
  *
- * max_len (<= 2^30) is a bound on the lengths that the host knows (it sets the
+ * max_len (<= 2^25) is a bound on the lengths that the host knows (it sets the
  * grid and the workspace); longer sequences are cut at it, as at the table's
  * row. With
  * track, weight[slot] of the cache grows by p_i summed over the query heads of
@@ -134,8 +134,8 @@ int gguf_attn_decode(const gguf_kv_cache* cache, const float* q, int64_t q_strid
  * and pos), so a call moves no more than it has to, and lengths[s] becomes
  * budget. The slots from budget on are left as they were and their pages are
  * free. Sequences of at most budget slots are left alone.
- * max_len bounds the lengths as for the attention (slots behind it are not
- * looked at). budget >= 1, 0 <= recent <= budget; cache->weight is needed; a page
+ * max_len (<= 2^30) bounds the lengths as for the attention (slots behind it are
+ * not looked at). budget >= 1, 0 <= recent <= budget; cache->weight is needed; a page
  * belongs to one sequence. */
 int64_t gguf_kv_evict_workspace(const gguf_kv_cache* cache, int64_t n_seqs, int64_t max_len,
                                 int64_t budget);
