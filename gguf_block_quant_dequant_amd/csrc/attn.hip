@@ -6,7 +6,15 @@
 namespace gqk {
 
 constexpr int64_t kAttnMaxLen = int64_t(1) << 25;   // splits of at least 1024 positions lie along a grid axis of 65535
-constexpr int64_t kAttnBlocks = 1024;               // blocks a call aims for
+// Blocks a call aims for, and the longest chunk of positions. Long chunks spare
+// prologues, short ones even out sequences of different lengths. A Q8_0 block's
+// prologue weighs more (its steps read half the bytes): 512 blocks and 2048
+// positions took 65 us against 70 with 1024 (8 sequences of 20001 .. 32768);
+// 16-bit types 221 us with 1024 positions against 226 with 2048 (32 sequences of
+// 1 .. 16384) and 68 us with 2048 blocks against 72 with 1024 (64 of 0 .. 4096);
+// at head dim 256 half the blocks (210 us against 239 for 1 GB).
+constexpr int64_t kAttnBlocks = 2048, kAttnBlocksQ80 = 512;
+constexpr int64_t kAttnChunk = 1024, kAttnChunkQ80 = 2048;
 
 // How a call is cut and what its workspace holds.
 struct AttnPlan {
@@ -24,13 +32,15 @@ static int attn_plan(const KvView& c, int64_t n_seqs, int64_t n_heads, int64_t m
   // positions a sequence can cover, from a tile's start
   p->span = window > 0 && window < max_len - (kAttnTile - 1) ? window + kAttnTile - 1 : max_len;
   if (p->span < 1) p->span = 1;
-  // Chunks of whole rounds of a block's waves; at least one round, at most 64
-  // pages (their ids lie one per lane) and 2048 positions.
+  // Chunks of whole tiles; at least 256 positions, at most 64
+  // pages (their ids lie one per lane).
   const int64_t round = kAttnTile * kAttnWaves;
+  const bool q8 = c.head_bytes != kv_head_bytes(false, c.dim, c.ps);
   int64_t most = int64_t(64) << c.shift;
-  if (most > 2048) most = 2048;
+  if (most > (q8 ? kAttnChunkQ80 : kAttnChunk)) most = q8 ? kAttnChunkQ80 : kAttnChunk;
   const int64_t cells = n_seqs * c.hkv * p->head_tiles;
-  int64_t want = cells > 0 ? kAttnBlocks / cells : 1;   // splits
+  const int64_t blocks = q8 ? kAttnBlocksQ80 : c.dim > 128 ? kAttnBlocks / 2 : kAttnBlocks;
+  int64_t want = cells > 0 ? blocks / cells : 1;   // splits
   if (want < 1) want = 1;
   int64_t chunk = ((p->span + want - 1) / want + round - 1) / round * round;
   if (chunk < 2 * round) chunk = 2 * round;

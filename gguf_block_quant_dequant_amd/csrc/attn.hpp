@@ -3,7 +3,7 @@
 // the cache's positions split over blocks and joined.
 //
 // A wave takes 32 positions at a time and up to 16 query heads of one kv head:
-//   S^T = K Q^T   two 16 x 16 tiles, A = K (rows: positions), B = Q (columns: heads)
+//   S^T = K Q^T   16 x 16 tiles, A = K (rows: positions), B = Q (columns: heads)
 //   O^T += V^T P^T   A = V^T (rows: dims), B = P^T (columns: heads)
 // Transposed products leave a lane with one head (its column) throughout: the
 // running maximum, sum and rescale are per-lane values, and the lane's eight
@@ -11,13 +11,19 @@
 // that feeds row r of tile t is position 8 (r / 4) + 4 t + r % 4 (a lane of
 // group g = lane / 16 then holds positions 8 g .. 8 g + 7). V is stored
 // transposed, so those eight positions of a dim are one aligned load. Nothing
-// goes through LDS but the join of a block's waves.
+// goes through LDS but the join of a block's waves. The waves of a block take
+// tiles in turn: two (Q8_0: four) of them then ask for a cache line of V at the
+// same time (with ranges of their own instead they fetched it twice: 345 against
+// 298 us for 1.1 GB; 64 positions per step of a Q8_0 cache took 256 registers
+// and 85 against 70 us).
 //
 // The kernel reads each cache byte once: the bound is HBM. The matrix cores
 // run at a fraction of their rate (16 columns for n_heads / n_kv_heads heads,
 // times two or three parts of the fp32 operand), which costs nothing here and
 // keeps fp32 accuracy.
 #pragma once
+
+#include <type_traits>
 
 #include "device_common.hpp"
 #include "kv_cache.hpp"
@@ -38,7 +44,8 @@ struct AttnArgs {
   float qscale;     // scale * log2(e)
 };
 
-constexpr int kAttnTile = 32;    // positions per step of a wave
+constexpr int kAttnJ = 8;                 // positions of a lane
+constexpr int kAttnTile = 4 * kAttnJ;     // and of a wave's step
 constexpr int kAttnWaves = 4;
 constexpr int kAttnThreads = kAttnWaves * 64;
 constexpr float kPScaleF16 = 16384.0f;   // softmax weights enter fp16 times 2^14: 2^-24 of the largest is normal
@@ -47,7 +54,7 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8v __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-// First position a sequence's attention covers, rounded down to a tile.
+// First position a sequence's attention covers.
 __device__ __forceinline__ int attn_first(int n, int64_t window) {
   return window > 0 && (int64_t)n > window ? (int)(n - window) : 0;
 }
@@ -119,10 +126,10 @@ __device__ __forceinline__ uint4 codes_f16(const uint2& q) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// A wave's 32 positions of K or V as loaded.
-// Q8_0: the 4 NB words of scales of a lane's eight positions (pairs of halves; K
-// [position][block], V [block][position]) are the same for the 16 lanes of its
-// group: lane c of the 16 holds words c and c + 16.
+// A wave's tile of K or V as loaded. Q8_0: the scales of a lane's eight positions
+// (4 NB words, pairs of halves; K [position][block], V [block][position]) are
+// the same for the 16 lanes of its group: lane c of the 16 holds words c and c +
+// 16 (all of them in every lane took 30 registers more).
 template <int KIND, int NB>
 struct AttnK {
   uint4 x[2][KIND == kKvQ80 ? 1 : NB];
@@ -147,7 +154,7 @@ template <int I, int N>
 __device__ __forceinline__ uint32_t scale_word(const uint32_t (&d)[N]) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)d[I / 16], 0x150 + I % 16, 0xF, 0xF, true);
 }
-// fn(integral constant I, word I) for every word.
+// fn(I, word I) for words I .. END - 1.
 template <int I, int END, class Fn, int N>
 __device__ __forceinline__ void each_scale(const uint32_t (&d)[N], Fn&& fn) {
   if constexpr (I < END) {
@@ -157,11 +164,12 @@ __device__ __forceinline__ void each_scale(const uint32_t (&d)[N], Fn&& fn) {
 }
 
 // One block: a chunk of one sequence's positions, up to 16 query heads of one
-// kv head; its waves take the chunk's 32-position tiles in turn and join in LDS.
+// kv head; its waves take the chunk's tiles in turn and join in LDS.
 template <int KIND, int NB, bool TRACK>
 __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArgs a) {
   constexpr int DIM = NB * 32;
   constexpr int NT = 2 * NB;   // 16-dim tiles of the output
+  constexpr int J = kAttnJ, TILE = kAttnTile, WORDS = 4 * NB, NW = (WORDS + 15) / 16;
   // operand parts: fp16 pairs for Q K^T of the F16 and Q8_0 caches and for P V of
   // F16; bf16 triples otherwise (a weight times a Q8_0 scale has any magnitude)
   constexpr int QK = KIND == kKvBF16 ? kKvBF16 : kKvF16;
@@ -205,26 +213,25 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
   if (!paged) pid = 0;   // behind the sequence's last page: whatever the entry, not followed
   const bool any_bad = __any(pid < 0);
 
-  const int k_row = 8 * (col >> 2) + (col & 3);   // + 4 t: the position in the tile of this lane's K row
+  const int k_row = J * (col >> 2) + (col & 3);   // + 4 t: the position in the tile of this lane's K row
   const uint8_t* const kh = a.c.k + (int64_t)h * a.c.head_bytes;
   const uint8_t* const vh = a.c.v + (int64_t)h * a.c.head_bytes;
   const int64_t page_bytes = (int64_t)a.c.hkv * a.c.head_bytes;
   const int smask = a.c.ps - 1;
 
-  auto page_at = [&](int local) -> int64_t {   // page id of the chunk's page `local` (uniform), 0 for a bad one
-    const int id = __builtin_amdgcn_readlane(pid, local);
-    return id < 0 ? 0 : id;
-  };
-  // A tile lies in one page, or in two of 16 positions; the second half of a
-  // last tile may have no page: lanes past the table hold page 0, whose values
-  // are then masked.
-  auto load_k = [&](AttnK<KIND, NB>& K, int t0) {
+  // Byte offset of the page of position `at` of tile t0 (page 0 for a bad one
+  // and behind the sequence, whose values are then masked): the tile's one page,
+  // or one per lane where pages are smaller than the tile.
+  auto page_base = [&](int t0, int at) -> int64_t {
     const int local = (t0 >> a.c.shift) - page0;
-    int64_t base = page_at(local) * page_bytes;
-    if (a.c.ps == 16 && k_row >= 16) base = page_at((local + 1) & 63) * page_bytes;
-    const uint8_t* p = kh + base;
+    int id = __builtin_amdgcn_readlane(pid, local);
+    if (a.c.ps < TILE) id = __shfl(pid, (((t0 + at) >> a.c.shift) - page0) & 63);
+    return (id < 0 ? 0 : id) * page_bytes;
+  };
+  auto load_k = [&](AttnK<KIND, NB>& K, int t0) {
+    const uint8_t* p = kh + page_base(t0, k_row);
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < J / 4; ++t) {
       const int slot = (t0 + k_row + 4 * t) & smask;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
@@ -233,31 +240,25 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
       }
     }
     if constexpr (KIND == kKvQ80) {
-      int64_t dbase = page_at(local) * page_bytes;
-      if (a.c.ps == 16 && g >= 2) dbase = page_at((local + 1) & 63) * page_bytes;
-      const uint8_t* dp = kh + dbase + a.c.ps * DIM + ((t0 + 8 * g) & smask) * (NB * 2);
+      const uint8_t* dp = kh + page_base(t0, J * g) + a.c.ps * DIM + ((t0 + J * g) & smask) * (NB * 2);
 #pragma unroll
-      for (int j = 0; j < (4 * NB + 15) / 16; ++j) {
+      for (int j = 0; j < NW; ++j) {
         const int w = col + 16 * j;
-        K.d[j] = load4(dp + 4 * (w < 4 * NB ? w : 0));
+        K.d[j] = load4(dp + 4 * (w < WORDS ? w : 0));
       }
     }
   };
   auto load_v = [&](AttnV<KIND, NB>& V, int t0) {
-    const int local = (t0 >> a.c.shift) - page0;
-    int64_t base = page_at(local) * page_bytes;
-    if (a.c.ps == 16 && g >= 2) base = page_at((local + 1) & 63) * page_bytes;
-    const uint8_t* p = vh + base;
-    const int slot = (t0 + 8 * g) & smask;
+    const uint8_t* p = vh + page_base(t0, J * g);
+    const int slot = (t0 + J * g) & smask;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
+    for (int t = 0; t < NT; ++t)
       if constexpr (KIND == kKvQ80) V.c[t] = load8(p + (t * 16 + col) * a.c.ps + slot);
       else V.x[t] = load16(p + ((t * 16 + col) * a.c.ps + slot) * 2);
-    }
     if constexpr (KIND == kKvQ80) {
 #pragma unroll
-      for (int j = 0; j < (4 * NB + 15) / 16; ++j) {
-        const int w = col + 16 * j < 4 * NB ? col + 16 * j : 0;
+      for (int j = 0; j < NW; ++j) {
+        const int w = col + 16 * j < WORDS ? col + 16 * j : 0;
         V.d[j] = load4(p + a.c.ps * DIM + ((w >> 2) * a.c.ps + slot) * 2 + (w & 3) * 4);
       }
     }
@@ -266,21 +267,16 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
   // Tiles of positions that all count, [t_lo, t_hi), run through a loop that
   // holds the next tile's loads in flight; the others (the window's first, the
   // last, and every one of a chunk with a bad page) behind it, masked.
-  const int step = kAttnTile * kAttnWaves;
-  const int mine = begin + wave * kAttnTile;
-  int t_lo = mine, t_hi = end & ~(kAttnTile - 1);
+  constexpr int step = TILE * kAttnWaves;
+  const int mine = begin + wave * TILE;
+  int t_lo = mine, t_hi = end & ~(TILE - 1);
   if (t_lo < first) t_lo += step;
   if (any_bad) t_hi = t_lo;
-  // Q8_0 has half the bytes per tile: two tiles ahead instead of one.
-  constexpr int kSets = KIND == kKvQ80 && NB <= 4 ? 2 : 1;
-  AttnK<KIND, NB> K[kSets];
-  AttnV<KIND, NB> V[kSets];
-#pragma unroll
-  for (int i = 0; i < kSets; ++i) {
-    if (t_lo + i * step < t_hi) {
-      load_k(K[i], t_lo + i * step);
-      load_v(V[i], t_lo + i * step);
-    }
+  AttnK<KIND, NB> K;
+  AttnV<KIND, NB> V;
+  if (t_lo < t_hi) {
+    load_k(K, t_lo);
+    load_v(V, t_lo);
   }
 
   // q of this lane's head: the B operand, dims 32 b + 8 g .. + 7
@@ -329,31 +325,34 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
   for (int t = 0; t < NT; ++t) o[t] = zero;
   float m = -__builtin_inff(), l = 0.f;   // of this lane's head; l over this lane's positions
 
-  // Scores of positions t0 + 8 g + j of this lane's head, from the K loaded.
-  auto scores = [&](const AttnK<KIND, NB>& K, float (&sc)[8]) {
+  // Scores of positions t0 + J g + j of this lane's head, from the K loaded.
+  auto scores = [&](const AttnK<KIND, NB>& K, float (&sc)[J]) {
     if constexpr (KIND == kKvQ80) {
-      f32x4 r[2][NB];   // per 32-dim block, before its scale
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
+      auto tile = [&](auto tt) {
+        constexpr int t = decltype(tt)::value;
+        f32x4 r[NB];   // per 32-dim block, before its scale
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           const uint4 kc = codes_f16(K.c[t][b]);
-          r[t][b] = zero;
+          r[b] = zero;
 #pragma unroll
-          for (int i = Q::kN - 1; i >= 0; --i) r[t][b] = attn_mfma<QK>(kc, q[b].p[i], r[t][b]);
+          for (int i = Q::kN - 1; i >= 0; --i) r[b] = attn_mfma<QK>(kc, q[b].p[i], r[b]);
         }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sc[j] = 0.f;
-      each_scale<0, 4 * NB>(K.d, [&](int w, uint32_t d) {
-        const int j0 = 2 * w / NB, b0 = 2 * w % NB, j1 = (2 * w + 1) / NB, b1 = (2 * w + 1) % NB;
-        sc[j0] = fmaf(r[j0 >> 2][b0][j0 & 3], half_lo(d), sc[j0]);
-        sc[j1] = fmaf(r[j1 >> 2][b1][j1 & 3], half_hi(d), sc[j1]);
-      });
+        for (int i = 0; i < 4; ++i) sc[4 * t + i] = 0.f;
+        each_scale<2 * NB * t, 2 * NB * (t + 1)>(K.d, [&](int w, uint32_t d) {
+          const int j0 = 2 * w / NB, b0 = 2 * w % NB, j1 = (2 * w + 1) / NB, b1 = (2 * w + 1) % NB;
+          sc[j0] = fmaf(r[b0][j0 & 3], half_lo(d), sc[j0]);
+          sc[j1] = fmaf(r[b1][j1 & 3], half_hi(d), sc[j1]);
+        });
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sc[j] *= sfac;
+        for (int i = 0; i < 4; ++i) sc[4 * t + i] *= sfac;
+      };
+      tile(std::integral_constant<int, 0>{});
+      tile(std::integral_constant<int, 1>{});
     } else {
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
+      for (int t = 0; t < J / 4; ++t) {
         f32x4 acc = zero;
 #pragma unroll
         for (int i = Q::kN - 1; i >= 0; --i)
@@ -364,18 +363,21 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
       }
     }
   };
-  auto keep_scores = [&](int t0, const float (&sc)[8]) {
+  auto keep_scores = [&](int t0, const float (&sc)[J]) {
     if constexpr (TRACK) {
       if (col < heads) {
-        float* sp = a.scores + ((int64_t)s * a.n_heads + head0 + col) * a.score_stride + t0 + 8 * g;
-        *reinterpret_cast<float4*>(sp) = make_float4(sc[0], sc[1], sc[2], sc[3]);
-        *reinterpret_cast<float4*>(sp + 4) = make_float4(sc[4], sc[5], sc[6], sc[7]);
+        float* sp = a.scores + ((int64_t)s * a.n_heads + head0 + col) * a.score_stride + t0 + J * g;
+#pragma unroll
+        for (int j = 0; j < J; j += 4)
+          *reinterpret_cast<float4*>(sp + j) = make_float4(sc[j], sc[j + 1], sc[j + 2], sc[j + 3]);
       }
     }
   };
   // Running maximum and sum; p becomes the weights relative to the maximum.
-  auto softmax = [&](const float (&sc)[8], float (&p)[8]) {
-    float mx = fmaxf(fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3])), fmaxf(fmaxf(sc[4], sc[5]), fmaxf(sc[6], sc[7])));
+  auto softmax = [&](const float (&sc)[J], float (&p)[J]) {
+    float mx = sc[0];
+#pragma unroll
+    for (int j = 1; j < J; ++j) mx = fmaxf(mx, sc[j]);
     mx = fmaxf(mx, __shfl_xor(mx, 16));
     mx = fmaxf(mx, __shfl_xor(mx, 32));
     if (__any(mx > m)) {
@@ -389,24 +391,24 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
     }
     const float base = m == -__builtin_inff() ? 0.f : m;   // nothing seen yet
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < J; ++j) {
       p[j] = __builtin_amdgcn_exp2f(sc[j] - base);
       l += p[j];
     }
   };
   // O^T += V^T P^T, from the V given.
-  auto accumulate = [&](const AttnV<KIND, NB>& v, float (&p)[8]) {
+  auto accumulate = [&](const AttnV<KIND, NB>& v, float (&p)[J]) {
     if constexpr (KIND == kKvQ80) {
-      float pd[8];
-      each_scale<0, 4 * NB>(v.d, [&](int w, uint32_t d) {
-        const int j = 2 * (w % 4);
+      float pd[8];   // weights times scales: eight positions of a 32-dim block
+      each_scale<0, WORDS>(v.d, [&](int w, uint32_t d) {
+        const int b = w / 4, j = 2 * (w % 4);
         pd[j] = p[j] * half_lo(d);
         pd[j + 1] = p[j + 1] * half_hi(d);
-        if (w % 4 == 3) {   // a block's eight weights
+        if (w % 4 == 3) {
           P pp;
           pp.set(pd);
 #pragma unroll
-          for (int t = 2 * (w / 4); t < 2 * (w / 4) + 2; ++t) {
+          for (int t = 2 * b; t < 2 * b + 2; ++t) {
             const uint4 vc = codes_bf16(v.c[t]);
 #pragma unroll
             for (int i = P::kN - 1; i >= 0; --i) o[t] = attn_mfma<KIND>(vc, pp.p[i], o[t]);
@@ -416,7 +418,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
     } else {
       if constexpr (KIND == kKvF16) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) p[j] *= kPScaleF16;
+        for (int j = 0; j < J; ++j) p[j] *= kPScaleF16;
       }
       P pp;
       pp.set(p);
@@ -427,20 +429,15 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
     }
   };
 
-  auto full_tile = [&](AttnK<KIND, NB>& K, AttnV<KIND, NB>& V, int t0) {
-    float sc[8], p[8];
+  for (int t0 = t_lo; t0 < t_hi; t0 += step) {
+    float sc[J], p[J];
     scores(K, sc);
-    const int next = t0 + kSets * step;   // uniform over the wave
-    if (next < t_hi) load_k(K, next);
+    const bool more = t0 + step < t_hi;   // uniform over the wave
+    if (more) load_k(K, t0 + step);
     keep_scores(t0, sc);
     softmax(sc, p);
     accumulate(V, p);
-    if (next < t_hi) load_v(V, next);
-  };
-  for (int t0 = t_lo; t0 < t_hi; t0 += kSets * step) {
-    full_tile(K[0], V[0], t0);
-    if constexpr (kSets == 2)
-      if (t0 + step < t_hi) full_tile(K[1], V[1], t0 + step);
+    if (more) load_v(V, t0 + step);
   }
   for (int t0 = mine; t0 < end; t0 += step) {
     if (t0 >= t_lo && t0 < t_hi) continue;
@@ -448,30 +445,28 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
     AttnV<KIND, NB> ev;
     load_k(ek, t0);
     load_v(ev, t0);
-    const int p0 = t0 + 8 * g;
+    const int p0 = t0 + J * g;
     int hi = end - p0, lo = first - p0;
-    hi = hi < 0 ? 0 : hi > 8 ? 8 : hi;
-    lo = lo < 0 ? 0 : lo > 8 ? 8 : lo;
-    uint32_t live = ((1u << hi) - 1u) & ~((1u << lo) - 1u);   // of the lane's eight positions
+    hi = hi < 0 ? 0 : hi > J ? J : hi;
+    lo = lo < 0 ? 0 : lo > J ? J : lo;
+    uint32_t live = ((1u << hi) - 1u) & ~((1u << lo) - 1u);   // of the lane's positions
     if (any_bad && __shfl(pid, ((p0 >> a.c.shift) - page0) & 63) < 0) live = 0u;
-    float sc[8], p[8];
+    float sc[J], p[J];
     scores(ek, sc);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sc[j] = (live >> j & 1) ? sc[j] : -__builtin_inff();
+    for (int j = 0; j < J; ++j) sc[j] = (live >> j & 1) ? sc[j] : -__builtin_inff();
     keep_scores(t0, sc);
     softmax(sc, p);
     // V behind the length may hold anything: masked positions become 0 (Q8_0:
     // their scales; any code is finite)
-    const uint32_t w0 = ((live & 1) ? 0xFFFFu : 0u) | ((live & 2) ? 0xFFFF0000u : 0u);
-    const uint32_t w1 = ((live & 4) ? 0xFFFFu : 0u) | ((live & 8) ? 0xFFFF0000u : 0u);
-    const uint32_t w2 = ((live & 16) ? 0xFFFFu : 0u) | ((live & 32) ? 0xFFFF0000u : 0u);
-    const uint32_t w3 = ((live & 64) ? 0xFFFFu : 0u) | ((live & 128) ? 0xFFFF0000u : 0u);
+    auto pair = [&](int i) { return ((live >> 2 * i & 1) ? 0xFFFFu : 0u) | ((live >> 2 * i & 2) ? 0xFFFF0000u : 0u); };
     AttnV<KIND, NB> mv = ev;
     if constexpr (KIND == kKvQ80) {
-      const uint32_t wd = (col & 3) == 0 ? w0 : (col & 3) == 1 ? w1 : (col & 3) == 2 ? w2 : w3;
+      const uint32_t mask = pair(col & 3);
 #pragma unroll
-      for (int j = 0; j < (4 * NB + 15) / 16; ++j) mv.d[j] = ev.d[j] & wd;
+      for (int j = 0; j < NW; ++j) mv.d[j] = ev.d[j] & mask;
     } else {
+      const uint32_t w0 = pair(0), w1 = pair(1), w2 = pair(2), w3 = pair(3);
 #pragma unroll
       for (int t = 0; t < NT; ++t)
         mv.x[t] = make_uint4(ev.x[t].x & w0, ev.x[t].y & w1, ev.x[t].z & w2, ev.x[t].w & w3);
