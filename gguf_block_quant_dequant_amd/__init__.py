@@ -586,6 +586,10 @@ def gguf_add_f32(a, b, out=None, stream=None):
 
 # ------------------------------------------------- paged key-value cache (include/gguf_kv.h)
 
+_F32 = (torch.float32,)
+_SOURCES = (torch.float32, torch.bfloat16)
+
+
 class KvCacheStruct(ctypes.Structure):
     """struct gguf_kv_cache of the C ABI."""
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("weight", ctypes.c_void_p),
@@ -607,6 +611,7 @@ class KvCache:
         if page < 0:
             raise GgufQkArgumentError(page, "KvCache")
         kp, vp = _dev(k, "k"), _dev(v, "v")
+        self.device = k.get_device()   # index
         nbytes = k.numel() * k.element_size()
         if nbytes == 0 or nbytes % page:
             raise ValueError(f"k holds {nbytes} bytes, not whole pages of {page}")
@@ -616,13 +621,13 @@ class KvCache:
         slots = self.n_pages * n_kv_heads * page_size
         for t, name, dt in ((weight, "weight", torch.float32), (pos, "pos", torch.int32)):
             if t is not None:
-                _dev(t, name, dt)
+                _tensor(t, name, self.device, dt)
                 if t.numel() != slots:
                     raise ValueError(f"{name} holds {t.numel()} values, expected {slots}")
-        _one_device(k, v, weight, pos)
+        if v.get_device() != self.device:
+            raise ValueError("k and v must be on one device")
         self.k, self.v, self.weight, self.pos = k, v, weight, pos
         self.type, self.n_kv_heads, self.head_dim, self.page_size = type, n_kv_heads, head_dim, page_size
-        self.device = k.device
         self.struct = KvCacheStruct(kp, vp, None if weight is None else weight.data_ptr(),
                                     None if pos is None else pos.data_ptr(), self.n_pages, type, n_kv_heads,
                                     head_dim, page_size)
@@ -642,67 +647,78 @@ class KvCache:
         return cls(k, v, type, n_kv_heads, head_dim, page_size, weight=w, pos=p)
 
 
-def _one_device(first, *rest):
-    for t in rest:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on two devices: {first.device} and {t.device}")
+def _tensor(t, name, device, dtype=None):
+    """The address of a contiguous tensor on device `device` (index). These calls
+    run once per decode step: the checks stay few and cheap."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be a tensor on device {device}, got {t.device}")
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t, name, device, row, dtypes):
+    """(address, row stride) of [n, row] or [n, heads, dim] values whose rows may lie apart."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be a tensor on device {device}, got {t.device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be one of {dtypes}, got {t.dtype}")
+    shape = t.shape
+    if len(shape) not in (2, 3) or math.prod(shape[1:]) != row:
+        raise ValueError(f"{name} must be rows of {row} values, got {tuple(shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), row
+    stride = t.stride()
+    if (row > 1 and stride[-1] != 1 and shape[-1] > 1) or (
+            len(shape) == 3 and shape[1] > 1 and stride[1] != shape[2]):
+        raise ValueError(f"{name} must be rows of {row} consecutive values, got strides {stride}")
+    return t.data_ptr(), (stride[0] if shape[0] > 1 else row)
+
+
+def _ints(t, name, device, n):
+    p = _tensor(t, name, device, torch.int32)
+    if t.numel() != n:
+        raise ValueError(f"{name} holds {t.numel()} values, expected {n}")
+    return p
+
+
+def _table(t, device):
+    p = _tensor(t, "page_table", device, torch.int32)
+    if t.dim() != 2 or t.shape[1] < 1:
+        raise ValueError("page_table must be [n_seqs, pages]")
+    return p
 
 
 def _call(device, stream, run):
-    """Runs run(stream handle) with the tensors' device current (the library works
-    on the current device) and, where a stream is given, that stream current for
-    what run allocates."""
-    index = device.index
-    if stream is None and index == torch.cuda.current_device():
-        return run(torch.cuda.current_stream().cuda_stream)
+    """Runs run(stream handle) with the tensors' device (index) current (the library
+    works on the current device) and, where a stream is given, that stream current
+    for what run allocates."""
+    if stream is None and torch._C._cuda_getDevice() == device:
+        return run(torch._C._cuda_getCurrentRawStream(device))
     with contextlib.ExitStack() as on:
         on.enter_context(torch.cuda.device(device))
         if stream is not None:
             if not isinstance(stream, torch.cuda.Stream):
                 stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
             on.enter_context(torch.cuda.stream(stream))
-        return run(torch.cuda.current_stream().cuda_stream)
-
-
-def _rows2d(t, name, row, dtypes):
-    """(pointer, row stride) of [n, row] values whose rows may lie apart."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name} must be one of {dtypes}, got {t.dtype}")
-    if t.dim() == 3 and t.shape[1] * t.shape[2] == row and t.stride(2) == 1 and (
-            t.shape[1] == 1 or t.stride(1) == t.shape[2]):
-        stride = t.stride(0)
-    elif t.dim() == 2 and t.shape[1] == row and (row == 1 or t.stride(1) == 1):
-        stride = t.stride(0)
-    else:
-        raise ValueError(f"{name} must be rows of {row} consecutive values, got {tuple(t.shape)}")
-    return t.data_ptr(), (max(stride, row) if t.shape[0] < 2 else stride)
-
-
-def _table(t):
-    p = _dev(t, "page_table", torch.int32)
-    if t.dim() != 2 or t.shape[1] < 1:
-        raise ValueError("page_table must be [n_seqs, pages]")
-    return p
-
-
-def _ints(t, name, n):
-    p = _dev(t, name, torch.int32)
-    if t.numel() != n:
-        raise ValueError(f"{name} holds {t.numel()} values, expected {n}")
-    return p
+        return run(torch._C._cuda_getCurrentRawStream(device))
 
 
 def _work(workspace, need, device):
-    """A workspace of `need` bytes: the caller's, or one of the call's own."""
-    if need < 0:
-        raise GgufQkArgumentError(need, "workspace")
+    """(tensor, address, bytes) of a workspace: the caller's, or one of the call's
+    own, of the bytes need() says."""
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    return workspace, _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+        n = need()
+        if n < 0:
+            raise GgufQkArgumentError(n, "workspace")
+        workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=torch.device("cuda", device))
+    return workspace, _tensor(workspace, "workspace", device), workspace.numel() * workspace.element_size()
 
 
 def gguf_kv_page_bytes(type_id: int, n_kv_heads: int, head_dim: int, page_size: int) -> int:
@@ -714,22 +730,20 @@ def gguf_kv_append(cache: KvCache, k, v, page_table, slot, seq=None, pos=None, s
     """Write tokens (rows of k and v, fp32 or bf16 [n_tokens, n_kv_heads * head_dim],
     rows may lie apart) to slot[t] of sequence seq[t] (None: t). A token with a
     slot or seq out of range is dropped."""
-    row = cache.n_kv_heads * cache.head_dim
-    dtypes = (torch.float32, torch.bfloat16)
-    (kp, ks), (vp, vs) = _rows2d(k, "k", row, dtypes), _rows2d(v, "v", row, dtypes)
+    row, dev = cache.n_kv_heads * cache.head_dim, cache.device
+    (kp, ks), (vp, vs) = _rows(k, "k", dev, row, _SOURCES), _rows(v, "v", dev, row, _SOURCES)
     n = k.shape[0]
-    if v.shape[0] != n or v.dtype != k.dtype or (n > 1 and ks != vs):
+    if v.shape[0] != n or v.dtype is not k.dtype or ks != vs:
         raise ValueError("k and v must have the same rows, type and row stride")
-    tp, sp = _table(page_table), _ints(slot, "slot", n)
-    qp = None if seq is None else _ints(seq, "seq", n)
-    pp = None if pos is None else _ints(pos, "pos", n)
-    _one_device(cache.k, k, v, page_table, slot, seq, pos)
-    src = TENSOR_F32 if k.dtype == torch.float32 else TENSOR_BF16
+    tp, sp = _table(page_table, dev), _ints(slot, "slot", dev, n)
+    qp = None if seq is None else _ints(seq, "seq", dev, n)
+    pp = None if pos is None else _ints(pos, "pos", dev, n)
+    src = TENSOR_F32 if k.dtype is torch.float32 else TENSOR_BF16
     if n == 0:   # empty tensors have no address
         return
-    _check(_call(cache.device, stream, lambda st: lib().gguf_kv_append(
-        cache.address, kp, vp, src, ks if n > 1 else row, n, qp, sp, pp, tp, page_table.shape[1],
-        page_table.shape[0], st)), "gguf_kv_append")
+    seqs, pages = page_table.shape
+    _check(_call(dev, stream, lambda st: lib().gguf_kv_append(
+        cache.address, kp, vp, src, ks, n, qp, sp, pp, tp, pages, seqs, st)), "gguf_kv_append")
 
 
 def gguf_attn_decode_workspace(cache: KvCache, n_seqs: int, n_heads: int, max_len: int, track: bool = False) -> int:
@@ -746,33 +760,30 @@ def gguf_attn_decode(cache: KvCache, q, page_table, lengths, max_len, scale=None
     by the attention each slot received. `workspace`: a tensor of at least
     gguf_attn_decode_workspace bytes that no overlapping call uses (None: the
     call allocates one)."""
-    d = cache.head_dim
-    n = q.shape[0]
-    row = math.prod(q.shape[1:])
+    d, dev, shape = cache.head_dim, cache.device, q.shape
+    n, row = shape[0], math.prod(shape[1:])
     if row == 0 or row % d:
         raise ValueError("q must be [n_seqs, n_heads, head_dim]")
-    qp, qs = _rows2d(q, "q", row, (torch.float32,))
     heads = row // d
-    tp, lp = _table(page_table), _ints(lengths, "lengths", n)
-    if page_table.shape[0] != n:
+    qp, qs = _rows(q, "q", dev, row, _F32)
+    tp, lp = _table(page_table, dev), _ints(lengths, "lengths", dev, n)
+    seqs, pages = page_table.shape
+    if seqs != n:
         raise ValueError("one row of page_table per sequence")
-    _one_device(cache.k, q, page_table, lengths, out, workspace)
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    max_len = int(max_len)
+    scale = d ** -0.5 if scale is None else scale
 
     def run(st):
-        o = torch.empty(q.shape, dtype=torch.float32, device=q.device) if out is None else out
-        op, os_ = _rows2d(o, "out", row, (torch.float32,))
+        o = torch.empty(shape, dtype=torch.float32, device=q.device) if out is None else out
+        op, os_ = _rows(o, "out", dev, row, _F32)
         if o.shape[0] != n:
             raise ValueError("out must have one row per sequence")
         if n == 0:   # empty tensors have no address
             return o
-        need = 0 if workspace is not None else gguf_attn_decode_workspace(cache, n, heads, max_len, track)
-        ws, wp, wn = _work(workspace, need, cache.device)
-        _check(lib().gguf_attn_decode(cache.address, qp, qs, op, os_, n, heads, tp, page_table.shape[1], lp, max_len,
-                                      scale, int(window), int(track), wp, wn, st), "gguf_attn_decode")
+        ws, wp, wn = _work(workspace, lambda: gguf_attn_decode_workspace(cache, n, heads, max_len, track), dev)
+        _check(lib().gguf_attn_decode(cache.address, qp, qs, op, os_, n, heads, tp, pages, lp, max_len, scale, window,
+                                      1 if track else 0, wp, wn, st), "gguf_attn_decode")
         return o
-    return _call(cache.device, stream, run)
+    return _call(dev, stream, run)
 
 
 def gguf_kv_evict_workspace(cache: KvCache, n_seqs: int, max_len: int, budget: int) -> int:
@@ -784,21 +795,18 @@ def gguf_kv_evict(cache: KvCache, page_table, lengths, max_len, budget, recent=0
     """Cut every sequence longer than `budget` to the `budget` slots per kv head
     that received most attention (the newest `recent` tokens always stay). Moves
     the kept slots behind the budget into the vacated ones and updates lengths."""
-    tp = _table(page_table)
-    n = page_table.shape[0]
-    lp = _ints(lengths, "lengths", n)
-    _one_device(cache.k, page_table, lengths, workspace)
-    max_len, budget = int(max_len), int(budget)
-
+    dev = cache.device
+    tp = _table(page_table, dev)
+    n, pages = page_table.shape
+    lp = _ints(lengths, "lengths", dev, n)
     if n == 0:
         return
 
     def run(st):
-        need = 0 if workspace is not None else gguf_kv_evict_workspace(cache, n, max_len, budget)
-        ws, wp, wn = _work(workspace, need, cache.device)
-        _check(lib().gguf_kv_evict(cache.address, n, tp, page_table.shape[1], lp, max_len, budget, int(recent), wp,
-                                   wn, st), "gguf_kv_evict")
-    _call(cache.device, stream, run)
+        ws, wp, wn = _work(workspace, lambda: gguf_kv_evict_workspace(cache, n, max_len, budget), dev)
+        _check(lib().gguf_kv_evict(cache.address, n, tp, pages, lp, max_len, budget, recent, wp, wn, st),
+               "gguf_kv_evict")
+    _call(dev, stream, run)
 
 
 class Logprobs(NamedTuple):
@@ -823,32 +831,34 @@ def gguf_logprobs(logits, tokens=None, top_k=0, workspace=None, stream=None) -> 
     x = logits.unsqueeze(0) if logits.dim() == 1 else logits
     if x.dim() != 2:
         raise ValueError("logits must be [n_rows, vocab]")
+    if not x.is_cuda:
+        raise ValueError("logits must be a device tensor")
+    dev = x.get_device()
     n, vocab = x.shape
-    xp, xs = _rows2d(x, "logits", vocab, (torch.float32, torch.bfloat16))
+    xp, xs = _rows(x, "logits", dev, vocab, _SOURCES)
     m, tp = 0, None
     if tokens is not None:
-        tp = _dev(tokens, "tokens", torch.int32)
+        tp = _tensor(tokens, "tokens", dev, torch.int32)
         m = tokens.numel() // n if n else 0
         if tokens.numel() != n * m or (tokens.dim() > 1 and tokens.shape[0] != n):
             raise ValueError("tokens must be [n_rows, n_tokens]")
-    _one_device(logits, tokens, workspace)
 
     def run(st):
-        f32 = dict(dtype=torch.float32, device=x.device)
-        lp = torch.empty((n, m), **f32) if m else None
-        ent = torch.empty(n, **f32)
-        ids = torch.empty((n, top_k), dtype=torch.int32, device=x.device) if top_k else None
-        top = torch.empty((n, top_k), **f32) if top_k else None
-        if n == 0:
-            return Logprobs(lp, ent, ids, top)
-        need = 0 if workspace is not None else gguf_logprobs_workspace(n, vocab, top_k)
-        ws, wp, wn = _work(workspace, need, x.device)
-        _check(lib().gguf_logprobs(xp, TENSOR_F32 if x.dtype == torch.float32 else TENSOR_BF16, n, vocab, xs, tp, m,
-                                   top_k, None if lp is None else lp.data_ptr(), ent.data_ptr(),
-                                   None if ids is None else ids.data_ptr(), None if top is None else top.data_ptr(),
-                                   wp, wn, st), "gguf_logprobs")
+        new = x.new_empty
+        ent = new((n,), dtype=torch.float32)
+        lp = new((n, m), dtype=torch.float32) if m else None
+        ids = new((n, top_k), dtype=torch.int32) if top_k else None
+        top = new((n, top_k), dtype=torch.float32) if top_k else None
+        if n:
+            ws, wp, wn = _work(workspace, lambda: gguf_logprobs_workspace(n, vocab, top_k), dev)
+            _check(lib().gguf_logprobs(xp, TENSOR_F32 if x.dtype is torch.float32 else TENSOR_BF16, n, vocab, xs, tp,
+                                       m, top_k, lp.data_ptr() if m else None, ent.data_ptr(),
+                                       ids.data_ptr() if top_k else None, top.data_ptr() if top_k else None, wp, wn,
+                                       st), "gguf_logprobs")
         return Logprobs(lp, ent, ids, top)
-    return _call(x.device, stream, run)
+    if not 0 <= top_k <= vocab:
+        raise GgufQkArgumentError(ERR_SHAPE, "top_k")
+    return _call(dev, stream, run)
 
 
 # ------------------------------------------------------------------ GGUF files

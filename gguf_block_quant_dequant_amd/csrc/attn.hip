@@ -44,10 +44,14 @@ static int attn_plan(const KvView& c, int64_t n_seqs, int64_t n_heads, int64_t m
   if (want < 1) want = 1;
   int64_t chunk = ((p->span + want - 1) / want + round - 1) / round * round;
   if (chunk < 2 * round) chunk = 2 * round;
+  // short sequences in one launch: the join costs more than the longer chunk
+  // (300 positions, in a graph: 8.7 us against 10.7; 512: 10.1 against 10.7)
+  if (p->span <= 4 * round) chunk = 4 * round;
   if (chunk > most) chunk = most;
   p->chunk = (int32_t)chunk;
   p->splits = (int32_t)((p->span + chunk - 1) / chunk);   // <= 2^25 / 1024 past the first 1024 blocks
-  // No shorter span, as a window leaves, is cut into more splits than this
+  // No shorter span, as a window leaves, is cut into more splits than this (one
+  // split needs no partial results)
   // (the count itself may grow as the span shrinks past a rounding of the chunk).
   p->most_splits = (p->span + most - 1) / most;
   if (p->most_splits < want) p->most_splits = want;
