@@ -25,8 +25,8 @@
 
 #include <type_traits>
 
-#include "device_common.hpp"
 #include "kv_cache.hpp"
+#include "wave_ops.hpp"
 
 namespace gqk {
 
@@ -539,16 +539,15 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
 // Maximum and sum of one head over the splits that hold positions, by one wave;
 // every lane returns them.
 __device__ __forceinline__ float2 attn_join_ml(const float* ml, int splits, int lane) {
-  float m = -__builtin_inff();
-  for (int i = lane; i < splits; i += 64) m = fmaxf(m, ml[2 * i]);
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+  const float2* p = reinterpret_cast<const float2*>(ml);
+  const float2 own = lane < splits ? p[lane] : make_float2(-__builtin_inff(), 0.f);   // the usual whole of it
+  float m = own.x;
+  for (int i = lane + 64; i < splits; i += 64) m = fmaxf(m, p[i].x);
+  m = wave_max(m);
   const float base = m == -__builtin_inff() ? 0.f : m;
-  float l = 0.f;
-  for (int i = lane; i < splits; i += 64) l = fmaf(ml[2 * i + 1], __builtin_amdgcn_exp2f(ml[2 * i] - base), l);
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) l += __shfl_xor(l, d);
-  return make_float2(base, l);
+  float l = own.y * __builtin_amdgcn_exp2f(own.x - base);
+  for (int i = lane + 64; i < splits; i += 64) l = fmaf(p[i].y, __builtin_amdgcn_exp2f(p[i].x - base), l);
+  return make_float2(base, wave_sum(l));
 }
 
 constexpr int kJoinThreads = 256;
@@ -570,14 +569,27 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const AttnArgs 
     const int head = blockIdx.x;
     const int64_t row = (int64_t)s * a.n_heads + head;
     const float* ml = a.part_ml + row * a.splits * 2;
-    const float2 r = attn_join_ml(ml, splits, lane);
     __shared__ __align__(16) f32x4 part[kGroups][kLanes];
     const int c = tid % kLanes, grp = tid / kLanes;
     f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+    // the first partials are asked for before the maximum is known
+    constexpr int kAhead = 4;
+    const float* po = a.part_o + row * a.splits * DIM + c * 4;
+    f32x4 v[kAhead];
+    float vm[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = grp + u * kGroups, at = i < splits ? i : 0;   // loads without a branch between them
+      v[u] = *reinterpret_cast<const f32x4*>(po + (int64_t)at * DIM);
+      vm[u] = ml[2 * at];
+    }
+    const float2 r = attn_join_ml(ml, splits, lane);
     if (grp < kGroups) {
-      const float* po = a.part_o + row * a.splits * DIM + c * 4;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (grp + u * kGroups < splits) sum += v[u] * __builtin_amdgcn_exp2f(vm[u] - r.x);
 #pragma unroll 4
-      for (int i = grp; i < splits; i += kGroups)
+      for (int i = grp + kAhead * kGroups; i < splits; i += kGroups)
         sum += *reinterpret_cast<const f32x4*>(po + (int64_t)i * DIM) * __builtin_amdgcn_exp2f(ml[2 * i] - r.x);
       part[grp][c] = sum;
     }
@@ -597,7 +609,29 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const AttnArgs 
   if (p0 >= n) return;
   __shared__ float2 hml[16];
   const int pos = p0 + tid * 4;
+  const bool live = pos < n;
+  // the slots and the first heads' scores are asked for before the maxima are known
+  int32_t page = -1;
+  float* w = nullptr;
+  float4 old = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (live) {
+    page = kv_page(a.table + (int64_t)s * a.table_stride, pos >> a.c.shift, a.table_stride, a.c.n_pages);
+    w = a.c.weight + kv_slot_at(a.c, page < 0 ? 0 : page, h, pos & (a.c.ps - 1));
+    old = *reinterpret_cast<const float4*>(w);
+  }
+  const float* sp = a.scores + ((int64_t)s * a.n_heads + h * a.group) * a.score_stride + pos;
+  constexpr int kAhead = 4;
+  float4 ahead[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+    if (live && i < a.group) ahead[i] = *reinterpret_cast<const float4*>(sp + i * a.score_stride);
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  auto add = [&](const float4& sc, const float2& r) {
+    acc[0] = fmaf(__builtin_amdgcn_exp2f(sc.x - r.x), r.y, acc[0]);
+    acc[1] = fmaf(__builtin_amdgcn_exp2f(sc.y - r.x), r.y, acc[1]);
+    acc[2] = fmaf(__builtin_amdgcn_exp2f(sc.z - r.x), r.y, acc[2]);
+    acc[3] = fmaf(__builtin_amdgcn_exp2f(sc.w - r.x), r.y, acc[3]);
+  };
   for (int h0 = 0; h0 < a.group; h0 += 16) {
     const int hn = a.group - h0 < 16 ? a.group - h0 : 16;
     __syncthreads();
@@ -606,26 +640,21 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const AttnArgs 
       if (lane == 0) hml[i] = make_float2(r.x, r.y == 0.f ? 0.f : 1.0f / r.y);
     }
     __syncthreads();
-    if (pos < n) {
-#pragma unroll 4
-      for (int i = 0; i < hn; ++i) {
-        const float4 sc = *reinterpret_cast<const float4*>(
-            a.scores + ((int64_t)s * a.n_heads + h * a.group + h0 + i) * a.score_stride + pos);
-        const float2 r = hml[i];
-        acc[0] = fmaf(__builtin_amdgcn_exp2f(sc.x - r.x), r.y, acc[0]);
-        acc[1] = fmaf(__builtin_amdgcn_exp2f(sc.y - r.x), r.y, acc[1]);
-        acc[2] = fmaf(__builtin_amdgcn_exp2f(sc.z - r.x), r.y, acc[2]);
-        acc[3] = fmaf(__builtin_amdgcn_exp2f(sc.w - r.x), r.y, acc[3]);
-      }
+    if (!live) continue;
+    if (h0 == 0) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (i < hn) add(ahead[i], hml[i]);
     }
+#pragma unroll 4
+    for (int i = h0 == 0 ? kAhead : 0; i < hn; ++i)
+      add(*reinterpret_cast<const float4*>(sp + (h0 + i) * a.score_stride), hml[i]);
   }
-  if (pos >= n) return;
-  const int32_t page = kv_page(a.table + (int64_t)s * a.table_stride, pos >> a.c.shift, a.table_stride, a.c.n_pages);
   if (page < 0) return;
-  float* w = a.c.weight + kv_slot_at(a.c, page, h, pos & (a.c.ps - 1));
+  const float o[4] = {old.x, old.y, old.z, old.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    if (pos + j >= first && pos + j < n) w[j] += acc[j];
+    if (pos + j >= first && pos + j < n) w[j] = o[j] + acc[j];
 }
 
 }  // namespace gqk
