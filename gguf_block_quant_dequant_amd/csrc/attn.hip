@@ -138,7 +138,7 @@ int gguf_attn_decode(const gguf_kv_cache* cache, const float* q, int64_t q_strid
   const int64_t tiles = (p.span + kWeightTile - 1) / kWeightTile;
   const int64_t weight_blocks = track ? tiles * a.c.hkv : 0;
   const int64_t joins = p.splits > 1 ? n_heads : 0;
-  if (joins + weight_blocks > INT32_MAX) return GGUF_QK_ERR_LIMIT;
+  if (joins + weight_blocks > INT32_MAX / kJoinThreads) return GGUF_QK_ERR_LIMIT;   // threads of a grid axis
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.table = page_table;
   a.lengths = lengths;

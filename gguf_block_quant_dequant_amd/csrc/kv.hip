@@ -151,11 +151,12 @@ int gguf_kv_append(const gguf_kv_cache* cache, const void* k, const void* v, int
   a.table_stride = table_stride;
   a.n_tokens = n_tokens;
   a.n_seqs = n_seqs;
-  // few tokens: small tiles, so that more than one CU works on them
+  // few tokens: small tiles, so that more CUs work on them (64 tokens, 8 heads:
+  // 3.7 us, 4.5 in tiles of 64; 2048 tokens 5.1 against 5.7)
   a.tile = kAppendTile;
   while (a.tile > 8 && (n_tokens + a.tile - 1) / a.tile * a.c.hkv < 512) a.tile /= 2;
   const int64_t blocks = (n_tokens + a.tile - 1) / a.tile;
-  if (blocks > INT32_MAX) return GGUF_QK_ERR_LIMIT;
+  if (blocks > INT32_MAX / kAppendThreads) return GGUF_QK_ERR_LIMIT;   // threads of a grid axis
   by_cache(kind_of(cache->type), a.c.dim,
            LaunchAppend{a, dim3((unsigned)blocks, (unsigned)a.c.hkv), src_type == GGUF_KV_TYPE_BF16, stream});
   return abi_launched();

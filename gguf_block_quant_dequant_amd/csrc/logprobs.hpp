@@ -11,6 +11,10 @@
 // values reach that bound. They are put in order by counting, per value, the
 // greater ones. Where ties make them too many to hold, or NaN is among the
 // values, k block-wide maxima take their place.
+//
+// Measured at a vocabulary of 128256: 1024 bf16 rows with the top 8 66 us for
+// 263 MB (4.0 TB/s; 49 us without a top, 5.4 TB/s) and 6 us for the joins; 64
+// fp32 rows 12 + 5 us, one row 5.3 + 4.1 (its dependent steps).
 #pragma once
 
 #include "wave_ops.hpp"
@@ -35,7 +39,7 @@ constexpr int kLpWaves = kLpThreads / 64;
 constexpr int kLpPer = 32;                          // values per thread
 constexpr int kLpSplit = kLpThreads * kLpPer;
 constexpr int kLpMaxTop = 64;
-constexpr int kLpQuadTop = 16;
+constexpr int kLpQuadTop = 16;                      // of four lanes' maxima up to here: 66 us, lanes' own 77 (1024 rows, top 8)
 constexpr int kLpCand = 512;                        // values held for the ordering
 constexpr int kLpWaveCand = kLpCand / kLpWaves;     // of one wave
 
@@ -98,7 +102,7 @@ __device__ __forceinline__ void lp_order(const uint64_t* cand, int count, int to
 }
 
 template <bool BF16>
-__global__ __launch_bounds__(kLpThreads, BF16 ? 6 : 4) void logprobs_split_kernel(const LogprobArgs a) {
+__global__ __launch_bounds__(kLpThreads) void logprobs_split_kernel(const LogprobArgs a) {
   constexpr int ES = BF16 ? 2 : 4, VE = 16 / ES, NV = kLpPer / VE;   // values per load, loads per thread
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int split = blockIdx.x;
@@ -169,29 +173,12 @@ __global__ __launch_bounds__(kLpThreads, BF16 ? 6 : 4) void logprobs_split_kerne
   m = wave_max(m);
   // Sums relative to the wave's own maximum: no barrier before the last value.
   float l = 0.f, t = 0.f;
-  if (fabsf(m) < 4096.f) {
-    // In the log2 domain, one fma per value: y = x log2(e) - c with c the
-    // rounded m log2(e). What c lacks (gap, exact by fma, below 2^-11) is
-    // taken out of the sums.
-    constexpr float kLog2e = 1.44269504088896340736f;
-    const float c = m * kLog2e, gap = fmaf(m, kLog2e, -c);
+  const float own = m == -__builtin_inff() ? 0.f : m;   // nothing but -inf: sums of 0
 #pragma unroll
-    for (int i = 0; i < kLpPer; ++i) {
-      const float y = fmaf(x[i], kLog2e, -c), e = __builtin_amdgcn_exp2f(y);
-      l += e;
-      t = fmaf(e, fmaxf(y, -2000.f), t);   // e is 0 there: 0 for -inf, too
-    }
-    const float f = __builtin_amdgcn_exp2f(-gap);
-    t = (t - gap * l) * (f * 0.693147180559945309417f);
-    l *= f;
-  } else {
-    const float base = m == -__builtin_inff() ? 0.f : m;   // nothing but -inf: sums of 0
-#pragma unroll
-    for (int i = 0; i < kLpPer; ++i) {
-      const float d = x[i] - base, e = lp_exp(d);
-      l += e;
-      t = fmaf(e, fmaxf(d, -1000.f), t);
-    }
+  for (int i = 0; i < kLpPer; ++i) {
+    const float d = x[i] - own, e = lp_exp(d);
+    l += e;
+    t = fmaf(e, fmaxf(d, -1000.f), t);   // e is 0 there: 0 for -inf, too
   }
   l = wave_sum(l);
   t = wave_sum(t);
@@ -296,7 +283,8 @@ __global__ __launch_bounds__(kLpThreads, BF16 ? 6 : 4) void logprobs_split_kerne
     }
     if (fits) {
       if (have <= 64) {
-        // one wave, a value per lane, read out lane by lane
+        // one wave, a value per lane, read out lane by lane (66 us for 1024
+        // rows; by the whole block out of LDS 81)
         if (wave == 0) {
           int w = 0, before = 0;
 #pragma unroll
@@ -404,6 +392,7 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_join_kernel(const Logprob
     a.top_id[r * a.top_k + rank] = (int32_t)~(uint32_t)c;
     a.top_lp[r * a.top_k + rank] = (key_logit((uint32_t)(c >> 32)) - M) - logl;
   };
+  // (one read of every list: 5 us for 64 rows of 16 lists of 20, 36 in rounds)
   if (total <= 16 * kLpThreads) {
     uint64_t mine[16];
 #pragma unroll

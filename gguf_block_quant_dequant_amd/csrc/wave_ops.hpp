@@ -25,19 +25,12 @@ __device__ __forceinline__ uint32_t lane_word(uint32_t v, int lane) {
   return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
 }
 
-// (with the maxima of the four rows of 16 lanes)
-__device__ __forceinline__ float wave_max(float v, float (&rows)[4]) {
+__device__ __forceinline__ float wave_max(float v) {
   v = fmaxf(v, dpp_float<0xB1>(v));
   v = fmaxf(v, dpp_float<0x4E>(v));
   v = fmaxf(v, dpp_float<0x141>(v));
   v = fmaxf(v, dpp_float<0x140>(v));
-#pragma unroll
-  for (int i = 0; i < 4; ++i) rows[i] = lane_float(v, 16 * i);
-  return fmaxf(fmaxf(rows[0], rows[1]), fmaxf(rows[2], rows[3]));
-}
-__device__ __forceinline__ float wave_max(float v) {
-  float rows[4];
-  return wave_max(v, rows);
+  return fmaxf(fmaxf(lane_float(v, 0), lane_float(v, 16)), fmaxf(lane_float(v, 32), lane_float(v, 48)));
 }
 
 __device__ __forceinline__ float wave_sum(float v) {
@@ -46,16 +39,6 @@ __device__ __forceinline__ float wave_sum(float v) {
   v += dpp_float<0x141>(v);
   v += dpp_float<0x140>(v);
   return (lane_float(v, 0) + lane_float(v, 16)) + (lane_float(v, 32) + lane_float(v, 48));
-}
-
-__device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b) { return a > b ? a : b; }
-
-__device__ __forceinline__ uint32_t wave_max_word(uint32_t v) {
-  v = max_word(v, dpp_word<0xB1>(v));
-  v = max_word(v, dpp_word<0x4E>(v));
-  v = max_word(v, dpp_word<0x141>(v));
-  v = max_word(v, dpp_word<0x140>(v));
-  return max_word(max_word(lane_word(v, 0), lane_word(v, 16)), max_word(lane_word(v, 32), lane_word(v, 48)));
 }
 
 }  // namespace gqk

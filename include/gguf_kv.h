@@ -81,11 +81,12 @@ int64_t gguf_kv_page_bytes(int type, int64_t n_kv_heads, int64_t head_dim, int64
  * slot[t] of sequence seq[t] (seq NULL: sequence t), rounded once to F16 or
  * BF16 (nearest-even; magnitudes past F16's range become infinities) or
  * quantized to Q8_0 (d = max|x| / 127 over 32 dims, stored as fp16; codes
- * round(x / d), ties to even, within +-127; zeros where d is 0). Where the
- * cache has them, the slots' weight becomes 0 and pos becomes pos[t] (pos
- * NULL: slot[t]). A token whose seq is outside 0 .. n_seqs - 1 or whose slot is
- * outside the table's row (a padding row, marked -1) is dropped. No two tokens
- * of a call may name the same slot (which one stays is undefined).
+ * round(x / d), ties to even, within +-127; zeros where d is 0; values have to
+ * be finite and below 8.3e6, where d leaves fp16's range). Where the cache has
+ * them, the slots' weight becomes 0 and pos becomes pos[t] (pos NULL: slot[t]).
+ * A token whose seq is outside 0 .. n_seqs - 1 or whose slot is outside the
+ * table's row (a padding row, marked -1) is dropped. No two tokens of a call may
+ * name the same slot (its contents are then undefined).
  * k, v 16-byte aligned, rows a multiple of 16 bytes apart. */
 int gguf_kv_append(const gguf_kv_cache* cache, const void* k, const void* v, int32_t src_type,
                    int64_t row_stride, int64_t n_tokens, const int32_t* seq, const int32_t* slot,
@@ -100,21 +101,24 @@ int gguf_kv_append(const gguf_kv_cache* cache, const void* k, const void* v, int
  *   p_i = softmax_i(scale * q . k_i),  out = sum_i p_i v_i
  * ("GGUF Inferencer in R", section 5.2.1, attend). q, out: fp32
  * [n_seqs][n_heads * head_dim], q_stride and out_stride floats from row to row
- * (multiples of 4, out not overlapping an input). A row with no position left
- * (lengths[s] <= 0: an idle slot of the batch) is zero. What lies in the pages
- * behind a sequence's length is not looked at, whatever it holds; keys and
- * values within the length have to be finite.
+ * (multiples of 4; the range from out's first row to its last may not overlap an
+ * input's). A row with no position left (lengths[s] <= 0: an idle slot of the
+ * batch) is zero. What lies in the pages behind a sequence's length is not
+ * looked at, whatever it holds; q, and keys and values within the length, have
+ * to be finite.
  *
  * max_len (<= 2^25) is a bound on the lengths that the host knows (it sets the
  * grid and the workspace); longer sequences are cut at it, as at the table's
- * row. With
- * track, weight[slot] of the cache grows by p_i summed over the query heads of
- * the kv head (needs cache->weight; a page then belongs to one sequence of the
- * call). Without, sequences may share pages.
+ * row. It costs little to set it too high (64 sequences of 1000 positions, 8 kv
+ * heads: 31 us with 1000, 33 with 32768, 61 with 131072), so one captured call
+ * can serve growing sequences. With track, weight[slot] of the cache grows by
+ * p_i summed over the query heads of the kv head (needs cache->weight; a page
+ * then belongs to one sequence of the call). Without, sequences may share pages.
  *
- * fp32 throughout: q and the softmax weights enter the matrix cores as sums of
- * two fp16 (F16 cache) or three bf16 (BF16, Q8_0) numbers, which carry 22 and
- * 24 bits, against the exact cache values. */
+ * fp32 throughout: against the exact cache values, q enters the matrix cores as
+ * the sum of two fp16 (F16 and Q8_0 cache) or three bf16 (BF16) numbers, the
+ * softmax weights as two fp16 (F16) or three bf16 (BF16; Q8_0, times the
+ * scales); two fp16 carry 22 bits, three bf16 24. */
 int64_t gguf_attn_decode_workspace(const gguf_kv_cache* cache, int64_t n_seqs, int64_t n_heads,
                                    int64_t max_len, int32_t track);
 int gguf_attn_decode(const gguf_kv_cache* cache, const float* q, int64_t q_stride, float* out,
