@@ -4,6 +4,7 @@
 
 #include "device_common.hpp"
 #include "kv_layout.hpp"
+#include "wave_ops.hpp"
 
 namespace gqk {
 
@@ -241,7 +242,7 @@ struct EvictArgs {
 
 constexpr int kEvictThreads = 1024;
 constexpr int kEvictWaves = kEvictThreads / 64;
-constexpr int kEvictFew = 4;      // slots past the budget up to which they are picked one by one
+constexpr int kEvictFew = 2;      // slots past the budget up to which they are picked one by one
 constexpr int kHistCopies = 16;   // copies of a digit's histogram, lane & 15: a few shared leading
                                   // digits (weights have few exponents) would queue on one LDS word
 
@@ -249,9 +250,9 @@ constexpr int kHistCopies = 16;   // copies of a digit's histogram, lane & 15: a
 // every NaN above the infinities, below the protected slots' key.
 constexpr uint32_t kKeyProtected = 0xFFFFFFFFu;
 __device__ __forceinline__ uint32_t weight_key(float w) {
-  if (w != w) return 0xFFFFFFFEu;
   const uint32_t b = __float_as_uint(w + 0.0f);
-  return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+  const uint32_t k = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+  return w != w ? 0xFFFFFFFEu : k;
 }
 
 // Exclusive prefix sum over the block's threads; *total: the sum. Two barriers.
@@ -284,15 +285,16 @@ __device__ __forceinline__ int block_scan(int v, int* lds /* kEvictWaves + 1 */,
 // slot order. Thread t holds slots [t S, (t + 1) S): prefix sums over threads
 // are prefix sums over slots.
 // Bound by the passes of its one CU over the keys, not by the 8 bytes per slot:
-// 29 us for 32768 slots with keys in registers, 108 read again per pass. Each
-// count of keys per thread is a kernel of its own (4097 slots by radix select: 12.6 us with 8
-// per thread, 14.0 with 32).
+// 25 us for 32768 slots (7 the loads, 3.5 the keys, 8 the digits, 7 the lists)
+// with keys in registers, 108 read again per pass, 31 in LDS with a lane per
+// slot and the lists from wave masks (a CU's 16 waves share one scalar unit).
+// Each count of keys per thread is a kernel of its own (4097 slots by radix
+// select: 12.2 us with 8 per thread, 14.0 with 32).
 template <int R>
 __global__ __launch_bounds__(kEvictThreads) void kv_evict_select_kernel(const EvictArgs a) {
   __shared__ __align__(16) int hist[256 * kHistCopies + 1024];
   __shared__ int digit_sum[256];
   __shared__ int scan[kEvictWaves + 1];
-  __shared__ int pick[2];
   const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
   const int64_t pair = (int64_t)s * a.c.hkv + h;
   const int n = (int)kv_length(a.lengths[s], a.max_len, a.table_stride, a.c.shift);
@@ -306,7 +308,12 @@ __global__ __launch_bounds__(kEvictThreads) void kv_evict_select_kernel(const Ev
   const int first = tid * S;   // 1024 * S < 2^31: n is
   // Four consecutive slots share a page. Every load goes out, from page 0 where
   // there is none (the value is then not used), so that none waits for another.
-  auto page4 = [&](int slot) { return slot < n ? kv_page(row, slot >> a.c.shift, a.table_stride, a.c.n_pages) : -1; };
+  auto entry4 = [&](int slot) { return row[slot < n ? slot >> a.c.shift : 0]; };   // n lies within the row
+  auto page_of = [&](int32_t id, int slot) {
+    return (int)(slot < n) & (int)(id >= 0) & (int)((int64_t)id < a.c.n_pages) ? id : -1;
+  };
+  auto page4 = [&](int slot) { return page_of(entry4(slot), slot); };
+  const int32_t* const pos = a.recent > 0 ? a.c.pos : reinterpret_cast<const int32_t*>(a.c.weight);   // not used for 0
   auto at4 = [&](int32_t page, int slot) { return kv_slot_at(a.c, page < 0 ? 0 : page, h, slot & (a.c.ps - 1)); };
   constexpr int kRegs = R > 0 ? R : 4;
   uint32_t key[kRegs];
@@ -317,13 +324,18 @@ __global__ __launch_bounds__(kEvictThreads) void kv_evict_select_kernel(const Ev
     const float f[4] = {w.x, w.y, w.z, w.w};
     const int q[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      k[j] = page < 0 ? 0u : (uint32_t)newest - (uint32_t)q[j] < recent ? kKeyProtected : weight_key(f[j]);
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t of = weight_key(f[j]), kept = (uint32_t)newest - (uint32_t)q[j] < recent ? kKeyProtected : of;
+      k[j] = page < 0 ? 0u : kept;
+    }
   };
   auto newest4 = [&](int32_t page, int slot, const int4& p, int m) {
     const int q[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) m = page >= 0 && slot + j < n && q[j] > m ? q[j] : m;
+    for (int j = 0; j < 4; ++j) {
+      const int v = (int)(page >= 0) & (int)(slot + j < n) ? q[j] : INT32_MIN;
+      m = v > m ? v : m;
+    }
     return m;
   };
   auto block_max = [&](int m) {
@@ -349,12 +361,13 @@ __global__ __launch_bounds__(kEvictThreads) void kv_evict_select_kernel(const Ev
     float4 w[R / 4];
     int4 p[R / 4];
 #pragma unroll
-    for (int r = 0; r < R / 4; ++r) page[r] = page4(base + 256 * r);
+    for (int r = 0; r < R / 4; ++r) page[r] = entry4(base + 256 * r);
 #pragma unroll
     for (int r = 0; r < R / 4; ++r) {
+      page[r] = page_of(page[r], base + 256 * r);
       const int64_t at = at4(page[r], base + 256 * r);
       w[r] = *reinterpret_cast<const float4*>(a.c.weight + at);
-      p[r] = a.recent > 0 ? *reinterpret_cast<const int4*>(a.c.pos + at) : make_int4(0, 0, 0, 0);
+      p[r] = *reinterpret_cast<const int4*>(pos + at);
     }
     if (a.recent > 0) {
       int m = INT32_MIN;
@@ -389,7 +402,7 @@ __global__ __launch_bounds__(kEvictThreads) void kv_evict_select_kernel(const Ev
     int m = INT32_MIN;
     for (int r = 0; r < S; r += 4) {
       const int32_t page = page4(first + r);
-      m = newest4(page, first + r, *reinterpret_cast<const int4*>(a.c.pos + at4(page, first + r)), m);
+      m = newest4(page, first + r, *reinterpret_cast<const int4*>(pos + at4(page, first + r)), m);
     }
     newest = block_max(m);
   }
@@ -405,8 +418,7 @@ __global__ __launch_bounds__(kEvictThreads) void kv_evict_select_kernel(const Ev
       for (int r = 0; r < S && first + r < n; r += 4) {
         const int32_t page = page4(first + r);
         const int64_t at = at4(page, first + r);
-        keys4(page, *reinterpret_cast<const float4*>(a.c.weight + at),
-              a.recent > 0 ? *reinterpret_cast<const int4*>(a.c.pos + at) : make_int4(0, 0, 0, 0), key);
+        keys4(page, *reinterpret_cast<const float4*>(a.c.weight + at), *reinterpret_cast<const int4*>(pos + at), key);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           if (first + r + j < n) fn(r + j, key[j]);
@@ -417,9 +429,8 @@ __global__ __launch_bounds__(kEvictThreads) void kv_evict_select_kernel(const Ev
   if (over <= kEvictFew) {
     // A sequence that grew past its budget by a few slots (one, step by step):
     // the least key, of equal ones the highest slot, goes, `over` times. A call
-    // for 16 sequences, 4 heads: past 4096 by one 9.5 us, by four 15.3, by radix
-    // select 15.3 and 16.0; past 16384 by one 14.8, by four 22.9, by five 26.9,
-    // by radix select 24.1, 25.2, 25.5.
+    // for 16 sequences, 4 heads: past 4096 by one 8.3 us (by radix select 10.5),
+    // by two 9.7 (10.7), by three 11.6 (11.1); past 16384 by one 13.4 (20.5).
     __shared__ uint64_t least[kEvictWaves];
     uint64_t gone = 0;   // keys up to this one are out
     int out[kEvictFew];
@@ -469,53 +480,62 @@ __global__ __launch_bounds__(kEvictThreads) void kv_evict_select_kernel(const Ev
   uint32_t prefix = 0;   // digits chosen so far
   int want = budget;     // rank (from the top) still to place among keys with the prefix
   for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256 * kHistCopies; i += kEvictThreads) hist[i] = 0;
+    reinterpret_cast<int4*>(hist)[tid] = make_int4(0, 0, 0, 0);
     __syncthreads();
     const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
     each([&](int, uint32_t k) {
       if ((k & mask) == prefix) atomicAdd(&hist[((k >> shift) & 255u) * kHistCopies + (lane & (kHistCopies - 1))], 1);
     });
     __syncthreads();
-    if (tid < 256) {
-      int sum = 0;
-#pragma unroll
-      for (int c = 0; c < kHistCopies; ++c) sum += hist[tid * kHistCopies + ((c + lane) & (kHistCopies - 1))];
-      digit_sum[tid] = sum;
+    {
+      const int4 c = reinterpret_cast<const int4*>(hist)[tid];   // a quarter of a digit's copies
+      uint32_t sum = (uint32_t)(c.x + c.y + c.z + c.w);
+      sum += dpp_word<0xB1>(sum);
+      sum += dpp_word<0x4E>(sum);
+      if ((tid & 3) == 0) digit_sum[tid >> 2] = (int)sum;
     }
     __syncthreads();
-    if (tid < 64) {   // one wave: lane l holds digits 255 - 4 l down to 252 - 4 l
-      int part[4], sum = 0;
+    // every wave finds the digit: lane l holds digits 255 - 4 l down to 252 - 4 l
+    int part[4], sum = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        part[j] = digit_sum[255 - 4 * lane - j];
-        sum += part[j];
-      }
-      int x = sum;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int y = __shfl_up(x, d);
-        if (lane >= d) x += y;
-      }
-      int above = x - sum;   // keys of greater digits
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (above < want && want <= above + part[j]) {
-          pick[0] = 255 - 4 * lane - j;
-          pick[1] = want - above;
-        }
-        above += part[j];
-      }
+    for (int j = 0; j < 4; ++j) {
+      part[j] = digit_sum[255 - 4 * lane - j];
+      sum += part[j];
     }
-    __syncthreads();
-    prefix |= (uint32_t)pick[0] << shift;
-    want = pick[1];
-    __syncthreads();
+    int x = sum;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int y = __shfl_up(x, d);
+      if (lane >= d) x += y;
+    }
+    int above = x - sum;   // keys of greater digits
+    int digit = -1, rest = 0, held = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (above < want && want <= above + part[j]) {
+        digit = 255 - 4 * lane - j;
+        rest = want - above;
+        held = part[j];
+      }
+      above += part[j];
+    }
+    const int at = __ffsll((unsigned long long)__ballot(digit >= 0)) - 1;   // one lane: 0 < want <= the keys' number
+    prefix |= lane_word((uint32_t)digit, at) << shift;
+    want = (int)lane_word((uint32_t)rest, at);
+    if (want == (int)lane_word((uint32_t)held, at)) {   // all that share the digits so far are kept
+      --prefix;   // not 0: there are more keys than the budget
+      want = 0;
+      break;
+    }
   }
-  // `want` of the keys equal to the threshold stay, lowest slots first
-  int equal = 0;
-  each([&](int, uint32_t k) { equal += k == prefix; });
-  int all;
-  int eq_rank = block_scan(equal, scan, &all);
+  // Kept are the keys above prefix and `want` of those equal to it, lowest slots
+  // first.
+  int all, eq_rank = 0;
+  if (want > 0) {   // the same in all threads
+    int equal = 0;
+    each([&](int, uint32_t k) { equal += k == prefix; });
+    eq_rank = block_scan(equal, scan, &all);
+  }
   const int cut = budget - first;   // the thread's slots from this index on are behind the budget
   int holes = 0, tails = 0, e = eq_rank;
   if constexpr (R > 0) {
@@ -529,10 +549,11 @@ __global__ __launch_bounds__(kEvictThreads) void kv_evict_select_kernel(const Ev
     uint32_t hole = ~keep & before, tail = keep & ~before;
     holes = __popc(hole);
     tails = __popc(tail);
-    int hole_at = block_scan(holes, scan, &all);
-    int tail_at = block_scan(tails, scan, &all);
-    int32_t* dst = a.dst + pair * a.max_moves + hole_at;
-    int32_t* src = a.src + pair * a.max_moves + tail_at;
+    // both counts in one sum: they are equal at the end, half of 1024 R slots at most
+    const uint32_t both = (uint32_t)block_scan(holes | tails << 16, scan, &all);
+    all &= 0xFFFF;
+    int32_t* dst = a.dst + pair * a.max_moves + (both & 0xFFFFu);
+    int32_t* src = a.src + pair * a.max_moves + (both >> 16);
     while (hole) {
       const int r = __ffs(hole) - 1;
       hole &= hole - 1;
