@@ -595,8 +595,8 @@ constexpr int kMoveThreads = 256;
 // move, row of a dim by row, so that the ascending slots of a wave share lines.
 // Block (0, 0, s) also cuts the length (the selection has read it). Bound by HBM:
 // a kept slot's V is one element of each of head_dim lines, so 4 sequences of
-// 32768 cut to 8192 read 154 MB and write 66 for the 52 MB each way that move,
-// in 49 us (4.5 TB/s).
+// 32768 cut to 8192 read 131 MB and write 62 for the 52 MB each way that move,
+// in 49 us (3.9 TB/s).
 template <int KIND, int DIM>
 __global__ __launch_bounds__(kMoveThreads) void kv_evict_move_kernel(const EvictArgs a) {
   __shared__ int64_t sp[kMoveTile], dp[kMoveTile];   // byte offset of page and head
