@@ -42,12 +42,15 @@ struct AttnArgs {
   int64_t table_stride, q_stride, out_stride, max_len, window, score_stride;
   int32_t n_heads, group, head_tiles, splits, chunk, chunk_pages;
   float qscale;     // scale * log2(e)
+  int32_t n_seqs;   // chunks by the lengths (share > 0): at most 64 sequences
+  float share;      // chunk per position of all sequences together; 0: `chunk` for every call
 };
 
 constexpr int kAttnJ = 8;                 // positions of a lane
 constexpr int kAttnTile = 4 * kAttnJ;     // and of a wave's step
 constexpr int kAttnWaves = 4;
 constexpr int kAttnThreads = kAttnWaves * 64;
+constexpr int kAttnLeast = 2 * kAttnTile * kAttnWaves;   // positions of the shortest chunk
 constexpr float kPScaleF16 = 16384.0f;   // softmax weights enter fp16 times 2^14: 2^-24 of the largest is normal
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
@@ -57,6 +60,46 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 // First position a sequence's attention covers.
 __device__ __forceinline__ int attn_first(int n, int64_t window) {
   return window > 0 && (int64_t)n > window ? (int)(n - window) : 0;
+}
+
+// Positions per split. Host code knows a bound on the lengths only; where it
+// leaves room (share > 0) the chunk is cut to the lengths there are, the same in
+// every block: long enough for the launched splits to cover the longest
+// sequence, and for all sequences to take about the blocks that run at once.
+// All 64 lanes of a wave call it.
+__device__ __forceinline__ int attn_chunk(const AttnArgs& a, int lane) {
+  if (a.share == 0.f) return a.chunk;
+  uint32_t span = 0;
+  if (lane < a.n_seqs) {
+    const int n = (int)kv_length(a.lengths[lane], a.max_len, a.table_stride, a.c.shift);
+    span = (uint32_t)(n - (attn_first(n, a.window) & ~(kAttnTile - 1)));
+  }
+  uint32_t total = span, most = span;   // < 2^32: 64 spans of at most 2^25
+  auto step = [&](uint32_t t, uint32_t m) {
+    total += t;
+    most = max_word(most, m);
+  };
+  step(dpp_word<0xB1>(total), dpp_word<0xB1>(most));
+  step(dpp_word<0x4E>(total), dpp_word<0x4E>(most));
+  step(dpp_word<0x141>(total), dpp_word<0x141>(most));
+  step(dpp_word<0x140>(total), dpp_word<0x140>(most));
+  total = lane_word(total, 0) + lane_word(total, 16) + lane_word(total, 32) + lane_word(total, 48);
+  most = max_word(max_word(lane_word(most, 0), lane_word(most, 16)), max_word(lane_word(most, 32), lane_word(most, 48)));
+  constexpr int kRound = kAttnTile * kAttnWaves;
+  const float fair = (float)total * a.share;
+  int c = fair < (float)a.chunk ? (int)fair + 1 : a.chunk;
+  const int cover = ((int)most + a.splits - 1) / a.splits;
+  c = c > cover ? c : cover;
+  c = (c + kRound - 1) / kRound * kRound;
+  c = c < kAttnLeast ? kAttnLeast : c;
+  return c < a.chunk ? c : a.chunk;   // splits * a.chunk covers any length
+}
+
+// Two values rounded to fp16 (nearest-even), in one instruction.
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ f16x2 to_f16x2(float a, float b) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  return __builtin_convertvector((f32x2){a, b}, f16x2);
 }
 
 // Eight fp32 values as parts whose sum they are: three bf16 by truncation (8
@@ -71,10 +114,9 @@ struct Parts {
     for (int j = 0; j < 4; ++j) {
       const float a = x[2 * j], b = x[2 * j + 1];
       if constexpr (KIND == kKvF16) {
-        const _Float16 ha = (_Float16)a, hb = (_Float16)b;
-        w[0][j] = (uint32_t)__builtin_bit_cast(uint16_t, ha) | (uint32_t)__builtin_bit_cast(uint16_t, hb) << 16;
-        const _Float16 la = (_Float16)(a - (float)ha), lb = (_Float16)(b - (float)hb);
-        w[1][j] = (uint32_t)__builtin_bit_cast(uint16_t, la) | (uint32_t)__builtin_bit_cast(uint16_t, lb) << 16;
+        const f16x2 h = to_f16x2(a, b);
+        w[0][j] = __builtin_bit_cast(uint32_t, h);
+        w[1][j] = __builtin_bit_cast(uint32_t, to_f16x2(a - (float)h.x, b - (float)h.y));
       } else {
         const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
         const float ra = a - __uint_as_float(ua & 0xFFFF0000u), rb = b - __uint_as_float(ub & 0xFFFF0000u);
@@ -100,22 +142,9 @@ __device__ __forceinline__ f32x4 attn_mfma(const uint4& a, const uint4& b, const
                                                    0, 0, 0);
 }
 
-// Eight int8 codes as bf16 (exact).
-__device__ __forceinline__ uint4 codes_bf16(const uint2& q) {
-  uint32_t w[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t u = j < 2 ? q.x : q.y;
-    const float lo = (j & 1) ? sbyte2(u) : sbyte0(u), hi = (j & 1) ? sbyte3(u) : sbyte1(u);
-    w[j] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// The same as fp16: with the sign bit flipped a code is 0 .. 255, as the low
-// byte of an fp16 between 1024 and 1279 (one unit per code).
+// Eight int8 codes as fp16 (exact): with the sign bit flipped a code is 0 .. 255,
+// as the low byte of an fp16 between 1024 and 1279 (one unit per code).
 __device__ __forceinline__ uint4 codes_f16(const uint2& q) {
-  typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
   const f16x2 off = {(_Float16)1152.0f, (_Float16)1152.0f};
   const uint32_t a = q.x ^ 0x80808080u, b = q.y ^ 0x80808080u;
   const uint32_t w[4] = {__builtin_amdgcn_perm(0x64646464u, a, 0x04010400u), __builtin_amdgcn_perm(0x64646464u, a, 0x04030402u),
@@ -163,6 +192,15 @@ __device__ __forceinline__ void each_scale(const uint32_t (&d)[N], Fn&& fn) {
   }
 }
 
+// fn(integral constant b) for blocks I .. END - 1.
+template <int I, int END, class Fn>
+__device__ __forceinline__ void each_block(Fn&& fn) {
+  if constexpr (I < END) {
+    fn(std::integral_constant<int, I>{});
+    each_block<I + 1, END>(fn);
+  }
+}
+
 // One block: a chunk of one sequence's positions, up to 16 query heads of one
 // kv head; its waves take the chunk's tiles in turn and join in LDS.
 template <int KIND, int NB, bool TRACK>
@@ -170,45 +208,52 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
   constexpr int DIM = NB * 32;
   constexpr int NT = 2 * NB;   // 16-dim tiles of the output
   constexpr int J = kAttnJ, TILE = kAttnTile, WORDS = 4 * NB, NW = (WORDS + 15) / 16;
-  // operand parts: fp16 pairs for Q K^T of the F16 and Q8_0 caches and for P V of
-  // F16; bf16 triples otherwise (a weight times a Q8_0 scale has any magnitude)
-  constexpr int QK = KIND == kKvBF16 ? kKvBF16 : kKvF16;
-  using Q = Parts<QK>;
-  using P = Parts<KIND>;
+  // operand parts: bf16 triples beside a BF16 cache, fp16 pairs otherwise
+  constexpr int PART = KIND == kKvBF16 ? kKvBF16 : kKvF16;
+  using Q = Parts<PART>;
+  using P = Parts<PART>;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, g = lane >> 4;
   // Heads run fastest, splits slowest: consecutive blocks go to the eight XCDs
   // in turn, and with the splits fastest the empty ones behind the sequences'
   // ends would leave the same XCDs idle (8 splits, half of them empty: 315
-  // instead of 190 us for 1 GB).
-  const int split = blockIdx.z, s = blockIdx.y;
+  // instead of 190 us for 1 GB). The sequences move on by one from split to
+  // split: with 4 heads a sequence would else keep to four XCDs, and the longer
+  // ones wait for a second round (32 sequences of 1 .. 16384, 8 heads: 221 us,
+  // with the turn 203; 64 of 0 .. 4096, 4 heads: 68.5, 66.5).
+  const int split = blockIdx.z, s = (int)((blockIdx.y + blockIdx.z) % (uint32_t)a.n_seqs);
   const int h = blockIdx.x / a.head_tiles, ht = blockIdx.x % a.head_tiles;
   // The chunk's page ids, one per lane (a chunk spans at most 64 pages). Without
-  // a window they are asked for beside the length, not behind it.
+  // a window and with a chunk known beforehand they are asked for beside the
+  // length, not behind it.
   const int32_t length = a.lengths[s];
   int32_t pid = 0;
-  if (a.window == 0 && lane < a.chunk_pages)
+  if (a.window == 0 && a.share == 0.f && lane < a.chunk_pages)
     pid = kv_page(a.table + (int64_t)s * a.table_stride, ((int64_t)split * a.chunk >> a.c.shift) + lane, a.table_stride,
                   a.c.n_pages);
   const int n = (int)kv_length(length, a.max_len, a.table_stride, a.c.shift);
   const int first = attn_first(n, a.window);
-  const int begin = (first & ~(kAttnTile - 1)) + split * a.chunk;   // < 2^31: max_len <= 2^25
+  const int base = first & ~(kAttnTile - 1);
   const int heads = a.group - ht * 16 < 16 ? a.group - ht * 16 : 16;   // valid columns
   const int head0 = h * a.group + ht * 16;
-  if (begin >= n) {
-    // nothing here; a sequence without positions is zero (with more splits
-    // than one the join writes it)
+  // splits cover little more than 2^25 positions: no overflow
+  if (base + split * (a.share == 0.f ? a.chunk : kAttnLeast) >= n) {
+    // nothing here, whatever the chunk; a sequence without positions is zero
+    // (with more splits than one the join writes it)
     if (a.splits == 1) {
       for (int i = tid; i < heads * DIM; i += kAttnThreads)
         a.out[(int64_t)s * a.out_stride + (int64_t)(head0 + i / DIM) * DIM + i % DIM] = 0.f;
     }
     return;
   }
-  const int end = n - begin < a.chunk ? n : begin + a.chunk;
+  const int chunk = __builtin_amdgcn_readfirstlane(attn_chunk(a, lane));
+  const int begin = base + split * chunk;
+  if (begin >= n) return;   // not with one split
+  const int end = n - begin < chunk ? n : begin + chunk;
 
   const int page0 = begin >> a.c.shift;
   const bool paged = page0 + lane <= (end - 1) >> a.c.shift;
-  if (a.window > 0 && paged)
+  if ((a.window > 0 || a.share > 0.f) && paged)
     pid = kv_page(a.table + (int64_t)s * a.table_stride, page0 + lane, a.table_stride, a.c.n_pages);
   if (!paged) pid = 0;   // behind the sequence's last page: whatever the entry, not followed
   const bool any_bad = __any(pid < 0);
@@ -298,7 +343,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
         amax = fmaxf(amax, fabsf(x[b][j]));
       }
     }
-    if constexpr (QK == kKvF16) {
+    if constexpr (PART == kKvF16) {
       // the row's largest magnitude to [512, 1024): both fp16 parts of every
       // value that matters are normal numbers
       amax = fmaxf(amax, __shfl_xor(amax, 16));
@@ -336,7 +381,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
           const uint4 kc = codes_f16(K.c[t][b]);
           r[b] = zero;
 #pragma unroll
-          for (int i = Q::kN - 1; i >= 0; --i) r[b] = attn_mfma<QK>(kc, q[b].p[i], r[b]);
+          for (int i = Q::kN - 1; i >= 0; --i) r[b] = attn_mfma<PART>(kc, q[b].p[i], r[b]);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) sc[4 * t + i] = 0.f;
@@ -357,7 +402,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
 #pragma unroll
         for (int i = Q::kN - 1; i >= 0; --i)
 #pragma unroll
-          for (int b = 0; b < NB; ++b) acc = attn_mfma<QK>(K.x[t][b], q[b].p[i], acc);
+          for (int b = 0; b < NB; ++b) acc = attn_mfma<PART>(K.x[t][b], q[b].p[i], acc);
 #pragma unroll
         for (int i = 0; i < 4; ++i) sc[4 * t + i] = acc[i] * sfac;
       }
@@ -396,22 +441,90 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
       l += p[j];
     }
   };
+  // Weights enter fp16 times a power of two. F16: 2^14. Q8_0: a weight times its
+  // position's scale d has any magnitude, so o of each 32-dim block b is kept in
+  // units of 2^-(ks + e_b), with d 2^e_b (exact) and the product with the weight
+  // 2^ks within fp16's range for every scale met so far: of products below the
+  // greatest by 2^-19 both parts still hold 22 bits. A lane keeps e for the
+  // blocks of its scale words, as the bits of the greatest scale e allows.
+  int ks = 14, e[NW];
+  uint32_t top[NW], most[NW], mul[NW];   // greatest scale met and allowed (bits), 2^e twice
+#pragma unroll
+  for (int j = 0; j < NW; ++j) {
+    e[j] = 15;
+    top[j] = most[j] = 0;
+    mul[j] = 0x78007800u;
+  }
+  auto fit_scales = [&](const uint32_t (&d)[NW]) {
+    bool over = false;
+#pragma unroll
+    for (int j = 0; j < NW; ++j) {
+      const uint32_t lo = d[j] & 0x7FFFu, hi = d[j] >> 16 & 0x7FFFu, mx = lo > hi ? lo : hi;
+      over |= mx > most[j];
+      top[j] = mx > top[j] ? mx : top[j];
+    }
+    if (!__any(over)) return;
+    uint32_t all = 0;
+#pragma unroll
+    for (int j = 0; j < NW; ++j) {   // over the 16 lanes that share a block, then over all
+      uint32_t t = top[j];
+      t = max_word(t, dpp_word<0xB1>(t));
+      t = max_word(t, dpp_word<0x4E>(t));
+      t = max_word(t, (uint32_t)__shfl_xor((int)t, 16));
+      top[j] = t = max_word(t, (uint32_t)__shfl_xor((int)t, 32));
+      all = max_word(all, t);
+    }
+    all = max_word(all, (uint32_t)__shfl_xor((int)all, 4));
+    all = max_word(all, (uint32_t)__shfl_xor((int)all, 8));
+    // a scale with exponent field E lies below 2^(E - 14): E + e + ks <= 30, one
+    // power of two to spare
+    const int E = (int)(all >> 10), k = E >= 29 ? 0 : E <= 15 ? 14 : 29 - E;
+    int grow[NW];
+#pragma unroll
+    for (int j = 0; j < NW; ++j) {
+      const int room = 29 - k - (int)(top[j] >> 10), n = room < 0 ? 0 : room > 15 ? 15 : room;
+      grow[j] = k - ks + n - e[j];
+      e[j] = n;
+      const int last = 30 - k - n;   // greatest exponent field
+      most[j] = last >= 30 ? 0x7FFFu : (uint32_t)last << 10 | 0x3FFu;
+      mul[j] = 0x00010001u * (uint32_t)((15 + n) << 10);
+    }
+    ks = k;
+    auto block = [&](auto bb) {
+      constexpr int b = decltype(bb)::value;
+      uint32_t by[NW];
+#pragma unroll
+      for (int j = 0; j < NW; ++j) by[j] = (uint32_t)grow[j];
+      const float f = __builtin_ldexpf(1.0f, (int)scale_word<4 * b>(by));
+      o[2 * b] *= f;
+      o[2 * b + 1] *= f;
+    };
+    each_block<0, NB>(block);
+  };
   // O^T += V^T P^T, from the V given.
   auto accumulate = [&](const AttnV<KIND, NB>& v, float (&p)[J]) {
     if constexpr (KIND == kKvQ80) {
+      fit_scales(v.d);
+      const float up = __builtin_ldexpf(1.0f, ks);
+#pragma unroll
+      for (int j = 0; j < J; ++j) p[j] *= up;
+      uint32_t sd[NW];
+#pragma unroll
+      for (int j = 0; j < NW; ++j)
+        sd[j] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, v.d[j]) * __builtin_bit_cast(f16x2, mul[j]));
       float pd[8];   // weights times scales: eight positions of a 32-dim block
-      each_scale<0, WORDS>(v.d, [&](int w, uint32_t d) {
+      each_scale<0, WORDS>(sd, [&](int w, uint32_t d) {
         const int b = w / 4, j = 2 * (w % 4);
-        pd[j] = p[j] * half_lo(d);
-        pd[j + 1] = p[j + 1] * half_hi(d);
+        pd[j] = fmaf(p[j], half_lo(d), 0.f);
+        pd[j + 1] = fmaf(p[j + 1], half_hi(d), 0.f);
         if (w % 4 == 3) {
           P pp;
           pp.set(pd);
 #pragma unroll
           for (int t = 2 * b; t < 2 * b + 2; ++t) {
-            const uint4 vc = codes_bf16(v.c[t]);
+            const uint4 vc = codes_f16(v.c[t]);
 #pragma unroll
-            for (int i = P::kN - 1; i >= 0; --i) o[t] = attn_mfma<KIND>(vc, pp.p[i], o[t]);
+            for (int i = P::kN - 1; i >= 0; --i) o[t] = attn_mfma<PART>(vc, pp.p[i], o[t]);
           }
         }
       });
@@ -425,7 +538,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
 #pragma unroll
       for (int i = P::kN - 1; i >= 0; --i)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) o[t] = attn_mfma<KIND>(v.x[t], pp.p[i], o[t]);
+        for (int t = 0; t < NT; ++t) o[t] = attn_mfma<PART>(v.x[t], pp.p[i], o[t]);
     }
   };
 
@@ -476,6 +589,18 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
   if constexpr (KIND == kKvF16) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) o[t] *= 1.0f / kPScaleF16;
+  }
+  if constexpr (KIND == kKvQ80) {
+    auto block = [&](auto bb) {
+      constexpr int b = decltype(bb)::value;
+      uint32_t by[NW];
+#pragma unroll
+      for (int j = 0; j < NW; ++j) by[j] = (uint32_t)-(ks + e[j]);
+      const float f = __builtin_ldexpf(1.0f, (int)scale_word<4 * b>(by));
+      o[2 * b] *= f;
+      o[2 * b + 1] *= f;
+    };
+    each_block<0, NB>(block);
   }
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
@@ -564,7 +689,8 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const AttnArgs 
   const int n = (int)kv_length(a.lengths[s], a.max_len, a.table_stride, a.c.shift);
   const int first = attn_first(n, a.window);
   const int base = first & ~(kAttnTile - 1);
-  const int splits = n > base ? (n - base + a.chunk - 1) / a.chunk : 0;   // that wrote partials
+  const int chunk = attn_chunk(a, lane);
+  const int splits = n > base ? (n - base + chunk - 1) / chunk : 0;   // that wrote partials
   if ((int)blockIdx.x < join_blocks) {
     const int head = blockIdx.x;
     const int64_t row = (int64_t)s * a.n_heads + head;

@@ -41,4 +41,6 @@ __device__ __forceinline__ float wave_sum(float v) {
   return (lane_float(v, 0) + lane_float(v, 16)) + (lane_float(v, 32) + lane_float(v, 48));
 }
 
+__device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
 }  // namespace gqk

@@ -132,3 +132,91 @@ def test_two_streams_at_once():
     for i in range(2):
         for o, t in zip(got[i], top[i]):
             assert np.array_equal(host(o), alone[i]) and np.array_equal(host(t), alone_top[i])
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_bounds_far_above_the_lengths(kind):
+    """Chunks are cut to the lengths on the device: any bound, any mix of lengths,
+    with a window, tracked, under a bound that cuts, and replayed with new lengths."""
+    rng = np.random.default_rng(45)
+    for lengths in ([3000, 1, 0, 2047], [5000], [700] * 9, list(rng.integers(0, 1500, 64))):
+        d = make(rng, TYPES[kind], lengths, -(-max(lengths) // 64), 4, 2, 64, 64, planes=True)
+        for max_len in (max(lengths), 40000, 300000, 1200):
+            for window in (0, 1111):
+                say(kind, len(lengths), max_len, window)
+                before = host(d["cache"].weight).astype(np.float64)
+                got = host(g.gguf_attn_decode(d["cache"], dev(d["q"]), dev(d["table"]), dev(d["lengths"]), max_len,
+                                              window=window, track=True))
+                want, bound, _ = attend_reference(d, 1 / 8, window=window, cut=max_len)
+                check_bound(got, want, bound, (kind, max_len, window))
+                grown = host(d["cache"].weight).astype(np.float64) - before
+                assert np.allclose(grown.sum(), 4 * (np.asarray(lengths) > 0).sum(), rtol=1e-3)
+
+
+def test_captured_under_a_far_bound():
+    rng = np.random.default_rng(46)
+    d = make(rng, TYPES["q8_0"], [6000, 6000, 6000], 47, 8, 2, 128, 128, planes=True, poisoned=False)
+    q, t, n = dev(d["q"]), dev(d["table"]), dev(d["lengths"])
+    out = torch.empty_like(q)
+    ws = torch.empty(g.gguf_attn_decode_workspace(d["cache"], 3, 8, 200000, True), dtype=torch.uint8, device=DEV)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        g.gguf_attn_decode(d["cache"], q, t, n, 200000, track=True, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g.gguf_attn_decode(d["cache"], q, t, n, 200000, track=True, out=out, workspace=ws)
+    for lengths in ([10, 6000, 0], [300, 301, 302], [5999, 1, 4096], [6000, 6000, 6000]):
+        d["lengths"] = np.array(lengths, np.int32)
+        n.copy_(dev(d["lengths"]))
+        graph.replay()
+        got = host(out)
+        assert np.array_equal(got, host(g.gguf_attn_decode(d["cache"], q, t, n, 200000)))
+        want, bound, _ = attend_reference(d, 128 ** -0.5)
+        check_bound(got, want, bound, lengths)
+
+
+def scaled(d, factor):
+    """Multiplies V's Q8_0 scales by factor [head, block, slot of the sequence] (one
+    sequence), rounded to fp16, in the arrays and on the device."""
+    nb, ps = d["dim"] // 32, d["ps"]
+    v = d["v"].reshape(d["n_pages"], d["hkv"], -1)
+    scales = v[..., ps * d["dim"]:].copy().view(np.float16).reshape(d["n_pages"], d["hkv"], nb, ps)
+    n = factor.shape[-1]
+    at = np.arange(n)
+    page, slot = d["table"][0][at // ps], at % ps
+    for h in range(d["hkv"]):
+        for b in range(nb):
+            scales[page, h, b, slot] = (scales[page, h, b, slot].astype(np.float64) * factor[h, b]).astype(np.float16)
+    v[..., ps * d["dim"]:] = scales.reshape(d["n_pages"], d["hkv"], -1).view(np.uint8)
+    d["cache"].v.copy_(dev(d["v"]).view(d["cache"].v.shape))
+
+
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+def test_q8_0_scales_of_all_magnitudes(dim):
+    """V's scales enter fp16 times powers of two that follow the greatest met: blocks
+    of unlike size, scales that grow or fall along the sequence, the type's greatest,
+    subnormal and zero ones. Values below the greatest by 2^-19 keep the full bound."""
+    rng = np.random.default_rng(dim)
+    n, nb = 900, dim // 32
+    ramp = np.linspace(0, 1, n)
+    cases = {
+        "blocks": np.exp2(rng.integers(-12, 21, (2, nb, 1)).astype(float)) * np.ones(n),
+        "rising": np.exp2(18 * ramp - 9) * np.ones((2, nb, 1)),
+        "falling": np.exp2(9 - 18 * ramp) * np.ones((2, nb, 1)),
+        "greatest": np.full((2, nb, n), 65504 / 0.03),
+        "subnormal": np.full((2, nb, n), 2.0 ** -17),
+        "zeros": np.where(rng.random((2, nb, n)) < 0.5, 0.0, 1.0),
+        "negative": np.where(rng.random((2, nb, n)) < 0.5, -1.0, 4.0),
+    }
+    for name, factor in cases.items():
+        d = make(rng, TYPES["q8_0"], [n], 15, 6, 2, dim, 64, poisoned=False)
+        scaled(d, factor)
+        say(dim, name)
+        got = host(g.gguf_attn_decode(d["cache"], dev(d["q"]), dev(d["table"]), dev(d["lengths"]), n))
+        want, bound, _ = attend_reference(d, dim ** -0.5)
+        check_bound(got, want, bound, (dim, name))
+    d = make(rng, TYPES["q8_0"], [n], 15, 6, 2, dim, 64, poisoned=False)
+    scaled(d, np.zeros((2, nb, n)))
+    got = host(g.gguf_attn_decode(d["cache"], dev(d["q"]), dev(d["table"]), dev(d["lengths"]), n))
+    assert not got.any()
