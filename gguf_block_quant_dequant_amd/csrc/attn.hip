@@ -9,10 +9,10 @@ constexpr int64_t kAttnMaxLen = int64_t(1) << 25;   // splits of at least 1024 p
 // Blocks a call aims for, and the longest chunk of positions. Long chunks spare
 // prologues, short ones even out sequences of different lengths. A Q8_0 block's
 // prologue weighs more (its steps read half the bytes): 512 blocks and 2048
-// positions took 65 us against 70 with 1024 (8 sequences of 20001 .. 32768);
-// 16-bit types 221 us with 1024 positions against 226 with 2048 (32 sequences of
-// 1 .. 16384) and 68 us with 2048 blocks against 72 with 1024 (64 of 0 .. 4096);
-// at head dim 256 half the blocks (210 us against 239 for 1 GB).
+// positions took 62 us against 66 with 1024 (8 sequences of 20001 .. 32768);
+// 16-bit types 200 us with 1024 positions against 215 with 2048 (32 sequences of
+// 1 .. 16384) and 67 us with 2048 blocks against 72 with 1024 (64 of 0 .. 4096);
+// at head dim 256 half the blocks (143 us against 158 for 0.62 GB).
 constexpr int64_t kAttnBlocks = 2048, kAttnBlocksQ80 = 512;
 constexpr int64_t kAttnChunk = 1024, kAttnChunkQ80 = 2048;
 

@@ -17,7 +17,9 @@
 // 298 us for 1.1 GB; 64 positions per step of a Q8_0 cache took 256 registers
 // and 85 against 70 us).
 //
-// The kernel reads each cache byte once: the bound is HBM. The matrix cores
+// The kernel reads each cache byte once: the bound is HBM (F16, 1.07 GB of 32
+// ragged sequences in 200 us: 5.3 TB/s; tracked BF16, 0.27 GB in 67 us: 4.0;
+// Q8_0, 0.23 GB in 60 us: 3.8, beside its conversions). The matrix cores
 // run at a fraction of their rate (16 columns for n_heads / n_kv_heads heads,
 // times two or three parts of the fp32 operand), which costs nothing here and
 // keeps fp32 accuracy.

@@ -109,16 +109,17 @@ int gguf_kv_append(const gguf_kv_cache* cache, const void* k, const void* v, int
  *
  * max_len (<= 2^25) is a bound on the lengths that the host knows (it sets the
  * grid and the workspace); longer sequences are cut at it, as at the table's
- * row. It costs little to set it too high (64 sequences of 1000 positions, 8 kv
- * heads: 31 us with 1000, 33 with 32768, 61 with 131072), so one captured call
- * can serve growing sequences. With track, weight[slot] of the cache grows by
+ * row. It costs little to set it too high (4 sequences of 3000 positions, 4 kv
+ * heads: 12.7 us with 3000, 13.8 with 131072; 64 of 1000: 31, 57), so one captured
+ * call can serve growing sequences. With track, weight[slot] of the cache grows by
  * p_i summed over the query heads of the kv head (needs cache->weight; a page
  * then belongs to one sequence of the call). Without, sequences may share pages.
  *
  * fp32 throughout: against the exact cache values, q enters the matrix cores as
- * the sum of two fp16 (F16 and Q8_0 cache) or three bf16 (BF16) numbers, the
- * softmax weights as two fp16 (F16) or three bf16 (BF16; Q8_0, times the
- * scales); two fp16 carry 22 bits, three bf16 24. */
+ * the sum of two fp16 (F16 and Q8_0 cache) or three bf16 (BF16) numbers, and so
+ * do the softmax weights (Q8_0: times V's scales). Three bf16 carry 24 bits, two
+ * fp16 22, of products from 2^-19 of a 32-dim block's greatest scale on; smaller
+ * ones are exact to 2^-41 of it. */
 int64_t gguf_attn_decode_workspace(const gguf_kv_cache* cache, int64_t n_seqs, int64_t n_heads,
                                    int64_t max_len, int32_t track);
 int gguf_attn_decode(const gguf_kv_cache* cache, const float* q, int64_t q_stride, float* out,
