@@ -220,3 +220,32 @@ def test_q8_0_scales_of_all_magnitudes(dim):
     scaled(d, np.zeros((2, nb, n)))
     got = host(g.gguf_attn_decode(d["cache"], dev(d["q"]), dev(d["table"]), dev(d["lengths"]), n))
     assert not got.any()
+
+
+@pytest.mark.parametrize("ps", [16, 32, 256])
+@pytest.mark.parametrize("kind,heads,hkv", [("f16", 34, 1), ("bf16", 5, 5), ("q8_0", 20, 1), ("q8_0", 8, 4)])
+def test_far_bounds_of_page_sizes_and_head_layouts(kind, heads, hkv, ps):
+    rng = np.random.default_rng([47, ps, heads])
+    lengths = [2500, 1029, 33, 0, 511]
+    d = make(rng, TYPES[kind], lengths, -(-2500 // ps) + 1, heads, hkv, 96, ps)
+    for max_len in (2500, 70000, 1 << 25):
+        for window in (0, 300):
+            say(kind, heads, hkv, ps, max_len, window)
+            got = host(g.gguf_attn_decode(d["cache"], dev(d["q"]), dev(d["table"]), dev(d["lengths"]), max_len,
+                                          window=window))
+            want, bound, _ = attend_reference(d, 96 ** -0.5, window=window)
+            check_bound(got, want, bound, (kind, ps, max_len, window))
+
+
+def test_bound_of_zero():
+    rng = np.random.default_rng(48)
+    d = make(rng, TYPES["f16"], [30, 20], 1, 4, 2, 64, 32, planes=True)
+    out = torch.full((2, 4, 64), 7.0, device=DEV)
+    g.gguf_attn_decode(d["cache"], dev(d["q"]), dev(d["table"]), dev(d["lengths"]), 0, track=True, out=out)
+    assert not host(out).any()
+    assert np.array_equal(host(d["cache"].weight), d["weight"])
+    k, v = host(d["cache"].k), host(d["cache"].v)
+    n = dev(d["lengths"])
+    g.gguf_kv_evict(d["cache"], dev(d["table"]), n, 0, 25)   # slots behind the bound are not looked at
+    assert host(n).tolist() == [25, 20]
+    assert np.array_equal(host(d["cache"].k), k) and np.array_equal(host(d["cache"].v), v)
