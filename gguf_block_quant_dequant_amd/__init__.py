@@ -755,8 +755,10 @@ def gguf_attn_decode(cache: KvCache, q, page_table, lengths, max_len, scale=None
                      workspace=None, stream=None):
     """Attention of one new token per sequence: q fp32 [n_seqs, n_heads, head_dim] or
     [n_seqs, n_heads * head_dim] over the first lengths[s] slots of the cache
-    (the last `window` of them where given), scale 1 / sqrt(head_dim) unless
-    given. Returns out, fp32 of q's shape. With `track` the cache's weight grows
+    (the last `window` of them where given: slots, which are the newest tokens only
+    until an eviction reorders them; gguf_kv_evict with budget = recent = the window
+    keeps a window of positions), scale 1 / sqrt(head_dim) unless given. Returns
+    out, fp32 of q's shape. With `track` the cache's weight grows
     by the attention each slot received. `workspace`: a tensor of at least
     gguf_attn_decode_workspace bytes that no overlapping call uses (None: the
     call allocates one)."""
@@ -794,7 +796,8 @@ def gguf_kv_evict_workspace(cache: KvCache, n_seqs: int, max_len: int, budget: i
 def gguf_kv_evict(cache: KvCache, page_table, lengths, max_len, budget, recent=0, workspace=None, stream=None):
     """Cut every sequence longer than `budget` to the `budget` slots per kv head
     that received most attention (the newest `recent` tokens always stay). Moves
-    the kept slots behind the budget into the vacated ones and updates lengths."""
+    the kept slots behind the budget into the vacated ones and updates lengths; the
+    slots are then no longer in the order of positions."""
     dev = cache.device
     tp = _table(page_table, dev)
     n, pages = page_table.shape

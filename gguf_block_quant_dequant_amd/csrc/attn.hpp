@@ -59,7 +59,7 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8v __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-// First position a sequence's attention covers.
+// First slot that a sequence's attention covers: a window counts slots, not cache positions.
 __device__ __forceinline__ int attn_first(int n, int64_t window) {
   return window > 0 && (int64_t)n > window ? (int)(n - window) : 0;
 }

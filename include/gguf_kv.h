@@ -48,7 +48,8 @@ extern "C" {
  * weight (fp32) and pos (int32), [n_pages][n_kv_heads][page_size] each, are
  * optional (NULL): the attention weight a slot has received so far, and the
  * position its token had in the sequence. Eviction leaves slots in another
- * order than positions; attention does not depend on the order.
+ * order than positions, in each kv head another; attention over all of them
+ * (window 0) does not depend on the order, a window does.
  *
  * type: F16, BF16 or Q8_0. head_dim: 64, 96, 128, 192 or 256. page_size: a
  * power of two from 16 to 256. All pointers 16-byte aligned. */
@@ -99,6 +100,11 @@ int gguf_kv_append(const gguf_kv_cache* cache, const void* k, const void* v, int
  * the positions i of [first, n), n = min(lengths[s], max_len) and first =
  * n - window or 0 (window 0: all positions):
  *   p_i = softmax_i(scale * q . k_i),  out = sum_i p_i v_i
+ * A window counts slots and does not look at cache->pos: it is the window's newest
+ * tokens only where slots are in the order of positions, which they no longer are
+ * once gguf_kv_evict has cut the sequence. Where both are wanted, let the eviction
+ * keep the window: append, gguf_kv_evict with budget = recent = the window (it
+ * leaves exactly the tokens with pos > max pos - window), then window 0 here.
  * ("GGUF Inferencer in R", section 5.2.1, attend). q, out: fp32
  * [n_seqs][n_heads * head_dim], q_stride and out_stride floats from row to row
  * (multiples of 4; the range from out's first row to its last may not overlap an
