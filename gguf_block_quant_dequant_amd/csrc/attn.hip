@@ -116,9 +116,8 @@ int gguf_attn_decode(const gguf_kv_cache* cache, const float* q, int64_t q_strid
   if (st) return st;
   if (attn_bytes(a.c, n_seqs, n_heads, p.splits, track != 0, &p) < 0) return GGUF_QK_ERR_LIMIT;
   const int64_t row = n_heads * a.c.dim;
-  if (table_stride < 1 || q_stride < row || out_stride < row || !(scale == scale) || scale > 3.0e38f ||
-      scale < -3.0e38f)
-    return GGUF_QK_ERR_SHAPE;
+  const float qscale = scale * 1.44269504088896340736f;   // infinite past |scale| = 2.358e38
+  if (table_stride < 1 || q_stride < row || out_stride < row || !(qscale - qscale == 0.f)) return GGUF_QK_ERR_SHAPE;
   if (abi_mul(abi_mul(n_seqs, q_stride), 4) < 0 || abi_mul(abi_mul(n_seqs, out_stride), 4) < 0 ||
       abi_mul(abi_mul(n_seqs, table_stride), 4) < 0)
     return GGUF_QK_ERR_SHAPE;
@@ -167,7 +166,7 @@ int gguf_attn_decode(const gguf_kv_cache* cache, const float* q, int64_t q_strid
   a.splits = p.splits;
   a.chunk = p.chunk;
   a.chunk_pages = (p.chunk + a.c.ps - 1) / a.c.ps + 1 < 64 ? (p.chunk + a.c.ps - 1) / a.c.ps + 1 : 64;
-  a.qscale = scale * 1.44269504088896340736f;
+  a.qscale = qscale;
   a.n_seqs = (int32_t)n_seqs;
   a.share = p.share;
   const dim3 grid((unsigned)(a.c.hkv * p.head_tiles), (unsigned)n_seqs, (unsigned)p.splits);

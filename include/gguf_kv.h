@@ -111,7 +111,8 @@ int gguf_kv_append(const gguf_kv_cache* cache, const void* k, const void* v, int
  * input's). A row with no position left (lengths[s] <= 0: an idle slot of the
  * batch) is zero. What lies in the pages behind a sequence's length is not
  * looked at, whatever it holds; q, and keys and values within the length, have
- * to be finite.
+ * to be finite, as have scale * log2(e) (|scale| up to 2.35e38, checked), its
+ * products with q, and the scores times log2(e), in fp32.
  *
  * max_len (<= 2^25) is a bound on the lengths that the host knows (it sets the
  * grid and the workspace); longer sequences are cut at it, as at the table's
