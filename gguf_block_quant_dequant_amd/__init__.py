@@ -747,7 +747,8 @@ def gguf_kv_append(cache: KvCache, k, v, page_table, slot, seq=None, pos=None, s
 
 
 def gguf_attn_decode_workspace(cache: KvCache, n_seqs: int, n_heads: int, max_len: int, track: bool = False) -> int:
-    """Bytes of workspace of a gguf_attn_decode call (any window), or a negative status."""
+    """Bytes of workspace of gguf_attn_decode calls with at most n_seqs sequences, at
+    most max_len and any window, or a negative status."""
     return lib().gguf_attn_decode_workspace(cache.address, n_seqs, n_heads, max_len, int(track))
 
 

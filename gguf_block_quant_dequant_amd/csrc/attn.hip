@@ -19,7 +19,7 @@ constexpr int64_t kAttnChunk = 1024, kAttnChunkQ80 = 2048;
 // How a call is cut and what its workspace holds.
 struct AttnPlan {
   int32_t group, head_tiles, splits, chunk;
-  int64_t span, score_stride, most_splits;
+  int64_t span, score_stride, most_partials;
   int64_t ml_bytes, o_bytes, bytes;
   float share;
 };
@@ -58,21 +58,26 @@ static int attn_plan(const KvView& c, int64_t n_seqs, int64_t n_heads, int64_t m
   const int64_t fill = (q8 ? blocks : blocks / 2) - cells;
   p->share = p->splits > 1 && chunk > kAttnLeast && n_seqs <= 64 && fill > blocks / 8
                  ? (float)((double)(c.hkv * p->head_tiles) / (double)fill) : 0.f;
-  // No shorter span, as a window leaves, is cut into more splits than this (one
-  // split needs no partial results)
-  // (the count itself may grow as the span shrinks past a rounding of the chunk).
-  p->most_splits = (p->span + most - 1) / most;
-  if (p->most_splits < want) p->most_splits = want;
-  if (p->most_splits > (p->span + kAttnLeast - 1) / kAttnLeast) p->most_splits = (p->span + kAttnLeast - 1) / kAttnLeast;
+  // Partial results (rows times splits) of the largest call with at most these
+  // sequences, this bound and any window: a plan's splits are at most `want`
+  // (rows * want <= n_heads * blocks / (hkv * head_tiles)) or, with the longest
+  // chunks, span / most, and never more than the shortest chunks give. 0 where no
+  // such call is split. It grows with n_seqs and max_len.
+  const int64_t rows = n_seqs * n_heads, least = (p->span + kAttnLeast - 1) / kAttnLeast;
+  p->most_partials = n_heads * blocks / (c.hkv * p->head_tiles);
+  if (p->most_partials < rows * ((p->span + most - 1) / most)) p->most_partials = rows * ((p->span + most - 1) / most);
+  if (p->most_partials > rows * least) p->most_partials = rows * least;
+  if (least == 1) p->most_partials = 0;
   p->score_stride = track ? (max_len + kAttnTile - 1) / kAttnTile * kAttnTile : 0;
   return GGUF_QK_OK;
 }
 
-// Sets the workspace's parts for `splits`; -1 where they do not fit.
-static int64_t attn_bytes(const KvView& c, int64_t n_seqs, int64_t n_heads, int64_t splits, bool track, AttnPlan* p) {
+// Sets the workspace's parts for `partials` partial results (0: one split); -1
+// where they do not fit.
+static int64_t attn_bytes(const KvView& c, int64_t n_seqs, int64_t n_heads, int64_t partials, bool track, AttnPlan* p) {
   const int64_t rows = n_seqs * n_heads;
-  p->ml_bytes = splits > 1 || track ? abi_mul(rows, splits * 8) : 0;
-  p->o_bytes = splits > 1 ? abi_mul(rows, splits * c.dim * 4) : 0;
+  p->ml_bytes = abi_mul(partials > 0 ? partials : track ? rows : 0, 8);
+  p->o_bytes = abi_mul(partials, c.dim * 4);
   const int64_t score_bytes = track ? abi_mul(rows, p->score_stride * 4) : 0;
   if (p->ml_bytes < 0 || p->o_bytes < 0 || score_bytes < 0) return -1;
   p->ml_bytes = (p->ml_bytes + 15) / 16 * 16;
@@ -98,7 +103,7 @@ int64_t gguf_attn_decode_workspace(const gguf_kv_cache* cache, int64_t n_seqs, i
   AttnPlan p;
   st = attn_plan(c, n_seqs, n_heads, max_len, 0, track != 0, &p);
   if (st) return st;
-  const int64_t b = attn_bytes(c, n_seqs, n_heads, p.most_splits, track != 0, &p);
+  const int64_t b = attn_bytes(c, n_seqs, n_heads, p.most_partials, track != 0, &p);
   return b < 0 ? GGUF_QK_ERR_LIMIT : b;
 }
 
@@ -114,7 +119,8 @@ int gguf_attn_decode(const gguf_kv_cache* cache, const float* q, int64_t q_strid
   AttnPlan p;
   st = attn_plan(a.c, n_seqs, n_heads, max_len, window, track != 0, &p);
   if (st) return st;
-  if (attn_bytes(a.c, n_seqs, n_heads, p.splits, track != 0, &p) < 0) return GGUF_QK_ERR_LIMIT;
+  const int64_t partials = p.splits > 1 ? n_seqs * n_heads * p.splits : 0;
+  if (attn_bytes(a.c, n_seqs, n_heads, partials, track != 0, &p) < 0) return GGUF_QK_ERR_LIMIT;
   const int64_t row = n_heads * a.c.dim;
   const float qscale = scale * 1.44269504088896340736f;   // infinite past |scale| = 2.358e38
   if (table_stride < 1 || q_stride < row || out_stride < row || !(qscale - qscale == 0.f)) return GGUF_QK_ERR_SHAPE;

@@ -122,6 +122,9 @@ int gguf_kv_append(const gguf_kv_cache* cache, const void* k, const void* v, int
  * p_i summed over the query heads of the kv head (needs cache->weight; a page
  * then belongs to one sequence of the call). Without, sequences may share pages.
  *
+ * The workspace serves every call with at most as many sequences and at most as
+ * large a bound, any window, and the same cache, n_heads and track.
+ *
  * fp32 throughout: against the exact cache values, q enters the matrix cores as
  * the sum of two fp16 (F16 and Q8_0 cache) or three bf16 (BF16) numbers, and so
  * do the softmax weights (Q8_0: times V's scales). Three bf16 carry 24 bits, two
