@@ -353,8 +353,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
       int e = 0;
       if (amax > 0.f && amax < __builtin_inff()) {
         (void)__builtin_frexpf(amax, &e);
-        e = 10 - e;
-        e = e > 100 ? 100 : e < -100 ? -100 : e;
+        e = 10 - e < 100 ? 10 - e : 100;   // -118 at least: 2^-e is finite
       }
 #pragma unroll
       for (int b = 0; b < NB; ++b)
