@@ -125,11 +125,17 @@ int gguf_kv_append(const gguf_kv_cache* cache, const void* k, const void* v, int
  * The workspace serves every call with at most as many sequences and at most as
  * large a bound, any window, and the same cache, n_heads and track.
  *
- * fp32 throughout: against the exact cache values, q enters the matrix cores as
- * the sum of two fp16 (F16 and Q8_0 cache) or three bf16 (BF16) numbers, and so
- * do the softmax weights (Q8_0: times V's scales). Three bf16 carry 24 bits, two
- * fp16 22, of products from 2^-19 of a 32-dim block's greatest scale on; smaller
- * ones are exact to 2^-41 of it. */
+ * Scores, maxima, sums and outputs are fp32. The matrix cores take the exact cache
+ * values against fp32 operands in parts: three bf16 (BF16 cache), which hold their 24
+ * bits, or two fp16 (F16 and Q8_0), which hold 22 bits of all but the smallest. Off by
+ * 2^-22 of itself or, where that is more:
+ *   an element of q by 2^-34 of its row's greatest,
+ *   a softmax weight (F16) by 2^-39 of the greatest,
+ *   a softmax weight times V's scale (Q8_0) by the greatest weight times 2^-39 of the
+ *     32-dim block's greatest scale, 2^-54 of the head's greatest, or 2^-54
+ * so that outputs lose digits only where values some 2^17 times larger than those of
+ * the heavy positions lie under weights below 2^-17. The sums over the positions'
+ * |v| have to stay within fp32. */
 int64_t gguf_attn_decode_workspace(const gguf_kv_cache* cache, int64_t n_seqs, int64_t n_heads,
                                    int64_t max_len, int32_t track);
 int gguf_attn_decode(const gguf_kv_cache* cache, const float* q, int64_t q_stride, float* out,
