@@ -701,6 +701,8 @@ def _call(device, stream, run):
     for what run allocates."""
     if stream is None and torch._C._cuda_getDevice() == device:
         return run(torch._C._cuda_getCurrentRawStream(device))
+    if isinstance(stream, torch.cuda.Stream) and stream.device_index != device:
+        raise ValueError(f"stream is on device {stream.device_index}, the tensors are on device {device}")
     with contextlib.ExitStack() as on:
         on.enter_context(torch.cuda.device(device))
         if stream is not None:
