@@ -731,7 +731,8 @@ def gguf_kv_page_bytes(type_id: int, n_kv_heads: int, head_dim: int, page_size: 
 def gguf_kv_append(cache: KvCache, k, v, page_table, slot, seq=None, pos=None, stream=None):
     """Write tokens (rows of k and v, fp32 or bf16 [n_tokens, n_kv_heads * head_dim],
     rows may lie apart) to slot[t] of sequence seq[t] (None: t). A token with a
-    slot or seq out of range is dropped."""
+    slot or seq out of range is dropped. pos: the tokens' positions where the cache
+    keeps them (None: the slots, right only before a sequence's first eviction)."""
     row, dev = cache.n_kv_heads * cache.head_dim, cache.device
     (kp, ks), (vp, vs) = _rows(k, "k", dev, row, _SOURCES), _rows(v, "v", dev, row, _SOURCES)
     n = k.shape[0]

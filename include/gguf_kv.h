@@ -84,7 +84,10 @@ int64_t gguf_kv_page_bytes(int type, int64_t n_kv_heads, int64_t head_dim, int64
  * quantized to Q8_0 (d = max|x| / 127 over 32 dims, stored as fp16; codes
  * round(x / d), ties to even, within +-127; zeros where d is 0; values have to
  * be finite and below 8.3e6, where d leaves fp16's range). Where the cache has
- * them, the slots' weight becomes 0 and pos becomes pos[t] (pos NULL: slot[t]).
+ * them, the slots' weight becomes 0 and pos becomes pos[t] (pos NULL: slot[t],
+ * which is the position only while a sequence has not been evicted from: after an
+ * eviction slots start again at the budget, and `recent` would take such a token
+ * for an old one; pass pos).
  * A token whose seq is outside 0 .. n_seqs - 1 or whose slot is outside the
  * table's row (a padding row, marked -1) is dropped. No two tokens of a call may
  * name the same slot (its contents are then undefined).
