@@ -801,7 +801,8 @@ def gguf_kv_evict(cache: KvCache, page_table, lengths, max_len, budget, recent=0
     """Cut every sequence longer than `budget` to the `budget` slots per kv head
     that received most attention (the newest `recent` tokens always stay). Moves
     the kept slots behind the budget into the vacated ones and updates lengths; the
-    slots are then no longer in the order of positions."""
+    slots are then no longer in the order of positions. max_len has to bound every
+    length: what lies behind it in a longer sequence is lost, `recent` tokens too."""
     dev = cache.device
     tp = _table(page_table, dev)
     n, pages = page_table.shape

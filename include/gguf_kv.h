@@ -158,8 +158,12 @@ int gguf_attn_decode(const gguf_kv_cache* cache, const float* q, int64_t q_strid
  * and pos), so a call moves no more than it has to, and lengths[s] becomes
  * budget. The slots from budget on are left as they were and their pages are
  * free. Sequences of at most budget slots are left alone.
- * max_len (<= 2^30) bounds the lengths as for the attention (slots behind it are
- * not looked at). budget >= 1, 0 <= recent <= budget; cache->weight is needed; a page
+ * max_len (<= 2^30) has to be a bound that no length exceeds, nor may a length pass
+ * its table row: such a sequence is taken to end there, and as it is cut to budget
+ * all the same, the slots behind (the newest tokens, with or without `recent`) are
+ * lost without having been looked at; with max_len <= budget nothing is selected and
+ * the first budget slots stay. A call captured into a graph needs the bound of its
+ * last replay. budget >= 1, 0 <= recent <= budget; cache->weight is needed; a page
  * belongs to one sequence. */
 int64_t gguf_kv_evict_workspace(const gguf_kv_cache* cache, int64_t n_seqs, int64_t max_len,
                                 int64_t budget);
