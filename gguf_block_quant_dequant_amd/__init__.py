@@ -831,8 +831,8 @@ def gguf_logprobs_workspace(n_rows: int, vocab: int, top_k: int) -> int:
 
 
 def gguf_logprobs(logits, tokens=None, top_k=0, workspace=None, stream=None) -> Logprobs:
-    """Log probabilities of the given tokens (int32 [n_rows, n_tokens] or [n_rows])
-    under logits (fp32 or bf16 [n_rows, vocab] or [vocab], rows may lie apart),
+    """Log probabilities of the given tokens (int32 [n_rows, n_tokens], or flat: one
+    per row, or those of the one row) under logits (fp32 or bf16 [n_rows, vocab] or [vocab], rows may lie apart),
     the entropy of each row, and its top_k tokens with theirs."""
     if not isinstance(logits, torch.Tensor):
         raise TypeError("logits must be a torch tensor")
@@ -847,9 +847,11 @@ def gguf_logprobs(logits, tokens=None, top_k=0, workspace=None, stream=None) -> 
     m, tp = 0, None
     if tokens is not None:
         tp = _tensor(tokens, "tokens", dev, torch.int32)
-        m = tokens.numel() // n if n else 0
-        if tokens.numel() != n * m or (tokens.dim() > 1 and tokens.shape[0] != n):
-            raise ValueError("tokens must be [n_rows, n_tokens]")
+        # a flat list: one token per row, or the tokens of the one row
+        shape = tuple(tokens.shape) if tokens.dim() != 1 else (1, len(tokens)) if n == 1 else (len(tokens), 1)
+        if len(shape) != 2 or shape[0] != n:
+            raise ValueError("tokens must be [n_rows, n_tokens] or [n_rows]")
+        m = shape[1]
 
     def run(st):
         new = x.new_empty
