@@ -10,7 +10,9 @@
 // for few alternatives) bounds its k-th value from below, and little more than k
 // values reach that bound. They are put in order by counting, per value, the
 // greater ones. Where ties make them too many to hold, or NaN is among the
-// values, k block-wide maxima take their place.
+// values, k block-wide maxima take their place; a split where fewer than k
+// lanes (or fours of them) hold a value above -inf is such a case of ties (64 rows of 128256, top 20: 15 us with
+// 99 % of the logits -inf, 234 with 99.9 %).
 //
 // Measured at a vocabulary of 128256: 1024 bf16 rows with the top 8 66 us for
 // 263 MB (4.0 TB/s; 49 us without a top, 5.4 TB/s) and 6 us for the joins; 64
