@@ -1,7 +1,8 @@
-"""Python binding of libgguf_qk (include/gguf_qk.h, gguf_kv.h, gguf_file.h): GGUF
-Q8_0 / Q4_K dequant, fused dequant x activation products, and the steps around
-them (paged key-value cache, single-token attention, log probabilities) on an
-MI355X (gfx950).
+"""Python binding of libgguf_qk (include/gguf_qk.h, gguf_kv.h, gguf_tokens.h,
+gguf_file.h): GGUF Q8_0 / Q4_K dequant, fused dequant x activation products, and
+the steps around them (rotation of queries and keys, paged key-value cache,
+attention of one or several new tokens, log probabilities, verification of drafted
+tokens) on an MI355X (gfx950).
 
 Argument marshalling only: each function takes torch device tensors, passes
 their raw pointers, sizes and the current HIP stream to the C entry point of
@@ -85,6 +86,14 @@ _SIGS = {
     "gguf_logprobs_workspace": (_I64, [_I64, _I64, ctypes.c_int32]),
     "gguf_logprobs": (ctypes.c_int, [_P, ctypes.c_int32, _I64, _I64, _I64, _P, _I64, ctypes.c_int32, _P, _P, _P,
                                      _P, _P, _I64, _P]),
+    "gguf_qk_rope": (ctypes.c_int, [_P, _I64, _P, _I64, _I64, _P, _I64, _P, _I64, _I64, ctypes.c_int32, _I64, _I64, _P,
+                                    _P, ctypes.c_float, _P, _P]),
+    "gguf_attn_extend_workspace": (_I64, [_P, ctypes.c_int32, _I64, _I64, _I64, _I64, _I64, _I64]),
+    "gguf_attn_extend": (ctypes.c_int, [_P, _P, ctypes.c_int32, _I64, _P, _I64, _P, _I64, _I64, _I64, _P, _I64, _P, _I64,
+                                        ctypes.c_float, _I64, _I64, _P, _I64, _P]),
+    "gguf_verify_draft_workspace": (_I64, [_I64, _I64, _I64, ctypes.c_int32]),
+    "gguf_verify_draft": (ctypes.c_int, [_P, _I64, _P, _I64, ctypes.c_int32, _P, _P, _P, _P, _I64, _I64, _I64, _P, _P,
+                                         _P, _P, _P, _I64, _P]),
     "gguf_tensor_nbytes": (_I64, [ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(ctypes.c_int64)]),
     "gguf_file_open": (ctypes.c_int, [ctypes.c_char_p, ctypes.POINTER(ctypes.c_void_p)]),
     "gguf_file_close": (None, [_P]),
@@ -869,6 +878,196 @@ def gguf_logprobs(logits, tokens=None, top_k=0, workspace=None, stream=None) -> 
     if not 0 <= top_k <= vocab:
         raise GgufQkArgumentError(ERR_SHAPE, "top_k")
     return _call(dev, stream, run)
+
+
+class RopeStruct(ctypes.Structure):
+    """struct gguf_rope of the C ABI."""
+    _fields_ = [("freqs", ctypes.c_void_p), ("axes", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+                ("pos_stride", ctypes.c_int64), ("n_axes", ctypes.c_int32), ("n_rot", ctypes.c_int32),
+                ("pairing", ctypes.c_int32), ("magnitude", ctypes.c_float)]
+
+
+ROPE_ADJACENT, ROPE_HALVES = 0, 1
+
+
+def gguf_qk_rope(q, k, pos=None, freqs=None, axes=None, halves=True, magnitude=1.0, q_norm=None, k_norm=None, eps=1e-6,
+                 q_out=None, k_out=None, stream=None):
+    """Norms of queries and keys per head (weights q_norm, k_norm: fp32 [head_dim]) and
+    the rotation by position. q [n_tokens, n_heads, head_dim] and k [n_tokens,
+    n_kv_heads, head_dim] (either may be None), fp32 or bf16, rows may lie apart. pos
+    int32 [n_tokens], or [n_axes, n_tokens] with axes int32 [len(freqs)] naming each
+    pair's axis; freqs fp64 [n_rot / 2] radians per position (both None: norms only).
+    halves: pair i is elements i and i + n_rot / 2, else 2 i and 2 i + 1. Returns
+    (q_out, k_out), which may be given (q and k themselves: in place)."""
+    given = [x for x in (q, k) if x is not None]
+    if not given:
+        raise ValueError("q or k must be given")
+    for x in given:
+        if not isinstance(x, torch.Tensor):
+            raise TypeError("q and k must be torch tensors")
+        if not x.is_cuda:
+            raise ValueError("q and k must be device tensors")
+        if x.dim() != 3:
+            raise ValueError("q and k must be [n_tokens, n_heads, head_dim]")
+    dev, (n, _, d), dt = given[0].get_device(), given[0].shape, given[0].dtype
+    if dt not in _SOURCES or any(x.dtype is not dt or x.shape[0] != n or x.shape[2] != d for x in given):
+        raise ValueError("q and k must be fp32 or bf16 of one type, with the same tokens and head_dim")
+    if (pos is None) != (freqs is None) or (axes is not None and freqs is None):
+        raise ValueError("pos and freqs belong together, and axes to them")
+    ref = None
+    if freqs is not None:
+        fp, half = _tensor(freqs, "freqs", dev, torch.float64), freqs.numel()
+        pp = _tensor(pos, "pos", dev, torch.int32)
+        if pos.dim() not in (1, 2) or pos.shape[-1] != n:
+            raise ValueError("pos must be [n_tokens] or [n_axes, n_tokens]")
+        ap = None if axes is None else _ints(axes, "axes", dev, half)
+        rope = RopeStruct(fp, ap, pp, n, 1 if pos.dim() == 1 else pos.shape[0], 2 * half,
+                          ROPE_HALVES if halves else ROPE_ADJACENT, magnitude)
+        ref = ctypes.addressof(rope)
+    norms = []
+    for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        p = None
+        if w is not None:
+            p = _tensor(w, name, dev, torch.float32)
+            if w.numel() != d:
+                raise ValueError(f"{name} holds {w.numel()} values, expected {d}")
+        norms.append(p)
+
+    def run(st):
+        outs, args = [], []
+        for x, o, name in ((q, q_out, "q"), (k, k_out, "k")):
+            if x is None:
+                outs.append(None)
+                args += [None, 0, None, 0, 0]
+                continue
+            if o is None:
+                o = torch.empty(x.shape, dtype=dt, device=x.device)
+            elif o.shape != x.shape:
+                raise ValueError(f"{name}_out must have {name}'s shape")
+            row = x.shape[1] * d
+            (xp, xs), (op, os_) = _rows(x, name, dev, row, (dt,)), _rows(o, name + "_out", dev, row, (dt,))
+            outs.append(o)
+            args += [xp, xs, op, os_, x.shape[1]]
+        if n:   # empty tensors have no address
+            _check(lib().gguf_qk_rope(*args, TENSOR_F32 if dt is torch.float32 else TENSOR_BF16, n, d, *norms, eps, ref,
+                                      st), "gguf_qk_rope")
+        return outs[0], outs[1]
+    return _call(dev, stream, run)
+
+
+def _source_id(dtype):
+    if dtype not in _SOURCES:
+        raise ValueError(f"expected fp32 or bf16, got {dtype}")
+    return TENSOR_F32 if dtype is torch.float32 else TENSOR_BF16
+
+
+def gguf_attn_extend_workspace(cache: KvCache, dtype, n_seqs: int, n_rows: int, n_heads: int, max_len: int,
+                               window: int = 0, sinks: int = 0) -> int:
+    """Bytes of workspace of a gguf_attn_extend call with queries of this dtype, or a
+    negative status."""
+    return lib().gguf_attn_extend_workspace(cache.address, _source_id(dtype), n_seqs, n_rows, n_heads, max_len, window,
+                                            sinks)
+
+
+def gguf_attn_extend(cache: KvCache, q, page_table, lengths, max_len, row_start=None, scale=None, window=0, sinks=0,
+                     out=None, workspace=None, stream=None):
+    """Attention of the newest tokens of each sequence over the cache that holds them:
+    q fp32 or bf16 [n_rows, n_heads, head_dim] or [n_rows, n_heads * head_dim], the rows
+    of sequence s from row_start[s] to row_start[s + 1] - 1 (int32 [n_seqs + 1]; None:
+    one row per sequence), the last of them at slot lengths[s] - 1. A row sees the slots
+    up to its own; with a window the last `window` of those and the first `sinks` of the
+    sequence. scale 1 / sqrt(head_dim) unless given. Returns out, of q's shape and type
+    (rows of no sequence are left as they were). `workspace`: a tensor of at least
+    gguf_attn_extend_workspace bytes that no overlapping call uses (None: the call
+    allocates one)."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch tensor")
+    d, dev, shape = cache.head_dim, cache.device, q.shape
+    rows, row = shape[0], math.prod(shape[1:])
+    if row == 0 or row % d:
+        raise ValueError("q must be [n_rows, n_heads, head_dim]")
+    heads, type_id = row // d, _source_id(q.dtype)
+    qp, qs = _rows(q, "q", dev, row, (q.dtype,))
+    tp = _table(page_table, dev)
+    seqs, pages = page_table.shape
+    lp = _ints(lengths, "lengths", dev, seqs)
+    rp = None if row_start is None else _ints(row_start, "row_start", dev, seqs + 1)
+    if row_start is None and rows != seqs:
+        raise ValueError("one row per sequence unless row_start is given")
+    scale = d ** -0.5 if scale is None else scale
+
+    def run(st):
+        o = torch.empty(shape, dtype=q.dtype, device=q.device) if out is None else out
+        op, os_ = _rows(o, "out", dev, row, (q.dtype,))
+        if o.shape[0] != rows:
+            raise ValueError("out must have q's rows")
+        if rows == 0 or seqs == 0:   # empty tensors have no address
+            return o
+        ws, wp, wn = _work(workspace, lambda: gguf_attn_extend_workspace(cache, q.dtype, seqs, rows, heads, max_len,
+                                                                         window, sinks), dev)
+        _check(lib().gguf_attn_extend(cache.address, qp, type_id, qs, op, os_, rp, rows, seqs, heads, tp, pages, lp,
+                                      max_len, scale, window, sinks, wp, wn, st), "gguf_attn_extend")
+        return o
+    return _call(dev, stream, run)
+
+
+class Verified(NamedTuple):
+    """What gguf_verify_draft returns."""
+    accepted: torch.Tensor      # int32 [n_seqs]: drafted tokens accepted
+    next_tokens: torch.Tensor   # int32 [n_seqs]: the token behind them
+    accept_prob: torch.Tensor   # fp32 [n_rows]: each drafted token's probability of acceptance
+
+
+def gguf_verify_draft_workspace(n_rows: int, n_seqs: int, vocab: int, has_draft: bool) -> int:
+    """Bytes of workspace of a gguf_verify_draft call, or a negative status."""
+    return lib().gguf_verify_draft_workspace(n_rows, n_seqs, vocab, int(has_draft))
+
+
+def gguf_verify_draft(target, tokens, uniform, uniform_next, row_start, draft=None, temperature=None, workspace=None,
+                      stream=None) -> Verified:
+    """Which drafted tokens the target accepts, and the token behind them, from given
+    random numbers. target and draft: logits, fp32 or bf16 [n_rows, vocab], rows may lie
+    apart (draft None: drafts without probabilities); the rows of sequence s are
+    row_start[s] to row_start[s + 1] - 1 (int32 [n_seqs + 1]), one per drafted token and
+    a last one. tokens int32 and uniform fp32 [n_rows] (the last rows' are not looked
+    at), uniform_next fp32 [n_seqs], temperature fp32 [n_seqs] (0: greedy; None: 1)."""
+    if not isinstance(target, torch.Tensor):
+        raise TypeError("target must be a torch tensor")
+    if target.dim() != 2 or not target.is_cuda:
+        raise ValueError("target must be a device tensor [n_rows, vocab]")
+    dev, (n, vocab), type_id = target.get_device(), target.shape, _source_id(target.dtype)
+    xp, xs = _rows(target, "target", dev, vocab, (target.dtype,))
+    yp, ys = None, 0
+    if draft is not None:
+        yp, ys = _rows(draft, "draft", dev, vocab, (target.dtype,))
+        if draft.shape != target.shape:
+            raise ValueError("draft must have target's shape")
+    sp = _tensor(row_start, "row_start", dev, torch.int32)
+    seqs = row_start.numel() - 1
+    if seqs < 0:
+        raise ValueError("row_start must hold n_seqs + 1 values")
+    tp, up = _ints(tokens, "tokens", dev, n), _floats(uniform, "uniform", dev, n)
+    np_ = _floats(uniform_next, "uniform_next", dev, seqs)
+    cp = None if temperature is None else _floats(temperature, "temperature", dev, seqs)
+
+    def run(st):
+        new = target.new_empty
+        accepted, nxt = new((seqs,), dtype=torch.int32), new((seqs,), dtype=torch.int32)
+        prob = new((n,), dtype=torch.float32)
+        if seqs:
+            ws, wp, wn = _work(workspace, lambda: gguf_verify_draft_workspace(n, seqs, vocab, draft is not None), dev)
+            _check(lib().gguf_verify_draft(xp, xs, yp, ys, type_id, tp, up, np_, sp, n, seqs, vocab, cp,
+                                           accepted.data_ptr(), nxt.data_ptr(), prob.data_ptr() if n else None, wp, wn,
+                                           st), "gguf_verify_draft")
+        return Verified(accepted, nxt, prob)
+    return _call(dev, stream, run)
+
+
+def _floats(t, name, device, n):
+    p = _tensor(t, name, device, torch.float32)
+    if t.numel() != n:
+        raise ValueError(f"{name} holds {t.numel()} values, expected {n}")
+    return p
 
 
 # ------------------------------------------------------------------ GGUF files

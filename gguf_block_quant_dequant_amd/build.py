@@ -72,6 +72,9 @@ UNITS = [
     ("attn_typed.hip", ["-DGQK_KV_KIND=1", *VGPR_FORM], "attn_bf16"),
     ("attn_typed.hip", ["-DGQK_KV_KIND=2", *VGPR_FORM], "attn_q8_0"),
     ("logprobs.hip", [], "logprobs"),
+    ("rope.hip", [], "rope"),
+    ("attn_extend.hip", [], "attn_extend"),
+    ("verify.hip", [], "verify"),
 ]
 
 

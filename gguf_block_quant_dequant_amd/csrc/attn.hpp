@@ -28,6 +28,7 @@
 #include <type_traits>
 
 #include "kv_cache.hpp"
+#include "token_rows.hpp"
 #include "wave_ops.hpp"
 
 namespace gqk {
@@ -46,6 +47,15 @@ struct AttnArgs {
   float qscale;     // scale * log2(e)
   int32_t n_seqs;   // chunks by the lengths (share > 0): at most 64 sequences
   float share;      // chunk per position of all sequences together; 0: `chunk` for every call
+};
+
+// Several new tokens per sequence (gguf_attn_extend): the columns of a wave's
+// tiles are (row, query head) pairs in place of query heads.
+struct AttnRowsArgs : AttnArgs {
+  const int32_t* row_start;   // [n_seqs + 1], or NULL: one row per sequence
+  int64_t n_rows;
+  int32_t sinks;
+  int32_t bf16;               // q and out: BF16, not F32 (strides in elements)
 };
 
 constexpr int kAttnJ = 8;                 // positions of a lane
@@ -207,8 +217,13 @@ __device__ __forceinline__ void each_block(Fn&& fn) {
 
 // One block: a chunk of one sequence's positions, up to 16 query heads of one
 // kv head; its waves take the chunk's tiles in turn and join in LDS.
-template <int KIND, int NB, bool TRACK>
-__global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArgs a) {
+// ARGS AttnRowsArgs: up to 16 (row, query head) pairs, each with positions of its
+// own (SlotRange); the tile's positions are numbered without the stretch between
+// the first slots and the window, so that the chunks cover only what is read.
+template <int KIND, int NB, bool TRACK, class ARGS = AttnArgs>
+__global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const ARGS a) {
+  constexpr bool ROWS = std::is_same<ARGS, AttnRowsArgs>::value;
+  static_assert(!(ROWS && TRACK), "weights are tracked for one token per sequence");
   constexpr int DIM = NB * 32;
   constexpr int NT = 2 * NB;   // 16-dim tiles of the output
   constexpr int J = kAttnJ, TILE = kAttnTile, WORDS = 4 * NB, NW = (WORDS + 15) / 16;
@@ -225,40 +240,97 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
   // split: with 4 heads a sequence would else keep to four XCDs, and the longer
   // ones wait for a second round (32 sequences of 1 .. 16384, 8 heads: 221 us,
   // with the turn 203; 64 of 0 .. 4096, 4 heads: 68.5, 66.5).
-  const int split = blockIdx.z, s = (int)((blockIdx.y + blockIdx.z) % (uint32_t)a.n_seqs);
-  const int h = blockIdx.x / a.head_tiles, ht = blockIdx.x % a.head_tiles;
+  const int split = blockIdx.z;
+  int s, h, ht, row0 = 0, rows = 1;   // ht: tile of columns; ROWS: the sequence's rows
+  if constexpr (ROWS) {
+    h = blockIdx.x;
+    const RowTile t = find_row_tile(a.row_start, a.n_seqs, a.n_rows, a.group, 16,
+                                    (int)((blockIdx.y + blockIdx.z) % gridDim.y), lane);
+    if (t.seq < 0) return;
+    s = t.seq;
+    ht = t.tile;
+    row0 = t.row0;
+    rows = t.rows;
+  } else {
+    s = (int)((blockIdx.y + blockIdx.z) % (uint32_t)a.n_seqs);
+    h = blockIdx.x / a.head_tiles;
+    ht = blockIdx.x % a.head_tiles;
+  }
   // The chunk's page ids, one per lane (a chunk spans at most 64 pages). Without
   // a window and with a chunk known beforehand they are asked for beside the
   // length, not behind it.
   const int32_t length = a.lengths[s];
   int32_t pid = 0;
-  if (a.window == 0 && a.share == 0.f && lane < a.chunk_pages)
+  if (!ROWS && a.window == 0 && a.share == 0.f && lane < a.chunk_pages)
     pid = kv_page(a.table + (int64_t)s * a.table_stride, ((int64_t)split * a.chunk >> a.c.shift) + lane, a.table_stride,
                   a.c.n_pages);
-  const int n = (int)kv_length(length, a.max_len, a.table_stride, a.c.shift);
-  const int first = attn_first(n, a.window);
-  const int base = first & ~(kAttnTile - 1);
-  const int heads = a.group - ht * 16 < 16 ? a.group - ht * 16 : 16;   // valid columns
-  const int head0 = h * a.group + ht * 16;
+  const int held = (int)kv_length(length, a.max_len, a.table_stride, a.c.shift);
+  // ROWS: n counts the positions read, gap lie unread behind the first pad of
+  // them, all columns see [first, full) of the positions
+  int n = held, first, base, full, gap = 0, pad = 0, near = 0;
+  SlotRange range;   // ROWS: of this lane's column
+  if constexpr (ROWS) {
+    const int width = rows * a.group;   // columns of the sequence
+    const TileRange r = tile_range(held, rows, a.group, ht, 16, a.window, a.sinks, a.c.ps > kAttnTile ? a.c.ps : kAttnTile);
+    const int c = ht * 16 + col;
+    range = slot_range(held, rows, (c < width ? c : width - 1) / a.group, a.window);
+    n = r.n;
+    gap = r.gap;
+    pad = r.pad;
+    near = r.near;
+    first = r.far - gap;
+    full = r.full - gap;
+    base = 0;
+  } else {
+    first = attn_first(n, a.window);
+    base = first & ~(kAttnTile - 1);
+    full = n;
+  }
+  const int columns = ROWS ? rows * a.group : a.group;
+  const int heads = columns - ht * 16 < 16 ? columns - ht * 16 : 16;   // valid columns
+  const int head0 = h * a.group + (ROWS ? 0 : ht * 16);
+  // the row of q and out and the query head of column c
+  auto column_row = [&](int c) -> int64_t { return ROWS ? row0 + (ht * 16 + c) / a.group : s; };
+  auto column_head = [&](int c) -> int { return head0 + (ROWS ? (ht * 16 + c) % a.group : c); };
+  auto store_out = [&](int c, int d, const f32x4& x) {   // dims d .. d + 3
+    if constexpr (ROWS) {
+      const int64_t at = column_row(c) * a.out_stride + (int64_t)column_head(c) * DIM + d;
+      if (a.bf16) {
+        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at) =
+            make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+        return;
+      }
+      *reinterpret_cast<f32x4*>(a.out + at) = x;
+    } else {
+      *reinterpret_cast<f32x4*>(a.out + (int64_t)s * a.out_stride + (int64_t)(head0 + c) * DIM + d) = x;
+    }
+  };
   // splits cover little more than 2^25 positions: no overflow
   if (base + split * (a.share == 0.f ? a.chunk : kAttnLeast) >= n) {
     // nothing here, whatever the chunk; a sequence without positions is zero
     // (with more splits than one the join writes it)
     if (a.splits == 1) {
-      for (int i = tid; i < heads * DIM; i += kAttnThreads)
-        a.out[(int64_t)s * a.out_stride + (int64_t)(head0 + i / DIM) * DIM + i % DIM] = 0.f;
+      if constexpr (ROWS) {
+        for (int i = tid; i < heads * (DIM / 4); i += kAttnThreads)
+          store_out(i / (DIM / 4), i % (DIM / 4) * 4, f32x4{0.f, 0.f, 0.f, 0.f});
+      } else {
+        for (int i = tid; i < heads * DIM; i += kAttnThreads)
+          a.out[(int64_t)s * a.out_stride + (int64_t)(head0 + i / DIM) * DIM + i % DIM] = 0.f;
+      }
     }
     return;
   }
-  const int chunk = __builtin_amdgcn_readfirstlane(attn_chunk(a, lane));
+  const int chunk = ROWS ? a.chunk : __builtin_amdgcn_readfirstlane(attn_chunk(a, lane));
   const int begin = base + split * chunk;
   if (begin >= n) return;   // not with one split
   const int end = n - begin < chunk ? n : begin + chunk;
 
   const int page0 = begin >> a.c.shift;
   const bool paged = page0 + lane <= (end - 1) >> a.c.shift;
-  if ((a.window > 0 || a.share > 0.f) && paged)
-    pid = kv_page(a.table + (int64_t)s * a.table_stride, page0 + lane, a.table_stride, a.c.n_pages);
+  if ((ROWS || a.window > 0 || a.share > 0.f) && paged) {
+    const int skipped = ROWS && page0 + lane >= pad >> a.c.shift ? gap >> a.c.shift : 0;
+    pid = kv_page(a.table + (int64_t)s * a.table_stride, page0 + lane + skipped, a.table_stride, a.c.n_pages);
+  }
   if (!paged) pid = 0;   // behind the sequence's last page: whatever the entry, not followed
   const bool any_bad = __any(pid < 0);
 
@@ -318,8 +390,12 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
   // last, and every one of a chunk with a bad page) behind it, masked.
   constexpr int step = TILE * kAttnWaves;
   const int mine = begin + wave * TILE;
-  int t_lo = mine, t_hi = end & ~(TILE - 1);
-  if (t_lo < first) t_lo += step;
+  int t_lo = mine, t_hi = (ROWS && full < end ? full : end) & ~(TILE - 1);
+  if constexpr (ROWS) {
+    if (t_lo < first) t_lo += (first - t_lo + step - 1) / step * step;
+  } else {
+    if (t_lo < first) t_lo += step;
+  }
   if (any_bad) t_hi = t_lo;
   AttnK<KIND, NB> K;
   AttnV<KIND, NB> V;
@@ -334,13 +410,26 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
   {
     float x[NB][8];
     const bool live = col < heads;
+    const int64_t q_at = column_row(live ? col : 0) * a.q_stride + (int64_t)column_head(live ? col : 0) * DIM + 8 * g;
     const float* qp = a.q + (int64_t)s * a.q_stride + (int64_t)(head0 + (live ? col : 0)) * DIM + 8 * g;
+    if constexpr (ROWS) qp = a.q + (a.bf16 ? 0 : q_at);
     float amax = 0.f;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const float4 u = *reinterpret_cast<const float4*>(qp + 32 * b);
-      const float4 v = *reinterpret_cast<const float4*>(qp + 32 * b + 4);
-      const float y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+      float y[8];
+      bool wide = true;
+      if constexpr (ROWS) wide = !a.bf16;
+      if (wide) {
+        const float4 u = *reinterpret_cast<const float4*>(qp + 32 * b);
+        const float4 v = *reinterpret_cast<const float4*>(qp + 32 * b + 4);
+        const float z[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = z[j];
+      } else {
+        Raw8<true> r;
+        r.load(a.q, q_at + 32 * b);
+        r.values(y);
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         x[b][j] = live ? y[j] * a.qscale : 0.f;
@@ -561,6 +650,11 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
   }
   for (int t0 = mine; t0 < end; t0 += step) {
     if (t0 >= t_lo && t0 < t_hi) continue;
+    const int skipped = ROWS && t0 >= pad ? gap : 0;
+    // between the first slots and the window, where that is less than a page
+    if constexpr (ROWS) {
+      if (t0 + skipped >= a.sinks && t0 + skipped + TILE <= near) continue;
+    }
     AttnK<KIND, NB> ek;
     AttnV<KIND, NB> ev;
     load_k(ek, t0);
@@ -570,7 +664,13 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
     hi = hi < 0 ? 0 : hi > J ? J : hi;
     lo = lo < 0 ? 0 : lo > J ? J : lo;
     uint32_t live = ((1u << hi) - 1u) & ~((1u << lo) - 1u);   // of the lane's positions
-    if (any_bad && __shfl(pid, ((p0 >> a.c.shift) - page0) & 63) < 0) live = 0u;
+    uint32_t real = live;                                      // of those whose values are looked at
+    if constexpr (ROWS) {
+      const int at = p0 + skipped;
+      live = slot_bits(range, a.sinks, at);
+      real = low_bits(end - p0);   // no column sees those behind, nor are their page ids known
+    }
+    if (any_bad && __shfl(pid, ((p0 >> a.c.shift) - page0) & 63) < 0) live = real = 0u;
     float sc[J], p[J];
     scores(ek, sc);
 #pragma unroll
@@ -579,7 +679,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
     softmax(sc, p);
     // V behind the length may hold anything: masked positions become 0 (Q8_0:
     // their scales; any code is finite)
-    auto pair = [&](int i) { return ((live >> 2 * i & 1) ? 0xFFFFu : 0u) | ((live >> 2 * i & 2) ? 0xFFFF0000u : 0u); };
+    auto pair = [&](int i) { return ((real >> 2 * i & 1) ? 0xFFFFu : 0u) | ((real >> 2 * i & 2) ? 0xFFFF0000u : 0u); };
     AttnV<KIND, NB> mv = ev;
     if constexpr (KIND == kKvQ80) {
       const uint32_t mask = pair(col & 3);
@@ -638,7 +738,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
   if ((partial || TRACK) && tid < heads) {
     float wf[kAttnWaves];
     const float2 r = joined(tid, wf);
-    float* d = a.part_ml + (((int64_t)s * a.n_heads + head0 + tid) * a.splits + split) * 2;
+    float* d = a.part_ml + ((column_row(tid) * a.n_heads + column_head(tid)) * a.splits + split) * 2;
     d[0] = r.x;
     d[1] = r.y;
   }
@@ -656,12 +756,11 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const AttnArg
 #pragma unroll
       for (int w = 0; w < kAttnWaves; ++w) sum += *reinterpret_cast<const f32x4*>(&part[w][c][d4]) * wf[w];
       if (partial) {
-        *reinterpret_cast<f32x4*>(a.part_o + (((int64_t)s * a.n_heads + head0 + c) * a.splits + split) * DIM + 32 * b +
-                                  d4) = sum;
+        *reinterpret_cast<f32x4*>(a.part_o + ((column_row(c) * a.n_heads + column_head(c)) * a.splits + split) * DIM +
+                                  32 * b + d4) = sum;
       } else {
         const float inv = r.y == 0.f ? 0.f : 1.0f / r.y;   // no position left: zeros
-        *reinterpret_cast<f32x4*>(a.out + (int64_t)s * a.out_stride + (int64_t)(head0 + c) * DIM + 32 * b + d4) =
-            sum * inv;
+        store_out(c, 32 * b + d4, sum * inv);
       }
     }
     if (b + 1 < NB) __syncthreads();
@@ -685,13 +784,53 @@ __device__ __forceinline__ float2 attn_join_ml(const float* ml, int splits, int 
 constexpr int kJoinThreads = 256;
 constexpr int kWeightTile = 1024;   // positions per block of the weight update
 
+// One (row, query head) of the output from its splits' partial results.
+template <int DIM>
+__device__ __forceinline__ void attn_join_row(const AttnArgs& a, int64_t row, int splits, int tid, int lane,
+                                              f32x4* sum_out, bool* store) {
+  constexpr int kLanes = DIM / 4;                    // float4 lanes of a row
+  constexpr int kGroups = kJoinThreads / kLanes;     // splits in flight side by side
+  const float* ml = a.part_ml + row * a.splits * 2;
+  __shared__ __align__(16) f32x4 part[kGroups][kLanes];
+  const int c = tid % kLanes, grp = tid / kLanes;
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+  // the first partials are asked for before the maximum is known
+  constexpr int kAhead = 4;
+  const float* po = a.part_o + row * a.splits * DIM + c * 4;
+  f32x4 v[kAhead];
+  float vm[kAhead];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) {
+    const int i = grp + u * kGroups, at = i < splits ? i : 0;   // loads without a branch between them
+    v[u] = *reinterpret_cast<const f32x4*>(po + (int64_t)at * DIM);
+    vm[u] = ml[2 * at];
+  }
+  const float2 r = attn_join_ml(ml, splits, lane);
+  if (grp < kGroups) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (grp + u * kGroups < splits) sum += v[u] * __builtin_amdgcn_exp2f(vm[u] - r.x);
+#pragma unroll 4
+    for (int i = grp + kAhead * kGroups; i < splits; i += kGroups)
+      sum += *reinterpret_cast<const f32x4*>(po + (int64_t)i * DIM) * __builtin_amdgcn_exp2f(ml[2 * i] - r.x);
+    part[grp][c] = sum;
+  }
+  __syncthreads();
+  *store = tid < kLanes;
+  if (tid < kLanes) {
+    sum = part[0][tid];
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i) sum += part[i][tid];
+    const float inv = r.y == 0.f ? 0.f : 1.0f / r.y;
+    *sum_out = sum * inv;
+  }
+}
+
 // Blocks x < join_blocks: the joined output of query head x. The others: the
 // weights of 1024 positions of one kv head, summed over its query heads in
 // order (p = exp2(score - max) / sum) and added to the slots' weight.
 template <int DIM>
 __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const AttnArgs a, int join_blocks, int weight_tiles) {
-  constexpr int kLanes = DIM / 4;                    // float4 lanes of a row
-  constexpr int kGroups = kJoinThreads / kLanes;     // splits in flight side by side
   const int s = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
   const int n = (int)kv_length(a.lengths[s], a.max_len, a.table_stride, a.c.shift);
   const int first = attn_first(n, a.window);
@@ -700,40 +839,10 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const AttnArgs 
   const int splits = n > base ? (n - base + chunk - 1) / chunk : 0;   // that wrote partials
   if ((int)blockIdx.x < join_blocks) {
     const int head = blockIdx.x;
-    const int64_t row = (int64_t)s * a.n_heads + head;
-    const float* ml = a.part_ml + row * a.splits * 2;
-    __shared__ __align__(16) f32x4 part[kGroups][kLanes];
-    const int c = tid % kLanes, grp = tid / kLanes;
-    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-    // the first partials are asked for before the maximum is known
-    constexpr int kAhead = 4;
-    const float* po = a.part_o + row * a.splits * DIM + c * 4;
-    f32x4 v[kAhead];
-    float vm[kAhead];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int i = grp + u * kGroups, at = i < splits ? i : 0;   // loads without a branch between them
-      v[u] = *reinterpret_cast<const f32x4*>(po + (int64_t)at * DIM);
-      vm[u] = ml[2 * at];
-    }
-    const float2 r = attn_join_ml(ml, splits, lane);
-    if (grp < kGroups) {
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u)
-        if (grp + u * kGroups < splits) sum += v[u] * __builtin_amdgcn_exp2f(vm[u] - r.x);
-#pragma unroll 4
-      for (int i = grp + kAhead * kGroups; i < splits; i += kGroups)
-        sum += *reinterpret_cast<const f32x4*>(po + (int64_t)i * DIM) * __builtin_amdgcn_exp2f(ml[2 * i] - r.x);
-      part[grp][c] = sum;
-    }
-    __syncthreads();
-    if (tid < kLanes) {
-      sum = part[0][tid];
-#pragma unroll
-      for (int i = 1; i < kGroups; ++i) sum += part[i][tid];
-      const float inv = r.y == 0.f ? 0.f : 1.0f / r.y;
-      *reinterpret_cast<f32x4*>(a.out + (int64_t)s * a.out_stride + (int64_t)head * DIM + tid * 4) = sum * inv;
-    }
+    f32x4 sum;
+    bool store;
+    attn_join_row<DIM>(a, (int64_t)s * a.n_heads + head, splits, tid, lane, &sum, &store);
+    if (store) *reinterpret_cast<f32x4*>(a.out + (int64_t)s * a.out_stride + (int64_t)head * DIM + tid * 4) = sum;
     return;
   }
   const int wb = blockIdx.x - join_blocks;
@@ -788,6 +897,30 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const AttnArgs 
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     if (pos + j >= first && pos + j < n) w[j] = o[j] + acc[j];
+}
+
+// The same for several new tokens per sequence: block (row, query head), with the
+// splits of the row's tile of `columns` (row, query head) pairs.
+template <int DIM>
+__global__ __launch_bounds__(kJoinThreads) void attn_join_rows_kernel(const AttnRowsArgs a, int columns, int unit) {
+  const int tid = threadIdx.x, lane = tid & 63, head = blockIdx.y;
+  const int64_t row = blockIdx.x;
+  const RowTile t = find_row(a.row_start, a.n_seqs, a.n_rows, row, lane);
+  if (t.seq < 0) return;   // of no sequence
+  const int held = (int)kv_length(a.lengths[t.seq], a.max_len, a.table_stride, a.c.shift);
+  const int c = (int)(row - t.row0) * a.group + head % a.group;
+  const TileRange r = tile_range(held, t.rows, a.group, c / columns, columns, a.window, a.sinks, unit);
+  const int splits = r.n > 0 ? (r.n + a.chunk - 1) / a.chunk : 0;   // that wrote partials
+  f32x4 sum;
+  bool store;
+  attn_join_row<DIM>(a, row * a.n_heads + head, splits, tid, lane, &sum, &store);
+  if (!store) return;
+  const int64_t at = row * a.out_stride + (int64_t)head * DIM + tid * 4;
+  if (a.bf16)
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at) =
+        make_uint2(pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3]));
+  else
+    *reinterpret_cast<f32x4*>(a.out + at) = sum;
 }
 
 }  // namespace gqk

@@ -1,0 +1,165 @@
+// Entry points of the attention of several new tokens per sequence
+// (include/gguf_tokens.h): checks, the split over the positions, launches.
+#include "../../include/gguf_tokens.h"
+#include "abi_check.hpp"
+#include "attn_launch.hpp"
+
+namespace gqk {
+
+constexpr int64_t kExtendMaxLen = int64_t(1) << 25;
+constexpr int64_t kExtendBlocks = 1024;   // blocks a call aims for
+constexpr int64_t kExtendChunk = 1024;    // longest chunk of positions of the few-rows kernel
+constexpr int kFewColumns = 16;           // columns of its tiles
+
+struct ExtendPlan {
+  int32_t group, splits, chunk, unit;
+  int64_t tiles;              // tiles of columns, at most
+  int64_t ml_bytes, bytes;
+};
+
+static int extend_plan(const KvView& c, int32_t type, int64_t n_seqs, int64_t n_rows, int64_t n_heads, int64_t max_len,
+                       int64_t window, int64_t sinks, ExtendPlan* p) {
+  if ((type != GGUF_KV_TYPE_F32 && type != GGUF_KV_TYPE_BF16) || n_seqs < 0 || n_rows < 0 || n_heads < 1 ||
+      n_heads % c.hkv || max_len < 0 || window < 0 || sinks < 0)
+    return GGUF_QK_ERR_SHAPE;
+  if (n_seqs > (1 << 20) || n_rows > (int64_t(1) << 23) || n_heads > 65535 || max_len > kExtendMaxLen ||
+      sinks > kExtendMaxLen)
+    return GGUF_QK_ERR_LIMIT;
+  p->group = (int32_t)(n_heads / c.hkv);
+  if (n_rows * p->group > INT32_MAX / 2) return GGUF_QK_ERR_LIMIT;
+  p->unit = c.ps > kAttnTile ? c.ps : kAttnTile;
+  p->tiles = (n_rows * p->group + n_seqs * (kFewColumns - 1)) / kFewColumns;
+  if (p->tiles > 65535) return GGUF_QK_ERR_LIMIT;   // along a grid axis
+  // positions that a tile's columns read, at most: the first slots, the window
+  // and the tile's rows, in whole units
+  int64_t span = max_len;
+  if (window > 0 && window < max_len) {
+    const int64_t pad = (sinks + p->unit - 1) / p->unit * p->unit;
+    const int64_t seen = pad + window + (kFewColumns - 1) / p->group + 1 + p->unit;
+    if (seen < span) span = seen;
+  }
+  if (span < 1) span = 1;
+  const int64_t round = kAttnTile * kAttnWaves;
+  int64_t most = int64_t(64) << c.shift;
+  if (most > kExtendChunk) most = kExtendChunk;
+  const int64_t cells = p->tiles * c.hkv;
+  int64_t want = cells > 0 ? kExtendBlocks / cells : 1;
+  if (want < 1) want = 1;
+  int64_t chunk = ((span + want - 1) / want + round - 1) / round * round;
+  if (chunk < kAttnLeast) chunk = kAttnLeast;
+  if (span <= 4 * round) chunk = 4 * round;
+  if (chunk > most) chunk = most;
+  p->chunk = (int32_t)chunk;
+  p->splits = (int32_t)((span + chunk - 1) / chunk);
+  const int64_t partials = p->splits > 1 ? abi_mul(n_rows * n_heads, p->splits) : 0;
+  const int64_t ob = abi_mul(partials, c.dim * 4), mb = abi_mul(partials, 8);
+  if (partials < 0 || ob < 0 || mb < 0 || ob > INT64_MAX - mb - 16) return GGUF_QK_ERR_LIMIT;
+  p->ml_bytes = (mb + 15) / 16 * 16;
+  p->bytes = p->ml_bytes + ob;
+  return GGUF_QK_OK;
+}
+
+template <int DIM>
+static void launch_join_rows(const AttnRowsArgs& a, int columns, int unit, dim3 grid, hipStream_t stream) {
+  hipLaunchKernelGGL(attn_join_rows_kernel<DIM>, grid, dim3(kJoinThreads), 0, stream, a, columns, unit);
+}
+
+}  // namespace gqk
+
+using namespace gqk;
+
+extern "C" {
+
+int64_t gguf_attn_extend_workspace(const gguf_kv_cache* cache, int32_t type, int64_t n_seqs, int64_t n_rows,
+                                   int64_t n_heads, int64_t max_len, int64_t window, int64_t sinks) {
+  KvView c;
+  int st = kv_view(cache, &c);
+  if (st) return st;
+  ExtendPlan p;
+  st = extend_plan(c, type, n_seqs, n_rows, n_heads, max_len, window, sinks, &p);
+  return st ? st : p.bytes;
+}
+
+int gguf_attn_extend(const gguf_kv_cache* cache, const void* q, int32_t type, int64_t q_stride, void* out,
+                     int64_t out_stride, const int32_t* row_start, int64_t n_rows, int64_t n_seqs, int64_t n_heads,
+                     const int32_t* page_table, int64_t table_stride, const int32_t* lengths, int64_t max_len,
+                     float scale, int64_t window, int64_t sinks, void* workspace, int64_t workspace_bytes,
+                     hipStream_t stream) {
+  AttnRowsArgs a;
+  int st = kv_view(cache, &a.c);
+  if (st) return st;
+  if (!q || !out || !page_table || !lengths) return GGUF_QK_ERR_NULL;
+  ExtendPlan p;
+  st = extend_plan(a.c, type, n_seqs, n_rows, n_heads, max_len, window, sinks, &p);
+  if (st) return st;
+  const int64_t row = n_heads * a.c.dim, es = type == GGUF_KV_TYPE_F32 ? 4 : 2;
+  const float qscale = scale * 1.44269504088896340736f;
+  if (table_stride < 1 || q_stride < row || out_stride < row || !(qscale - qscale == 0.f) ||
+      (!row_start && n_rows != n_seqs))
+    return GGUF_QK_ERR_SHAPE;
+  if (abi_mul(abi_mul(n_rows, q_stride), es) < 0 || abi_mul(abi_mul(n_rows, out_stride), es) < 0 ||
+      abi_mul(abi_mul(n_seqs, table_stride), 4) < 0)
+    return GGUF_QK_ERR_SHAPE;
+  if (!abi_aligned(q, 16) || !abi_aligned(out, 16) || q_stride * es % 16 || out_stride * es % 16 ||
+      !abi_aligned(page_table, 4) || !abi_aligned(lengths, 4) || !abi_aligned(row_start, 4) || !abi_aligned(workspace, 16))
+    return GGUF_QK_ERR_ALIGN;
+  if (n_seqs == 0 || n_rows == 0) return GGUF_QK_OK;
+  if (p.bytes > 0 && !workspace) return GGUF_QK_ERR_NULL;
+  if (workspace_bytes < p.bytes) return GGUF_QK_ERR_LIMIT;
+  const void* w = p.bytes > 0 ? workspace : nullptr;
+  const int64_t ob = ((n_rows - 1) * out_stride + row) * es;
+  const void* in[4] = {q, page_table, lengths, row_start};
+  const int64_t in_bytes[4] = {((n_rows - 1) * q_stride + row) * es, n_seqs * table_stride * 4, n_seqs * 4,
+                               (n_seqs + 1) * 4};
+  for (int i = 0; i < 4; ++i)
+    if (abi_overlap(out, ob, in[i], in_bytes[i]) || abi_overlap(w, p.bytes, in[i], in_bytes[i]))
+      return GGUF_QK_ERR_ALIAS;
+  if (kv_touches(a.c, out, ob) || abi_overlap(w, p.bytes, out, ob) || kv_touches(a.c, w, p.bytes))
+    return GGUF_QK_ERR_ALIAS;
+  st = abi_device();
+  if (st) return st;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.table = page_table;
+  a.lengths = lengths;
+  a.q = static_cast<const float*>(q);
+  a.out = static_cast<float*>(out);
+  a.part_ml = reinterpret_cast<float*>(ws);
+  a.part_o = reinterpret_cast<float*>(ws + p.ml_bytes);
+  a.scores = nullptr;
+  a.table_stride = table_stride;
+  a.q_stride = q_stride;
+  a.out_stride = out_stride;
+  a.max_len = max_len;
+  a.window = window;
+  a.score_stride = 0;
+  a.n_heads = (int32_t)n_heads;
+  a.group = p.group;
+  a.head_tiles = 0;
+  a.splits = p.splits;
+  a.chunk = p.chunk;
+  a.chunk_pages = 64;
+  a.qscale = qscale;
+  a.n_seqs = (int32_t)n_seqs;
+  a.share = 0.f;
+  a.row_start = row_start;
+  a.n_rows = n_rows;
+  a.sinks = (int32_t)sinks;
+  a.bf16 = type == GGUF_KV_TYPE_BF16;
+  const dim3 grid((unsigned)a.c.hkv, (unsigned)p.tiles, (unsigned)p.splits);
+  if (cache->type == GGUF_KV_TYPE_F16) launch_attn_rows_f16(a, grid, stream);
+  else if (cache->type == GGUF_KV_TYPE_BF16) launch_attn_rows_bf16(a, grid, stream);
+  else launch_attn_rows_q8_0(a, grid, stream);
+  st = abi_launched();
+  if (st || p.splits == 1) return st;
+  const dim3 jgrid((unsigned)n_rows, (unsigned)n_heads);   // rows <= 2^23: threads of a grid axis
+  switch (a.c.dim) {
+    case 64: launch_join_rows<64>(a, kFewColumns, p.unit, jgrid, stream); break;
+    case 96: launch_join_rows<96>(a, kFewColumns, p.unit, jgrid, stream); break;
+    case 128: launch_join_rows<128>(a, kFewColumns, p.unit, jgrid, stream); break;
+    case 192: launch_join_rows<192>(a, kFewColumns, p.unit, jgrid, stream); break;
+    default: launch_join_rows<256>(a, kFewColumns, p.unit, jgrid, stream); break;
+  }
+  return abi_launched();
+}
+
+}  // extern "C"

@@ -11,6 +11,11 @@ static void launch_dim(const AttnArgs& a, bool track, dim3 grid, hipStream_t str
     hipLaunchKernelGGL((attn_decode_kernel<GQK_KV_KIND, NB, false>), grid, dim3(kAttnThreads), 0, stream, a);
 }
 
+template <int NB>
+static void launch_dim(const AttnRowsArgs& a, dim3 grid, hipStream_t stream) {
+  hipLaunchKernelGGL((attn_decode_kernel<GQK_KV_KIND, NB, false, AttnRowsArgs>), grid, dim3(kAttnThreads), 0, stream, a);
+}
+
 #if GQK_KV_KIND == 0
 void launch_attn_f16(const AttnArgs& a, bool track, dim3 grid, hipStream_t stream) {
 #elif GQK_KV_KIND == 1
@@ -24,6 +29,22 @@ void launch_attn_q8_0(const AttnArgs& a, bool track, dim3 grid, hipStream_t stre
     case 128: return launch_dim<4>(a, track, grid, stream);
     case 192: return launch_dim<6>(a, track, grid, stream);
     default: return launch_dim<8>(a, track, grid, stream);
+  }
+}
+
+#if GQK_KV_KIND == 0
+void launch_attn_rows_f16(const AttnRowsArgs& a, dim3 grid, hipStream_t stream) {
+#elif GQK_KV_KIND == 1
+void launch_attn_rows_bf16(const AttnRowsArgs& a, dim3 grid, hipStream_t stream) {
+#else
+void launch_attn_rows_q8_0(const AttnRowsArgs& a, dim3 grid, hipStream_t stream) {
+#endif
+  switch (a.c.dim) {
+    case 64: return launch_dim<2>(a, grid, stream);
+    case 96: return launch_dim<3>(a, grid, stream);
+    case 128: return launch_dim<4>(a, grid, stream);
+    case 192: return launch_dim<6>(a, grid, stream);
+    default: return launch_dim<8>(a, grid, stream);
   }
 }
 
