@@ -74,6 +74,8 @@ UNITS = [
     ("logprobs.hip", [], "logprobs"),
     ("rope.hip", [], "rope"),
     ("attn_extend.hip", [], "attn_extend"),
+    ("attn_prompt_typed.hip", ["-DGQK_KV_KIND=0", *VGPR_FORM], "prompt_f16"),
+    ("attn_prompt_typed.hip", ["-DGQK_KV_KIND=1", *VGPR_FORM], "prompt_bf16"),
     ("verify.hip", [], "verify"),
 ]
 

@@ -3,6 +3,7 @@
 #include "../../include/gguf_tokens.h"
 #include "abi_check.hpp"
 #include "attn_launch.hpp"
+#include "attn_prompt_launch.hpp"
 
 namespace gqk {
 
@@ -10,9 +11,12 @@ constexpr int64_t kExtendMaxLen = int64_t(1) << 25;
 constexpr int64_t kExtendBlocks = 1024;   // blocks a call aims for
 constexpr int64_t kExtendChunk = 1024;    // longest chunk of positions of the few-rows kernel
 constexpr int kFewColumns = 16;           // columns of its tiles
+constexpr int64_t kPromptBlocks = 512;    // blocks that run at once
+constexpr int64_t kPromptLeast = 512;     // shortest chunk of the prompt kernel
 
 struct ExtendPlan {
-  int32_t group, splits, chunk, unit;
+  bool prompt;                // the kernel for many rows
+  int32_t group, splits, chunk, unit, columns;
   int64_t tiles;              // tiles of columns, at most
   int64_t ml_bytes, bytes;
 };
@@ -27,28 +31,39 @@ static int extend_plan(const KvView& c, int32_t type, int64_t n_seqs, int64_t n_
     return GGUF_QK_ERR_LIMIT;
   p->group = (int32_t)(n_heads / c.hkv);
   if (n_rows * p->group > INT32_MAX / 2) return GGUF_QK_ERR_LIMIT;
-  p->unit = c.ps > kAttnTile ? c.ps : kAttnTile;
-  p->tiles = (n_rows * p->group + n_seqs * (kFewColumns - 1)) / kFewColumns;
+  p->prompt = type == GGUF_KV_TYPE_BF16 && c.head_bytes == kv_head_bytes(false, c.dim, c.ps) &&
+              n_rows * p->group > 2 * kFewColumns * n_seqs;
+  p->columns = p->prompt ? kPromptColumns : kFewColumns;
+  const int tile = p->prompt ? prompt_slots(c.dim) : kAttnTile;
+  p->unit = c.ps > tile ? c.ps : tile;
+  p->tiles = (n_rows * p->group + n_seqs * (p->columns - 1)) / p->columns;
   if (p->tiles > 65535) return GGUF_QK_ERR_LIMIT;   // along a grid axis
   // positions that a tile's columns read, at most: the first slots, the window
   // and the tile's rows, in whole units
   int64_t span = max_len;
   if (window > 0 && window < max_len) {
     const int64_t pad = (sinks + p->unit - 1) / p->unit * p->unit;
-    const int64_t seen = pad + window + (kFewColumns - 1) / p->group + 1 + p->unit;
+    const int64_t seen = pad + window + (p->columns - 1) / p->group + 1 + p->unit;
     if (seen < span) span = seen;
   }
   if (span < 1) span = 1;
-  const int64_t round = kAttnTile * kAttnWaves;
-  int64_t most = int64_t(64) << c.shift;
-  if (most > kExtendChunk) most = kExtendChunk;
   const int64_t cells = p->tiles * c.hkv;
-  int64_t want = cells > 0 ? kExtendBlocks / cells : 1;
-  if (want < 1) want = 1;
-  int64_t chunk = ((span + want - 1) / want + round - 1) / round * round;
-  if (chunk < kAttnLeast) chunk = kAttnLeast;
-  if (span <= 4 * round) chunk = 4 * round;
-  if (chunk > most) chunk = most;
+  int64_t chunk;
+  if (p->prompt) {
+    const int64_t want = cells > 0 && cells < kPromptBlocks ? kPromptBlocks / cells : 1;
+    chunk = ((span + want - 1) / want + 63) / 64 * 64;
+    if (chunk < kPromptLeast) chunk = kPromptLeast;
+  } else {
+    const int64_t round = kAttnTile * kAttnWaves;
+    int64_t most = int64_t(64) << c.shift;
+    if (most > kExtendChunk) most = kExtendChunk;
+    int64_t want = cells > 0 ? kExtendBlocks / cells : 1;
+    if (want < 1) want = 1;
+    chunk = ((span + want - 1) / want + round - 1) / round * round;
+    if (chunk < kAttnLeast) chunk = kAttnLeast;
+    if (span <= 4 * round) chunk = 4 * round;
+    if (chunk > most) chunk = most;
+  }
   p->chunk = (int32_t)chunk;
   p->splits = (int32_t)((span + chunk - 1) / chunk);
   const int64_t partials = p->splits > 1 ? abi_mul(n_rows * n_heads, p->splits) : 0;
@@ -85,7 +100,7 @@ int gguf_attn_extend(const gguf_kv_cache* cache, const void* q, int32_t type, in
                      const int32_t* page_table, int64_t table_stride, const int32_t* lengths, int64_t max_len,
                      float scale, int64_t window, int64_t sinks, void* workspace, int64_t workspace_bytes,
                      hipStream_t stream) {
-  AttnRowsArgs a;
+  AttnPromptArgs a;
   int st = kv_view(cache, &a.c);
   if (st) return st;
   if (!q || !out || !page_table || !lengths) return GGUF_QK_ERR_NULL;
@@ -146,18 +161,22 @@ int gguf_attn_extend(const gguf_kv_cache* cache, const void* q, int32_t type, in
   a.sinks = (int32_t)sinks;
   a.bf16 = type == GGUF_KV_TYPE_BF16;
   const dim3 grid((unsigned)a.c.hkv, (unsigned)p.tiles, (unsigned)p.splits);
-  if (cache->type == GGUF_KV_TYPE_F16) launch_attn_rows_f16(a, grid, stream);
+  a.tiles = (int32_t)p.tiles;
+  if (p.prompt) {
+    if (cache->type == GGUF_KV_TYPE_F16) launch_prompt_f16(a, grid, stream);
+    else launch_prompt_bf16(a, grid, stream);
+  } else if (cache->type == GGUF_KV_TYPE_F16) launch_attn_rows_f16(a, grid, stream);
   else if (cache->type == GGUF_KV_TYPE_BF16) launch_attn_rows_bf16(a, grid, stream);
   else launch_attn_rows_q8_0(a, grid, stream);
   st = abi_launched();
   if (st || p.splits == 1) return st;
   const dim3 jgrid((unsigned)n_rows, (unsigned)n_heads);   // rows <= 2^23: threads of a grid axis
   switch (a.c.dim) {
-    case 64: launch_join_rows<64>(a, kFewColumns, p.unit, jgrid, stream); break;
-    case 96: launch_join_rows<96>(a, kFewColumns, p.unit, jgrid, stream); break;
-    case 128: launch_join_rows<128>(a, kFewColumns, p.unit, jgrid, stream); break;
-    case 192: launch_join_rows<192>(a, kFewColumns, p.unit, jgrid, stream); break;
-    default: launch_join_rows<256>(a, kFewColumns, p.unit, jgrid, stream); break;
+    case 64: launch_join_rows<64>(a, p.columns, p.unit, jgrid, stream); break;
+    case 96: launch_join_rows<96>(a, p.columns, p.unit, jgrid, stream); break;
+    case 128: launch_join_rows<128>(a, p.columns, p.unit, jgrid, stream); break;
+    case 192: launch_join_rows<192>(a, p.columns, p.unit, jgrid, stream); break;
+    default: launch_join_rows<256>(a, p.columns, p.unit, jgrid, stream); break;
   }
   return abi_launched();
 }

@@ -1,0 +1,13 @@
+// Between the entry points of the attention of several new tokens (attn_extend.hip)
+// and the kernels for many of them (attn_prompt_typed.hip, once per cache type).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "attn_prompt.hpp"
+
+namespace gqk {
+void launch_prompt_f16(const AttnPromptArgs& a, dim3 grid, hipStream_t stream);
+void launch_prompt_bf16(const AttnPromptArgs& a, dim3 grid, hipStream_t stream);
+void launch_prompt_q8_0(const AttnPromptArgs& a, dim3 grid, hipStream_t stream);
+}  // namespace gqk
