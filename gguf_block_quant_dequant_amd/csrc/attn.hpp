@@ -899,28 +899,64 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const AttnArgs 
     if (pos + j >= first && pos + j < n) w[j] = o[j] + acc[j];
 }
 
-// The same for several new tokens per sequence: block (row, query head), with the
-// splits of the row's tile of `columns` (row, query head) pairs.
+// The same for several new tokens per sequence: the splits of (row, query head), those
+// of the row's tile of `columns` such pairs. -1: the row belongs to no sequence.
+__device__ __forceinline__ int attn_row_splits(const AttnRowsArgs& a, int64_t row, int head, int columns, int unit) {
+  const SeqOf q = seq_of_row(a.row_start, a.n_seqs, a.n_rows, row);
+  if (q.seq < 0) return -1;
+  const int held = (int)kv_length(a.lengths[q.seq], a.max_len, a.table_stride, a.c.shift);
+  const int c = (int)(row - q.rows.row0) * a.group + head % a.group;
+  const TileRange r = tile_range(held, q.rows.rows, a.group, c / columns, columns, a.window, a.sinks, unit);
+  return r.n > 0 ? (r.n + a.chunk - 1) / a.chunk : 0;
+}
+__device__ __forceinline__ void attn_store_row(const AttnRowsArgs& a, int64_t at, const f32x4& x) {
+  if (a.bf16)
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at) =
+        make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+  else
+    *reinterpret_cast<f32x4*>(a.out + at) = x;
+}
+
+// A block per (row, query head).
 template <int DIM>
 __global__ __launch_bounds__(kJoinThreads) void attn_join_rows_kernel(const AttnRowsArgs a, int columns, int unit) {
   const int tid = threadIdx.x, lane = tid & 63, head = blockIdx.y;
   const int64_t row = blockIdx.x;
-  const RowTile t = find_row(a.row_start, a.n_seqs, a.n_rows, row, lane);
-  if (t.seq < 0) return;   // of no sequence
-  const int held = (int)kv_length(a.lengths[t.seq], a.max_len, a.table_stride, a.c.shift);
-  const int c = (int)(row - t.row0) * a.group + head % a.group;
-  const TileRange r = tile_range(held, t.rows, a.group, c / columns, columns, a.window, a.sinks, unit);
-  const int splits = r.n > 0 ? (r.n + a.chunk - 1) / a.chunk : 0;   // that wrote partials
+  const int splits = attn_row_splits(a, row, head, columns, unit);
+  if (splits < 0) return;
   f32x4 sum;
   bool store;
   attn_join_row<DIM>(a, row * a.n_heads + head, splits, tid, lane, &sum, &store);
-  if (!store) return;
-  const int64_t at = row * a.out_stride + (int64_t)head * DIM + tid * 4;
-  if (a.bf16)
-    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at) =
-        make_uint2(pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3]));
-  else
-    *reinterpret_cast<f32x4*>(a.out + at) = sum;
+  if (store) attn_store_row(a, row * a.out_stride + (int64_t)head * DIM + tid * 4, sum);
+}
+
+// Few splits of many rows: DIM / 4 lanes per (row, query head), several per block.
+constexpr int kJoinFew = 16;   // most splits
+template <int DIM>
+__global__ __launch_bounds__(kJoinThreads) void attn_join_few_kernel(const AttnRowsArgs a, int columns, int unit) {
+  constexpr int kLanes = DIM / 4, kItems = kJoinThreads / kLanes;
+  const int tid = threadIdx.x, c = tid % kLanes;
+  const int64_t item = (int64_t)blockIdx.x * kItems + tid / kLanes;
+  if (tid >= kItems * kLanes || item >= a.n_rows * a.n_heads) return;
+  const int64_t row = item / a.n_heads;
+  const int head = (int)(item - row * a.n_heads);
+  const int splits = attn_row_splits(a, row, head, columns, unit);
+  if (splits < 0) return;
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + item * a.splits;
+  const float* po = a.part_o + item * a.splits * DIM + c * 4;
+  float m = -__builtin_inff(), l = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < splits; ++i) m = fmaxf(m, ml[i].x);
+  const float base = m == -__builtin_inff() ? 0.f : m;
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int i = 0; i < splits; ++i) {
+    const float2 p = ml[i];
+    const float w = __builtin_amdgcn_exp2f(p.x - base);
+    l = fmaf(p.y, w, l);
+    sum += *reinterpret_cast<const f32x4*>(po + (int64_t)i * DIM) * w;
+  }
+  attn_store_row(a, row * a.out_stride + (int64_t)head * DIM + c * 4, sum * (l == 0.f ? 0.f : 1.0f / l));
 }
 
 }  // namespace gqk

@@ -34,7 +34,7 @@ static int extend_plan(const KvView& c, int32_t type, int64_t n_seqs, int64_t n_
   p->prompt = type == GGUF_KV_TYPE_BF16 && c.head_bytes == kv_head_bytes(false, c.dim, c.ps) &&
               n_rows * p->group > 2 * kFewColumns * n_seqs;
   p->columns = p->prompt ? kPromptColumns : kFewColumns;
-  const int tile = p->prompt ? prompt_slots(c.dim) : kAttnTile;
+  const int tile = p->prompt ? kPromptSlots : kAttnTile;
   p->unit = c.ps > tile ? c.ps : tile;
   p->tiles = (n_rows * p->group + n_seqs * (p->columns - 1)) / p->columns;
   if (p->tiles > 65535) return GGUF_QK_ERR_LIMIT;   // along a grid axis
@@ -75,8 +75,14 @@ static int extend_plan(const KvView& c, int32_t type, int64_t n_seqs, int64_t n_
 }
 
 template <int DIM>
-static void launch_join_rows(const AttnRowsArgs& a, int columns, int unit, dim3 grid, hipStream_t stream) {
-  hipLaunchKernelGGL(attn_join_rows_kernel<DIM>, grid, dim3(kJoinThreads), 0, stream, a, columns, unit);
+static void launch_join_rows(const AttnRowsArgs& a, int columns, int unit, hipStream_t stream) {
+  constexpr int kItems = kJoinThreads / (DIM / 4);
+  const int64_t items = a.n_rows * a.n_heads, blocks = (items + kItems - 1) / kItems;
+  if (a.splits <= kJoinFew && blocks <= INT32_MAX / kJoinThreads)
+    hipLaunchKernelGGL(attn_join_few_kernel<DIM>, dim3((unsigned)blocks), dim3(kJoinThreads), 0, stream, a, columns, unit);
+  else   // rows <= 2^23: threads of a grid axis
+    hipLaunchKernelGGL(attn_join_rows_kernel<DIM>, dim3((unsigned)a.n_rows, (unsigned)a.n_heads), dim3(kJoinThreads), 0,
+                       stream, a, columns, unit);
 }
 
 }  // namespace gqk
@@ -162,6 +168,7 @@ int gguf_attn_extend(const gguf_kv_cache* cache, const void* q, int32_t type, in
   a.bf16 = type == GGUF_KV_TYPE_BF16;
   const dim3 grid((unsigned)a.c.hkv, (unsigned)p.tiles, (unsigned)p.splits);
   a.tiles = (int32_t)p.tiles;
+  a.fold = p.prompt && p.splits == 1 && p.tiles * a.c.hkv <= kPromptBlocks && p.tiles * a.c.hkv > kPromptBlocks / 2 ? (int32_t)(kPromptBlocks / 2 / a.c.hkv) : 0;
   if (p.prompt) {
     if (cache->type == GGUF_KV_TYPE_F16) launch_prompt_f16(a, grid, stream);
     else launch_prompt_bf16(a, grid, stream);
@@ -170,13 +177,12 @@ int gguf_attn_extend(const gguf_kv_cache* cache, const void* q, int32_t type, in
   else launch_attn_rows_q8_0(a, grid, stream);
   st = abi_launched();
   if (st || p.splits == 1) return st;
-  const dim3 jgrid((unsigned)n_rows, (unsigned)n_heads);   // rows <= 2^23: threads of a grid axis
   switch (a.c.dim) {
-    case 64: launch_join_rows<64>(a, p.columns, p.unit, jgrid, stream); break;
-    case 96: launch_join_rows<96>(a, p.columns, p.unit, jgrid, stream); break;
-    case 128: launch_join_rows<128>(a, p.columns, p.unit, jgrid, stream); break;
-    case 192: launch_join_rows<192>(a, p.columns, p.unit, jgrid, stream); break;
-    default: launch_join_rows<256>(a, p.columns, p.unit, jgrid, stream); break;
+    case 64: launch_join_rows<64>(a, p.columns, p.unit, stream); break;
+    case 96: launch_join_rows<96>(a, p.columns, p.unit, stream); break;
+    case 128: launch_join_rows<128>(a, p.columns, p.unit, stream); break;
+    case 192: launch_join_rows<192>(a, p.columns, p.unit, stream); break;
+    default: launch_join_rows<256>(a, p.columns, p.unit, stream); break;
   }
   return abi_launched();
 }

@@ -20,14 +20,22 @@ namespace gqk {
 
 struct AttnPromptArgs : AttnRowsArgs {
   int32_t tiles;   // tiles of columns of the grid
+  int32_t fold;
 };
 
 constexpr int kPromptColumns = 128;
 constexpr int kPromptThreads = 256;
 constexpr int kPromptWaves = 4;
+#ifndef PB
+#define PB (NB <= 4 ? 2 : 1)
+#endif
 // The maximum that weights are relative to is raised only where one exceeds it by a
 // factor of 2^8: rescaling the output costs half as much as a tile's exponentials.
 constexpr float kPromptSlack = 8.0f;
+#ifndef AHEAD
+#define AHEAD 4
+#endif
+constexpr int kPromptAhead = AHEAD;
 
 typedef float f32x16v __attribute__((ext_vector_type(16)));
 
@@ -39,7 +47,7 @@ __device__ __forceinline__ f32x16v prompt_mfma(const uint4& a, const uint4& b, c
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-constexpr int prompt_slots(int dim) { return dim <= 128 ? 64 : 32; }   // of a tile
+constexpr int kPromptSlots = 64;   // of a tile
 
 // Slots of a tile, and where its values lie in LDS: rows of 16-byte chunks, a chunk at
 // chunk ^ swizzle(row), so that sixteen consecutive rows' chunks of one number lie in
@@ -47,7 +55,7 @@ constexpr int prompt_slots(int dim) { return dim <= 128 ? 64 : 32; }   // of a t
 template <int NB>
 struct PromptTile {
   static constexpr int kDim = NB * 32;
-  static constexpr int kSlots = prompt_slots(kDim);
+  static constexpr int kSlots = kPromptSlots;
   static constexpr int kKChunks = kDim / 8;    // of a slot's row of K
   static constexpr int kVChunks = kSlots / 8;  // of a dim's row of V
   static constexpr int kBytes = kSlots * kDim * 2;
@@ -73,17 +81,52 @@ __device__ __forceinline__ void prompt_load_lds(const uint8_t* p, uint32_t lds) 
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(lds) : "memory");
 }
 
+// 16 bytes of LDS.
+__device__ __forceinline__ uint4 prompt_lds16(uint32_t at) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4), aligned(16)));
+  const u32x4 v = *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>(at);
+  return make_uint4(v.x, v.y, v.z, v.w);
+}
+
+// N matrix instructions, their operands read from LDS `kPromptAhead` of them before, with
+// the chunks 0 .. CHUNKS - 1 of vector work spread between them, in this order: left to
+// itself the compiler puts each read right before its use and the vector work behind.
+template <int N, int CHUNKS, class Load, class Mma, class Work>
+__device__ __forceinline__ void prompt_phase(Load&& load, Mma&& mma, Work&& work) {
+  uint4 f[N];
+#pragma unroll
+  for (int i = 0; i < N && i < kPromptAhead; ++i) f[i] = load(i);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+#pragma unroll
+    for (int c = i * CHUNKS / N; c < (i + 1) * CHUNKS / N; ++c) work(c);
+    __builtin_amdgcn_sched_barrier(0);
+    mma(i, f[i]);
+    if (i + kPromptAhead < N) f[i + kPromptAhead] = load(i + kPromptAhead);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// The greater of a value and the other half wave's.
+__device__ __forceinline__ float prompt_half_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
 template <int KIND, int NB>
-__global__ __launch_bounds__(kPromptThreads, NB <= 6 ? 2 : 1) void attn_prompt_kernel(const AttnPromptArgs a) {
+__global__ __launch_bounds__(kPromptThreads, PB) void attn_prompt_kernel(const AttnPromptArgs a) {
   using Tile = PromptTile<NB>;
   constexpr int DIM = Tile::kDim, T = Tile::kSlots, KC = Tile::kKChunks, VC = Tile::kVChunks, LOADS = Tile::kLoads;
-  constexpr int KS = DIM / 16, NS = T / 32, NT = DIM / 32;   // steps of S, tiles of S, tiles of O
+  constexpr int KS = DIM / 16, NT = DIM / 32;   // steps of S, tiles of O
   constexpr int MM = KIND == kKvBF16 ? kKvBF16 : kKvF16;     // type of the products
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, hf = lane >> 5;
   const int h = blockIdx.x, split = blockIdx.z;
   // the last tiles of a sequence see most: they go first
-  const RowTile rt = find_row_tile(a.row_start, a.n_seqs, a.n_rows, a.group, kPromptColumns, a.tiles - 1 - (int)blockIdx.y, lane);
+  int target = a.tiles - 1 - (int)blockIdx.y;
+  if (a.fold && (int)blockIdx.y >= a.fold) target = (int)blockIdx.y - a.fold;
+  const RowTile rt = find_row_tile(a.row_start, a.n_seqs, a.n_rows, a.group, kPromptColumns, target, lane);
   if (rt.seq < 0) return;
   const int s = rt.seq;
   const int held = (int)kv_length(a.lengths[s], a.max_len, a.table_stride, a.c.shift);
@@ -112,8 +155,8 @@ __global__ __launch_bounds__(kPromptThreads, NB <= 6 ? 2 : 1) void attn_prompt_k
   const int w_hi = wr.n + wr.gap;   // slots from here on no column of this wave sees
 
   // K and V of two tiles
-  __shared__ __align__(1024) uint8_t lds[2][2][Tile::kBytes];
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&lds[0][0][0];
+  __shared__ __align__(1024) uint8_t lds[4][Tile::kBytes];   // K, K, V, V
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&lds[0][0];
 
   const uint8_t* const kh = a.c.k + (int64_t)h * a.c.head_bytes;
   const uint8_t* const vh = a.c.v + (int64_t)h * a.c.head_bytes;
@@ -137,50 +180,68 @@ __global__ __launch_bounds__(kPromptThreads, NB <= 6 ? 2 : 1) void attn_prompt_k
     while (v < end && real_of(v) >= a.sinks && real_of(v) + T <= r.near) v += T;
     return v;
   };
-  // Whole tile in one page: offsets within a page are the same for every tile.
+  // This lane's chunk of load i: slot of the tile and byte in the slot's row of K, or
+  // slot and dim of V.
+  auto k_chunk = [&](int i, int lane_, int& slot, int& at) {
+    const int L = (wave * LOADS + i) * 64 + lane_, r = L / KC;
+    slot = (r & ~31) | prompt_slot(r & 31);
+    at = ((L % KC) ^ Tile::k_swizzle(r)) * 16;
+  };
+  auto v_chunk = [&](int i, int lane_, int& slot, int& dim) {
+    const int L = (wave * LOADS + i) * 64 + lane_;
+    dim = L / VC;
+    slot = ((L % VC) ^ Tile::v_swizzle(dim)) * 8;
+  };
+  // Where a tile lies in one page, offsets are the same for every tile.
   const bool whole = a.c.ps >= T;
-  uint32_t k_at[LOADS], v_at[LOADS];   // this lane's chunks: offset in the page's head, from the tile's slot on
-  int k_slot[LOADS], v_slot[LOADS];    // and the slot in the tile
+  uint32_t k_at[LOADS], v_at[LOADS];
 #pragma unroll
   for (int i = 0; i < LOADS; ++i) {
-    const int L = (wave * LOADS + i) * 64 + lane;
-    const int kr = L / KC, kc = (L % KC) ^ Tile::k_swizzle(kr);
-    k_slot[i] = (kr & ~31) | prompt_slot(kr & 31);
-    k_at[i] = kc * 16;
-    const int vr = L / VC, vc = (L % VC) ^ Tile::v_swizzle(vr);
-    v_slot[i] = vc * 8;
-    v_at[i] = vr * a.c.ps * 2;
+    int slot, at;
+    k_chunk(i, lane, slot, at);
+    k_at[i] = slot * (DIM * 2) + at;
+    v_chunk(i, lane, slot, at);
+    v_at[i] = (at * a.c.ps + slot) * 2;
   }
-  auto issue = [&](int v0, int buf) {
-    if (((v0 + T - 1) >> shift) - page0 >= 64) fetch_pages(v0 >> shift);
-    const uint32_t to = lds0 + buf * 2 * Tile::kBytes + wave * LOADS * 1024;
+  // Sixteen bytes per lane of K or V of the tile at v0.
+  auto issue_k = [&](int v0, int buf) {
+    const uint32_t to = lds0 + buf * Tile::kBytes + wave * LOADS * 1024;
     if (whole) {
       const int id = __builtin_amdgcn_readlane(pid, (v0 >> shift) - page0);
-      const int64_t page = (id < 0 ? 0 : id) * page_bytes;
-      const uint8_t* kb = kh + page + (v0 & smask) * (DIM * 2);
-      const uint8_t* vb = vh + page + (v0 & smask) * 2;
+      const uint8_t* from = kh + (id < 0 ? 0 : id) * page_bytes + (v0 & smask) * (DIM * 2);
 #pragma unroll
-      for (int i = 0; i < LOADS; ++i) prompt_load_lds(kb, k_at[i] + k_slot[i] * (DIM * 2), to + i * 1024);
-#pragma unroll
-      for (int i = 0; i < LOADS; ++i) prompt_load_lds(vb, v_at[i] + v_slot[i] * 2, to + Tile::kBytes + i * 1024);
+      for (int i = 0; i < LOADS; ++i) prompt_load_lds(from, k_at[i], to + i * 1024);
     } else {
 #pragma unroll
       for (int i = 0; i < LOADS; ++i) {
-        const int p = v0 + k_slot[i], id = __shfl(pid, (p >> shift) - page0);
-        prompt_load_lds(kh + (id < 0 ? 0 : id) * page_bytes + (p & smask) * (DIM * 2) + k_at[i], to + i * 1024);
+        int slot, at;
+        k_chunk(i, (int)opaque(lane), slot, at);   // not kept in registers
+        const int p = v0 + slot, id = __shfl(pid, (p >> shift) - page0);
+        prompt_load_lds(kh + (id < 0 ? 0 : id) * page_bytes + (p & smask) * (DIM * 2) + at, to + i * 1024);
       }
+    }
+  };
+  auto issue_v = [&](int v0, int buf) {
+    const uint32_t to = lds0 + (2 + buf) * Tile::kBytes + wave * LOADS * 1024;
+    if (whole) {
+      const int id = __builtin_amdgcn_readlane(pid, (v0 >> shift) - page0);
+      const uint8_t* from = vh + (id < 0 ? 0 : id) * page_bytes + (v0 & smask) * 2;
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) prompt_load_lds(from, v_at[i], to + i * 1024);
+    } else {
 #pragma unroll
       for (int i = 0; i < LOADS; ++i) {
-        const int p = v0 + v_slot[i], id = __shfl(pid, (p >> shift) - page0);
-        prompt_load_lds(vh + (id < 0 ? 0 : id) * page_bytes + (p & smask) * 2 + v_at[i], to + Tile::kBytes + i * 1024);
+        int slot, dim;
+        v_chunk(i, (int)opaque(lane), slot, dim);
+        const int p = v0 + slot, id = __shfl(pid, (p >> shift) - page0);
+        prompt_load_lds(vh + (id < 0 ? 0 : id) * page_bytes + (dim * a.c.ps + (p & smask)) * 2, to + i * 1024);
       }
     }
   };
   // Slots of a tile whose values are looked at.
   auto present = [&](int v0) -> uint64_t {
     const int n = end - v0;
-    uint64_t m = n >= 64 ? ~0ull : (1ull << n) - 1;
-    if (T < 64) m &= (1ull << (T & 63)) - 1;
+    uint64_t m = n >= T ? ~0ull : (1ull << n) - 1;
     for (int p = v0; p < v0 + T && p < end; p += a.c.ps) {
       const int id = __builtin_amdgcn_readlane(pid, (p >> shift) - page0);
       if (id < 0) m &= whole ? 0 : ~(((1ull << a.c.ps) - 1) << (p - v0));
@@ -188,9 +249,12 @@ __global__ __launch_bounds__(kPromptThreads, NB <= 6 ? 2 : 1) void attn_prompt_k
     return m;
   };
 
-  fetch_pages(begin >> shift);
   int v0 = seen_from(begin);
-  if (v0 < end) issue(v0, 0);
+  fetch_pages(v0 >> shift);
+  if (v0 < end) {
+    issue_k(v0, 0);
+    issue_v(v0, 0);
+  }
 
   // q of this lane's column: the B operand, dims 16 k + 8 hf .. + 7
   uint4 q[KS];
@@ -240,93 +304,123 @@ __global__ __launch_bounds__(kPromptThreads, NB <= 6 ? 2 : 1) void attn_prompt_k
   // Offsets of this lane's operands in LDS: K's row of 32, V's row of 32.
   uint32_t k_off[KS], v_off[T / 16];
 #pragma unroll
-  for (int k = 0; k < KS; ++k) k_off[k] = col * (DIM * 2) + (((2 * k + hf) ^ Tile::k_swizzle(col)) * 16);
+  for (int k = 0; k < KS; ++k) k_off[k] = lds0 + col * (DIM * 2) + (((2 * k + hf) ^ Tile::k_swizzle(col)) * 16);
 #pragma unroll
-  for (int k = 0; k < T / 16; ++k) v_off[k] = col * (T * 2) + (((2 * k + hf) ^ Tile::v_swizzle(col)) * 16);
+  for (int k = 0; k < T / 16; ++k) v_off[k] = lds0 + 2 * Tile::kBytes + col * (T * 2) + (((2 * k + hf) ^ Tile::v_swizzle(col)) * 16);
 
   f32x16v o[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) o[t] = f32x16v{};
   float m = -__builtin_inff(), l = 0.f;
 
-  for (int buf = 0; v0 < end; buf ^= 1) {
+  // What a column does not see of the 32 slots from `real` on.
+  auto mask = [&](f32x16v& sc, int real, uint32_t here) {
+    const uint32_t bits = slot_bits(range, a.sinks, real) & here;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (!(bits >> ((i & 8) * 2 + 8 * hf + (i & 7)) & 1)) sc[i] = -__builtin_inff();
+  };
+  // The softmax of 32 slots in ten chunks: the maximum; whether it is raised, and the
+  // factor alpha that the sums so far then take; eight pairs of weights.
+  float mx, base, alpha;
+  bool raise;
+  uint32_t w[8];
+  auto soften = [&](const f32x16v& sc, int chunk) {
+    if (chunk == 0) {
+      mx = sc[0];
+#pragma unroll
+      for (int i = 1; i < 16; ++i) mx = fmaxf(mx, sc[i]);
+    } else if (chunk == 1) {
+      mx = prompt_half_max(mx) * factor;
+      raise = __any(mx > m + kPromptSlack);
+      const float old = m;
+      m = raise ? fmaxf(m, mx) : m;
+      base = m == -__builtin_inff() ? 0.f : m;   // nothing seen yet
+      alpha = __builtin_amdgcn_exp2f(old - base);
+      l *= alpha;
+    } else {
+      const int j = chunk - 2;
+      const float x = __builtin_amdgcn_exp2f(fmaf(sc[2 * j], factor, -base));
+      const float y = __builtin_amdgcn_exp2f(fmaf(sc[2 * j + 1], factor, -base));
+      l += x + y;
+      w[j] = MM == kKvBF16 ? pack_bf16x2(x, y) : __builtin_bit_cast(uint32_t, to_f16x2(x, y));
+    }
+  };
+  auto weights = [&](uint4 (&p)[2]) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      p[t] = make_uint4(w[4 * t], w[4 * t + 1], w[4 * t + 2], w[4 * t + 3]);
+      asm volatile("" : "+v"(p[t].x), "+v"(p[t].y), "+v"(p[t].z), "+v"(p[t].w));   // computed here, not where it is used
+    }
+  };
+  // Scores of 32 slots, K's rows `at` bytes behind the first buffer's, beside chunks of work.
+  auto scores = [&](uint32_t at, f32x16v& sc, auto chunks, auto&& work) {
+    sc = f32x16v{};
+    prompt_phase<KS, decltype(chunks)::value>([&](int i) { return prompt_lds16(k_off[i] + at); },
+                                              [&](int i, const uint4& f) { sc = prompt_mfma<MM>(f, q[i], sc); }, work);
+  };
+  // Weights times V of 32 slots.
+  auto weigh = [&](uint32_t at, int n, const uint4 (&p)[2], auto chunks, auto&& work) {
+    prompt_phase<2 * NT, decltype(chunks)::value>(
+        [&](int i) { return prompt_lds16(v_off[2 * n + i / NT] + at + i % NT * 32 * T * 2); },
+        [&](int i, const uint4& f) { o[i % NT] = prompt_mfma<MM>(f, p[i / NT], o[i % NT]); }, work);
+  };
+  auto rescale = [&]() {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) o[t] *= alpha;
+  };
+
+  // One tile, in buffer BUF.
+  auto step = [&](auto buffer) {
+    constexpr int BUF = decltype(buffer)::value;
+    constexpr uint32_t kt = BUF * Tile::kBytes, vt = BUF * Tile::kBytes;
     // this tile's loads have arrived, everyone's; the other buffer is free
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    const int real0 = real_of(v0);
     const uint64_t here = present(v0);
-    const int next = seen_from(v0 + T);
-    if (next < end) issue(next, buf ^ 1);
-    const bool whole_tile = here == (T < 64 ? (1ull << (T & 63)) - 1 : ~0ull);
-    uint8_t* const kt = lds[buf][0];
-    uint8_t* const vt = lds[buf][1];
-    if (!whole_tile) {
+    const int real0 = real_of(v0), next = seen_from(v0 + T);
+    if (next < end) {
+      if (((next + T - 1) >> shift) - page0 >= 64) fetch_pages(next >> shift);
+      issue_k(next, BUF ^ 1);
+      issue_v(next, BUF ^ 1);
+    }
+    if (here != ~0ull) {
       // V behind the end may hold anything: zero
       for (int i = tid; i < DIM * VC; i += kPromptThreads) {
         const int vr = i / VC, vc = (i % VC) ^ Tile::v_swizzle(vr);
         const uint32_t bits = (uint32_t)(here >> (8 * vc)) & 0xFFu;
         if (bits == 0xFFu) continue;
-        uint16_t* p = reinterpret_cast<uint16_t*>(vt + i * 16);
+        uint16_t* p = reinterpret_cast<uint16_t*>(lds[2 + BUF] + i * 16);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           if (!(bits >> j & 1)) p[j] = 0;
       }
       __syncthreads();
     }
-    const bool none = idle || real0 >= w_hi || (real0 >= a.sinks && real0 + T <= wr.near);
-    if (!none) {
-      f32x16v sc[NS];
-#pragma unroll
-      for (int n = 0; n < NS; ++n) {
-        sc[n] = f32x16v{};
-#pragma unroll
-        for (int k = 0; k < KS; ++k) sc[n] = prompt_mfma<MM>(load16(kt + n * 32 * DIM * 2 + k_off[k]), q[k], sc[n]);
-      }
-      if (!(whole_tile && real0 >= wr.far && real0 + T <= wr.full)) {
-#pragma unroll
-        for (int n = 0; n < NS; ++n) {
-          const uint32_t bits = slot_bits(range, a.sinks, real0 + 32 * n) & (uint32_t)(here >> (32 * n));
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (!(bits >> ((i & 8) * 2 + 8 * hf + (i & 7)) & 1)) sc[n][i] = -__builtin_inff();
-        }
-      }
-      float mx = sc[0][0];
-#pragma unroll
-      for (int n = 0; n < NS; ++n)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, sc[n][i]);
-      mx = fmaxf(mx, __shfl_xor(mx, 32)) * factor;
-      if (__any(mx > m + kPromptSlack)) {
-        const float mn = fmaxf(m, mx);
-        const float alpha = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
-        m = mn;
-        l *= alpha;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) o[t] *= alpha;
-      }
-      const float base = m == -__builtin_inff() ? 0.f : m;   // nothing seen yet
-      uint4 p[T / 16];
-#pragma unroll
-      for (int n = 0; n < NS; ++n)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          uint32_t w[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float x = __builtin_amdgcn_exp2f(fmaf(sc[n][8 * t + 2 * j], factor, -base));
-            const float y = __builtin_amdgcn_exp2f(fmaf(sc[n][8 * t + 2 * j + 1], factor, -base));
-            l += x + y;
-            w[j] = MM == kKvBF16 ? pack_bf16x2(x, y) : __builtin_bit_cast(uint32_t, to_f16x2(x, y));
-          }
-          p[2 * n + t] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-#pragma unroll
-      for (int k = 0; k < T / 16; ++k)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) o[t] = prompt_mfma<MM>(load16(vt + t * 32 * T * 2 + v_off[k]), p[k], o[t]);
-    }
     v0 = next;
+    if (idle || real0 >= w_hi || (real0 >= a.sinks && real0 + T <= wr.near)) return;
+    using None = std::integral_constant<int, 0>;
+    using Softmax = std::integral_constant<int, 10>;
+    const auto idle_work = [](int) {};
+    uint4 p[2];
+    f32x16v sa, sb;
+    const bool edge = here != ~0ull || real0 < wr.far || real0 + T > wr.full;
+    // matrix and vector units side by side, by halves of the tile
+    scores(kt, sa, None{}, idle_work);
+    if (edge) mask(sa, real0, (uint32_t)here);
+    scores(kt + 32 * DIM * 2, sb, Softmax{}, [&](int c) { soften(sa, c); });
+    weights(p);
+    if (raise) rescale();
+    if (edge) mask(sb, real0 + 32, (uint32_t)(here >> 32));
+    weigh(vt, 0, p, Softmax{}, [&](int c) { soften(sb, c); });
+    weights(p);
+    if (raise) rescale();
+    weigh(vt, 1, p, None{}, idle_work);
+  };
+  while (v0 < end) {
+    step(std::integral_constant<int, 0>{});
+    if (v0 >= end) break;
+    step(std::integral_constant<int, 1>{});
   }
 
   l += __shfl_xor(l, 32);

@@ -63,6 +63,23 @@ GQK_HD TileRange tile_range(int32_t held, int32_t rows, int32_t group, int32_t t
   return r;
 }
 
+// The sequence that holds row `row` (seq -1: none), of ascending row_start.
+struct SeqOf {
+  int32_t seq;
+  SeqRows rows;
+};
+GQK_HD SeqOf seq_of_row(const int32_t* row_start, int32_t n_seqs, int64_t n_rows, int64_t row) {
+  if (!row_start) return {(int32_t)row, {(int32_t)row, 1}};
+  int32_t lo = 0, hi = n_seqs;   // the last of 0 .. n_seqs - 1 that starts at or before the row
+  while (hi - lo > 1) {
+    const int32_t mid = lo + (hi - lo) / 2;
+    if (row_start[mid] <= row) lo = mid;
+    else hi = mid;
+  }
+  const SeqRows r = seq_rows(row_start, lo, n_rows);
+  return row >= r.row0 && row < (int64_t)r.row0 + r.rows ? SeqOf{lo, r} : SeqOf{-1, {0, 0}};
+}
+
 #if defined(__HIP__)
 // Tile `target` of the tiles of `columns` (row, query head) pairs that all
 // sequences' rows make, in order; seq -1 behind the last. All 64 lanes of a wave
