@@ -20,22 +20,15 @@ namespace gqk {
 
 struct AttnPromptArgs : AttnRowsArgs {
   int32_t tiles;   // tiles of columns of the grid
-  int32_t fold;
 };
 
 constexpr int kPromptColumns = 128;
-constexpr int kPromptThreads = 256;
-constexpr int kPromptWaves = 4;
-#ifndef PB
-#define PB (NB <= 4 ? 2 : 1)
-#endif
+constexpr int kPromptWaves = 4;     // that share a tile of slots
+constexpr int kPromptThreads = kPromptWaves * 64;
 // The maximum that weights are relative to is raised only where one exceeds it by a
 // factor of 2^8: rescaling the output costs half as much as a tile's exponentials.
 constexpr float kPromptSlack = 8.0f;
-#ifndef AHEAD
-#define AHEAD 4
-#endif
-constexpr int kPromptAhead = AHEAD;
+constexpr int kPromptAhead = 4;   // reads of LDS before their matrix instruction
 
 typedef float f32x16v __attribute__((ext_vector_type(16)));
 
@@ -114,19 +107,20 @@ __device__ __forceinline__ float prompt_half_max(float x) {
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
-template <int KIND, int NB>
-__global__ __launch_bounds__(kPromptThreads, PB) void attn_prompt_kernel(const AttnPromptArgs a) {
+// GROUPS of four waves take the tiles of slots in turn and join in LDS.
+template <int KIND, int NB, int GROUPS>
+__global__ __launch_bounds__(kPromptThreads * GROUPS, NB <= 4 ? 2 : 1) void attn_prompt_kernel(const AttnPromptArgs a) {
   using Tile = PromptTile<NB>;
   constexpr int DIM = Tile::kDim, T = Tile::kSlots, KC = Tile::kKChunks, VC = Tile::kVChunks, LOADS = Tile::kLoads;
   constexpr int KS = DIM / 16, NT = DIM / 32;   // steps of S, tiles of O
   constexpr int MM = KIND == kKvBF16 ? kKvBF16 : kKvF16;     // type of the products
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int group = GROUPS == 1 ? 0 : __builtin_amdgcn_readfirstlane(tid / kPromptThreads);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) % kPromptWaves;   // of the group
   const int col = lane & 31, hf = lane >> 5;
   const int h = blockIdx.x, split = blockIdx.z;
   // the last tiles of a sequence see most: they go first
-  int target = a.tiles - 1 - (int)blockIdx.y;
-  if (a.fold && (int)blockIdx.y >= a.fold) target = (int)blockIdx.y - a.fold;
-  const RowTile rt = find_row_tile(a.row_start, a.n_seqs, a.n_rows, a.group, kPromptColumns, target, lane);
+  const RowTile rt = find_row_tile(a.row_start, a.n_seqs, a.n_rows, a.group, kPromptColumns, a.tiles - 1 - (int)blockIdx.y, lane);
   if (rt.seq < 0) return;
   const int s = rt.seq;
   const int held = (int)kv_length(a.lengths[s], a.max_len, a.table_stride, a.c.shift);
@@ -141,7 +135,7 @@ __global__ __launch_bounds__(kPromptThreads, PB) void attn_prompt_kernel(const A
   const int head = h * a.group + cc % a.group;
   uint16_t* const out = reinterpret_cast<uint16_t*>(a.out) + row * a.out_stride + (int64_t)head * DIM;
   if (begin >= r.n) {
-    if (a.splits == 1 && live) {   // nothing seen
+    if (a.splits == 1 && live && group == 0) {   // nothing seen
 #pragma unroll
       for (int i = 0; i < DIM / 8; ++i)
         if ((i & 1) == hf) *reinterpret_cast<uint4*>(out + 8 * i) = make_uint4(0, 0, 0, 0);
@@ -154,9 +148,9 @@ __global__ __launch_bounds__(kPromptThreads, PB) void attn_prompt_kernel(const A
                                   a.window, a.sinks, unit);
   const int w_hi = wr.n + wr.gap;   // slots from here on no column of this wave sees
 
-  // K and V of two tiles
-  __shared__ __align__(1024) uint8_t lds[4][Tile::kBytes];   // K, K, V, V
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&lds[0][0];
+  // K and V of two tiles of each group: K, K, V, V
+  __shared__ __align__(1024) uint8_t lds[GROUPS][4][Tile::kBytes];
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&lds[group][0][0];
 
   const uint8_t* const kh = a.c.k + (int64_t)h * a.c.head_bytes;
   const uint8_t* const vh = a.c.v + (int64_t)h * a.c.head_bytes;
@@ -180,62 +174,43 @@ __global__ __launch_bounds__(kPromptThreads, PB) void attn_prompt_kernel(const A
     while (v < end && real_of(v) >= a.sinks && real_of(v) + T <= r.near) v += T;
     return v;
   };
-  // This lane's chunk of load i: slot of the tile and byte in the slot's row of K, or
-  // slot and dim of V.
-  auto k_chunk = [&](int i, int lane_, int& slot, int& at) {
-    const int L = (wave * LOADS + i) * 64 + lane_, r = L / KC;
-    slot = (r & ~31) | prompt_slot(r & 31);
-    at = ((L % KC) ^ Tile::k_swizzle(r)) * 16;
-  };
-  auto v_chunk = [&](int i, int lane_, int& slot, int& dim) {
-    const int L = (wave * LOADS + i) * 64 + lane_;
-    dim = L / VC;
-    slot = ((L % VC) ^ Tile::v_swizzle(dim)) * 8;
-  };
-  // Where a tile lies in one page, offsets are the same for every tile.
+  // This lane's chunk of load i. Of K a wave loads sixteen slots, which lie in one
+  // page; of V whole rows of dims, whose chunks of eight slots lie in up to four pages,
+  // of two patterns over the lanes that loads take in turn (v_swizzle).
+  uint32_t k_at[LOADS], v_at[LOADS];   // offset in the page's head, of V without the slot where pages are small
   const bool whole = a.c.ps >= T;
-  uint32_t k_at[LOADS], v_at[LOADS];
 #pragma unroll
   for (int i = 0; i < LOADS; ++i) {
-    int slot, at;
-    k_chunk(i, lane, slot, at);
-    k_at[i] = slot * (DIM * 2) + at;
-    v_chunk(i, lane, slot, at);
-    v_at[i] = (at * a.c.ps + slot) * 2;
+    const int L = (wave * LOADS + i) * 64 + lane;
+    const int kr = L / KC, vr = L / VC;
+    const int slot = (kr & ~31) | prompt_slot(kr & 31);
+    k_at[i] = (slot - 16 * wave) * (DIM * 2) + ((L % KC) ^ Tile::k_swizzle(kr)) * 16;
+    v_at[i] = (vr * a.c.ps + (whole ? ((L % VC) ^ Tile::v_swizzle(vr)) * 8 : 0)) * 2;
   }
-  // Sixteen bytes per lane of K or V of the tile at v0.
-  auto issue_k = [&](int v0, int buf) {
-    const uint32_t to = lds0 + buf * Tile::kBytes + wave * LOADS * 1024;
-    if (whole) {
-      const int id = __builtin_amdgcn_readlane(pid, (v0 >> shift) - page0);
-      const uint8_t* from = kh + (id < 0 ? 0 : id) * page_bytes + (v0 & smask) * (DIM * 2);
-#pragma unroll
-      for (int i = 0; i < LOADS; ++i) prompt_load_lds(from, k_at[i], to + i * 1024);
-    } else {
-#pragma unroll
-      for (int i = 0; i < LOADS; ++i) {
-        int slot, at;
-        k_chunk(i, (int)opaque(lane), slot, at);   // not kept in registers
-        const int p = v0 + slot, id = __shfl(pid, (p >> shift) - page0);
-        prompt_load_lds(kh + (id < 0 ? 0 : id) * page_bytes + (p & smask) * (DIM * 2) + at, to + i * 1024);
-      }
-    }
+  auto page_at = [&](int v) {   // of uniform slot v
+    const int id = __builtin_amdgcn_readlane(pid, (v >> shift) - page0);
+    return (id < 0 ? 0 : id) * page_bytes;
   };
-  auto issue_v = [&](int v0, int buf) {
-    const uint32_t to = lds0 + (2 + buf) * Tile::kBytes + wave * LOADS * 1024;
+  auto issue = [&](int v, int buf) {
+    const uint32_t to = lds0 + buf * Tile::kBytes + wave * LOADS * 1024;
+    const int vk = v + 16 * wave;
+    const uint8_t* from = kh + page_at(vk) + (vk & smask) * (DIM * 2);
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) prompt_load_lds(from, k_at[i], to + i * 1024);
     if (whole) {
-      const int id = __builtin_amdgcn_readlane(pid, (v0 >> shift) - page0);
-      const uint8_t* from = vh + (id < 0 ? 0 : id) * page_bytes + (v0 & smask) * 2;
+      from = vh + page_at(v) + (v & smask) * 2;
 #pragma unroll
-      for (int i = 0; i < LOADS; ++i) prompt_load_lds(from, v_at[i], to + i * 1024);
+      for (int i = 0; i < LOADS; ++i) prompt_load_lds(from, v_at[i], to + 2 * Tile::kBytes + i * 1024);
     } else {
+      const uint8_t* of[2];
 #pragma unroll
-      for (int i = 0; i < LOADS; ++i) {
-        int slot, dim;
-        v_chunk(i, (int)opaque(lane), slot, dim);
-        const int p = v0 + slot, id = __shfl(pid, (p >> shift) - page0);
-        prompt_load_lds(vh + (id < 0 ? 0 : id) * page_bytes + (dim * a.c.ps + (p & smask)) * 2, to + i * 1024);
+      for (int j = 0; j < 2; ++j) {
+        const int p = v + ((lane % VC) ^ Tile::v_swizzle(j * 8 + lane / VC)) * 8, id = __shfl(pid, (p >> shift) - page0);
+        of[j] = vh + (id < 0 ? 0 : id) * page_bytes + (p & smask) * 2;
       }
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i)
+        prompt_load_lds(of[(wave * LOADS + i) & 1] + v_at[i], to + 2 * Tile::kBytes + i * 1024);
     }
   };
   // Slots of a tile whose values are looked at.
@@ -249,12 +224,14 @@ __global__ __launch_bounds__(kPromptThreads, PB) void attn_prompt_kernel(const A
     return m;
   };
 
-  int v0 = seen_from(begin);
-  fetch_pages(v0 >> shift);
-  if (v0 < end) {
-    issue_k(v0, 0);
-    issue_v(v0, 0);
-  }
+  // the group's tile and the one behind its next; all groups count alike
+  int first = seen_from(begin);
+  auto mine = [&](int v) {
+    for (int g = 0; g < group; ++g) v = seen_from(v + T);
+    return v;
+  };
+  fetch_pages(first >> shift);
+  if (mine(first) < end) issue(mine(first), 0);
 
   // q of this lane's column: the B operand, dims 16 k + 8 hf .. + 7
   uint4 q[KS];
@@ -374,31 +351,32 @@ __global__ __launch_bounds__(kPromptThreads, PB) void attn_prompt_kernel(const A
   auto step = [&](auto buffer) {
     constexpr int BUF = decltype(buffer)::value;
     constexpr uint32_t kt = BUF * Tile::kBytes, vt = BUF * Tile::kBytes;
-    // this tile's loads have arrived, everyone's; the other buffer is free
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    const uint64_t here = present(v0);
-    const int real0 = real_of(v0), next = seen_from(v0 + T);
-    if (next < end) {
-      if (((next + T - 1) >> shift) - page0 >= 64) fetch_pages(next >> shift);
-      issue_k(next, BUF ^ 1);
-      issue_v(next, BUF ^ 1);
-    }
-    if (here != ~0ull) {
-      // V behind the end may hold anything: zero
-      for (int i = tid; i < DIM * VC; i += kPromptThreads) {
-        const int vr = i / VC, vc = (i % VC) ^ Tile::v_swizzle(vr);
-        const uint32_t bits = (uint32_t)(here >> (8 * vc)) & 0xFFu;
-        if (bits == 0xFFu) continue;
-        uint16_t* p = reinterpret_cast<uint16_t*>(lds[2 + BUF] + i * 16);
+    const int v0 = mine(first), real0 = real_of(v0);
+    const bool any = v0 < end;
+    const uint64_t here = any ? present(v0) : 0;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this tile's loads have arrived
+    if (any && here != ~0ull) {
+      // V behind the end may hold anything: zero, each wave what it has loaded
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) {
+        const int L = (wave * LOADS + i) * 64 + lane;
+        const uint32_t bits = (uint32_t)(here >> (8 * ((L % VC) ^ Tile::v_swizzle(L / VC)))) & 0xFFu;
+        uint16_t* p = reinterpret_cast<uint16_t*>(lds[group][2 + BUF] + L * 16);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           if (!(bits >> j & 1)) p[j] = 0;
       }
-      __syncthreads();
     }
-    v0 = next;
-    if (idle || real0 >= w_hi || (real0 >= a.sinks && real0 + T <= wr.near)) return;
+    __syncthreads();   // everyone's have, and the other buffer is free
+    int next = first;
+    for (int g = 0; g < GROUPS; ++g) next = seen_from(next + T);
+    first = next;
+    const int v1 = mine(next);
+    if (v1 < end) {
+      if (((v1 + T - 1) >> shift) - page0 >= 64) fetch_pages(v1 >> shift);
+      issue(v1, BUF ^ 1);
+    }
+    if (!any || idle || real0 >= w_hi || (real0 >= a.sinks && real0 + T <= wr.near)) return;
     using None = std::integral_constant<int, 0>;
     using Softmax = std::integral_constant<int, 10>;
     const auto idle_work = [](int) {};
@@ -417,13 +395,42 @@ __global__ __launch_bounds__(kPromptThreads, PB) void attn_prompt_kernel(const A
     if (raise) rescale();
     weigh(vt, 1, p, None{}, idle_work);
   };
-  while (v0 < end) {
+  while (first < end) {
     step(std::integral_constant<int, 0>{});
-    if (v0 >= end) break;
+    if (first >= end) break;
     step(std::integral_constant<int, 1>{});
   }
 
   l += __shfl_xor(l, 32);
+  if constexpr (GROUPS == 2) {
+    // the second group's sums go to the first's waves, lane by lane
+    static_assert(kPromptThreads * NT * 64 + kPromptThreads * 8 <= sizeof(lds), "sums fit");
+    f32x4* const os = reinterpret_cast<f32x4*>(&lds[0][0][0]) + wave * NT * 4 * 64 + lane;
+    float2* const ms = reinterpret_cast<float2*>(&lds[0][0][0] + kPromptThreads * NT * 64) + wave * 64 + lane;
+    __syncthreads();
+    if (group == 1) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) os[(t * 4 + i) * 64] = f32x4{o[t][4 * i], o[t][4 * i + 1], o[t][4 * i + 2], o[t][4 * i + 3]};
+      *ms = make_float2(m, l);
+    }
+    __syncthreads();
+    if (group == 1) return;
+    const float2 other = *ms;
+    const float top = fmaxf(m, other.x), from = top == -__builtin_inff() ? 0.f : top;
+    const float f0 = __builtin_amdgcn_exp2f(m - from), f1 = __builtin_amdgcn_exp2f(other.x - from);
+    m = top;
+    l = fmaf(other.y, f1, l * f0);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f32x4 x = os[(t * 4 + i) * 64];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[t][4 * i + j] = fmaf(x[j], f1, o[t][4 * i + j] * f0);
+      }
+  }
   if (!live) return;
   // a lane holds dims 32 t + 8 i + 4 hf .. + 3
   if (a.splits > 1) {

@@ -7,7 +7,8 @@
 #include "attn_prompt.hpp"
 
 namespace gqk {
-void launch_prompt_f16(const AttnPromptArgs& a, dim3 grid, hipStream_t stream);
-void launch_prompt_bf16(const AttnPromptArgs& a, dim3 grid, hipStream_t stream);
-void launch_prompt_q8_0(const AttnPromptArgs& a, dim3 grid, hipStream_t stream);
+// groups: of four waves per block, 1 or (up to head dim 128) 2.
+void launch_prompt_f16(const AttnPromptArgs& a, int groups, dim3 grid, hipStream_t stream);
+void launch_prompt_bf16(const AttnPromptArgs& a, int groups, dim3 grid, hipStream_t stream);
+void launch_prompt_q8_0(const AttnPromptArgs& a, int groups, dim3 grid, hipStream_t stream);
 }  // namespace gqk
