@@ -76,6 +76,7 @@ UNITS = [
     ("attn_extend.hip", [], "attn_extend"),
     ("attn_prompt_typed.hip", ["-DGQK_KV_KIND=0", *VGPR_FORM], "prompt_f16"),
     ("attn_prompt_typed.hip", ["-DGQK_KV_KIND=1", *VGPR_FORM], "prompt_bf16"),
+    ("attn_prompt_typed.hip", ["-DGQK_KV_KIND=2", *VGPR_FORM], "prompt_q8_0"),
     ("verify.hip", [], "verify"),
 ]
 

@@ -11,7 +11,7 @@ constexpr int64_t kExtendMaxLen = int64_t(1) << 25;
 constexpr int64_t kExtendBlocks = 1024;   // blocks a call aims for
 constexpr int64_t kExtendChunk = 1024;    // longest chunk of positions of the few-rows kernel
 constexpr int kFewColumns = 16;           // columns of its tiles
-constexpr int64_t kPromptBlocks = 256;    // blocks of two groups of waves that run at once
+constexpr int64_t kPromptBlocks = 256;    // blocks that run at once: one per CU, or two of one group of waves to head dim 128
 // Blocks from which one group of waves each, two blocks at a time, does better: 8 prompts
 // to 4096 (4680 blocks) 560 us against 685; one of 4096 (512) 110 against 104.
 constexpr int64_t kPromptSingle = 1024;
@@ -34,8 +34,7 @@ static int extend_plan(const KvView& c, int32_t type, int64_t n_seqs, int64_t n_
     return GGUF_QK_ERR_LIMIT;
   p->group = (int32_t)(n_heads / c.hkv);
   if (n_rows * p->group > INT32_MAX / 2) return GGUF_QK_ERR_LIMIT;
-  p->prompt = type == GGUF_KV_TYPE_BF16 && c.head_bytes == kv_head_bytes(false, c.dim, c.ps) &&
-              n_rows * p->group > 2 * kFewColumns * n_seqs;
+  p->prompt = type == GGUF_KV_TYPE_BF16 && n_rows * p->group > 2 * kFewColumns * n_seqs;
   p->columns = p->prompt ? kPromptColumns : kFewColumns;
   const int tile = p->prompt ? kPromptSlots : kAttnTile;
   p->unit = c.ps > tile ? c.ps : tile;
@@ -53,10 +52,11 @@ static int extend_plan(const KvView& c, int32_t type, int64_t n_seqs, int64_t n_
   const int64_t cells = p->tiles * c.hkv;
   int64_t chunk;
   if (p->prompt) {
-    const int64_t want = cells > 0 && cells < kPromptBlocks ? kPromptBlocks / cells : 1;
+    p->groups = cells < kPromptSingle ? prompt_groups(c.head_bytes != kv_head_bytes(false, c.dim, c.ps), c.dim) : 1;
+    const int64_t blocks = p->groups == 2 || c.dim > 128 ? kPromptBlocks : 2 * kPromptBlocks;
+    const int64_t want = cells > 0 && cells < blocks ? blocks / cells : 1;
     chunk = ((span + want - 1) / want + 63) / 64 * 64;
     if (chunk < kPromptLeast) chunk = kPromptLeast;
-    p->groups = c.dim <= 128 && cells < kPromptSingle ? 2 : 1;
   } else {
     const int64_t round = kAttnTile * kAttnWaves;
     int64_t most = int64_t(64) << c.shift;
@@ -174,7 +174,8 @@ int gguf_attn_extend(const gguf_kv_cache* cache, const void* q, int32_t type, in
   a.tiles = (int32_t)p.tiles;
   if (p.prompt) {
     if (cache->type == GGUF_KV_TYPE_F16) launch_prompt_f16(a, p.groups, grid, stream);
-    else launch_prompt_bf16(a, p.groups, grid, stream);
+    else if (cache->type == GGUF_KV_TYPE_BF16) launch_prompt_bf16(a, p.groups, grid, stream);
+    else launch_prompt_q8_0(a, p.groups, grid, stream);
   } else if (cache->type == GGUF_KV_TYPE_F16) launch_attn_rows_f16(a, grid, stream);
   else if (cache->type == GGUF_KV_TYPE_BF16) launch_attn_rows_bf16(a, grid, stream);
   else launch_attn_rows_q8_0(a, grid, stream);

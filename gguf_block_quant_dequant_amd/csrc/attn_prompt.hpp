@@ -18,6 +18,10 @@
 
 namespace gqk {
 
+// Most groups of four waves of a block: registers hold two up to head dim 128 (Q8_0,
+// whose codes are converted on the way, 64).
+constexpr int prompt_groups(bool q8, int dim) { return dim <= (q8 ? 64 : 128) ? 2 : 1; }
+
 struct AttnPromptArgs : AttnRowsArgs {
   int32_t tiles;   // tiles of columns of the grid
 };
@@ -101,6 +105,18 @@ __device__ __forceinline__ void prompt_phase(Load&& load, Mma&& mma, Work&& work
   }
 }
 
+__device__ __forceinline__ void prompt_store16(uint32_t at, const uint4& x) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4), aligned(16)));
+  *reinterpret_cast<__attribute__((address_space(3))) u32x4*>(at) = u32x4{x.x, x.y, x.z, x.w};
+}
+
+// A value the compiler takes for new each time: what is formed from it is not kept in
+// registers over the loop.
+__device__ __forceinline__ int prompt_anew(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 // The greater of a value and the other half wave's.
 __device__ __forceinline__ float prompt_half_max(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -114,6 +130,10 @@ __global__ __launch_bounds__(kPromptThreads * GROUPS, NB <= 4 ? 2 : 1) void attn
   constexpr int DIM = Tile::kDim, T = Tile::kSlots, KC = Tile::kKChunks, VC = Tile::kVChunks, LOADS = Tile::kLoads;
   constexpr int KS = DIM / 16, NT = DIM / 32;   // steps of S, tiles of O
   constexpr int MM = KIND == kKvBF16 ? kKvBF16 : kKvF16;     // type of the products
+  constexpr bool Q8 = KIND == kKvQ80;
+  constexpr int RUNS = (NB + 1) / 2;               // Q8_0: runs of sixteen codes of a lane, K and V each
+  constexpr int SC = T * NB * 2 / 16;              // Q8_0: 16-byte chunks of a tile's scales, K and V each (at most 64)
+  constexpr int SLOADS = Q8 ? (SC + 63) / 64 : 1;
   const int tid = threadIdx.x, lane = tid & 63;
   const int group = GROUPS == 1 ? 0 : __builtin_amdgcn_readfirstlane(tid / kPromptThreads);
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) % kPromptWaves;   // of the group
@@ -150,7 +170,11 @@ __global__ __launch_bounds__(kPromptThreads * GROUPS, NB <= 4 ? 2 : 1) void attn
 
   // K and V of two tiles of each group: K, K, V, V
   __shared__ __align__(1024) uint8_t lds[GROUPS][4][Tile::kBytes];
+  // Q8_0: the scales of a tile of K and V, a copy per wave
+  __shared__ __align__(1024) uint8_t lds_scales[Q8 ? GROUPS * kPromptWaves : 1][Q8 ? 2 * SLOADS * 1024 : 16];
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&lds[group][0][0];
+  const uint32_t scales0 =
+      (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&lds_scales[Q8 ? group * kPromptWaves + wave : 0][0];
 
   const uint8_t* const kh = a.c.k + (int64_t)h * a.c.head_bytes;
   const uint8_t* const vh = a.c.v + (int64_t)h * a.c.head_bytes;
@@ -177,10 +201,10 @@ __global__ __launch_bounds__(kPromptThreads * GROUPS, NB <= 4 ? 2 : 1) void attn
   // This lane's chunk of load i. Of K a wave loads sixteen slots, which lie in one
   // page; of V whole rows of dims, whose chunks of eight slots lie in up to four pages,
   // of two patterns over the lanes that loads take in turn (v_swizzle).
-  uint32_t k_at[LOADS], v_at[LOADS];   // offset in the page's head, of V without the slot where pages are small
+  uint32_t k_at[Q8 ? 1 : LOADS], v_at[Q8 ? 1 : LOADS];   // offset in the page's head, of V without the slot where pages are small
   const bool whole = a.c.ps >= T;
 #pragma unroll
-  for (int i = 0; i < LOADS; ++i) {
+  for (int i = 0; i < (Q8 ? 0 : LOADS); ++i) {
     const int L = (wave * LOADS + i) * 64 + lane;
     const int kr = L / KC, vr = L / VC;
     const int slot = (kr & ~31) | prompt_slot(kr & 31);
@@ -191,6 +215,17 @@ __global__ __launch_bounds__(kPromptThreads * GROUPS, NB <= 4 ? 2 : 1) void attn
     const int id = __builtin_amdgcn_readlane(pid, (v >> shift) - page0);
     return (id < 0 ? 0 : id) * page_bytes;
   };
+  // Slots of a tile whose values are looked at.
+  auto present = [&](int v0) -> uint64_t {
+    const int n = end - v0;
+    uint64_t m = n >= T ? ~0ull : (1ull << n) - 1;
+    for (int p = v0; p < v0 + T && p < end; p += a.c.ps) {
+      const int id = __builtin_amdgcn_readlane(pid, (p >> shift) - page0);
+      if (id < 0) m &= whole ? 0 : ~(((1ull << a.c.ps) - 1) << (p - v0));
+    }
+    return m;
+  };
+
   auto issue = [&](int v, int buf) {
     const uint32_t to = lds0 + buf * Tile::kBytes + wave * LOADS * 1024;
     const int vk = v + 16 * wave;
@@ -213,15 +248,126 @@ __global__ __launch_bounds__(kPromptThreads * GROUPS, NB <= 4 ? 2 : 1) void attn
         prompt_load_lds(of[(wave * LOADS + i) & 1] + v_at[i], to + 2 * Tile::kBytes + i * 1024);
     }
   };
-  // Slots of a tile whose values are looked at.
-  auto present = [&](int v0) -> uint64_t {
-    const int n = end - v0;
-    uint64_t m = n >= T ? ~0ull : (1ull << n) - 1;
-    for (int p = v0; p < v0 + T && p < end; p += a.c.ps) {
-      const int id = __builtin_amdgcn_readlane(pid, (p >> shift) - page0);
-      if (id < 0) m &= whole ? 0 : ~(((1ull << a.c.ps) - 1) << (p - v0));
+  // Q8_0: a tile's codes go through registers, its scales to LDS as they are. Offsets are
+  // formed anew for each tile: registers are short.
+  uint4 k_raw[Q8 ? RUNS : 1], v_raw[Q8 ? RUNS : 1];
+  auto fetch = [&](auto is_k, int v) {
+    if constexpr (Q8) {
+      constexpr bool K = decltype(is_k)::value;
+      const int ln = prompt_anew(lane);
+#pragma unroll
+      for (int i = 0; i < RUNS; ++i) {
+        int u = i * 64 + ln;
+        if (NB % 2 && u >= 32 * NB) u = ln;
+        if constexpr (K) {
+          const int vk = v + 16 * wave;
+          k_raw[i] = load16(kh + page_at(vk) + (((vk & smask) + u / (2 * NB)) * DIM + u % (2 * NB) * 16));
+        } else {
+          const int p = v + u % 4 * 16, id = whole ? 0 : __shfl(pid, (p >> shift) - page0);
+          const int64_t page = whole ? page_at(v) : (id < 0 ? 0 : id) * page_bytes;
+          v_raw[i] = load16(vh + page + ((wave * 8 * NB + u / 4) * a.c.ps + (p & smask)));
+        }
+      }
+      // K's scales [slot][block], V's [block][slot], behind the codes of their page
+#pragma unroll
+      for (int i = 0; i < SLOADS; ++i) {
+        const int u = i * 64 + ln, c = u < SC ? u : 0;
+        const int p = K ? v + c * 8 / NB : v + c % (T / 8) * 8, id = whole ? 0 : __shfl(pid, (p >> shift) - page0);
+        const int64_t page = whole ? page_at(v) : (id < 0 ? 0 : id) * page_bytes;
+        const uint8_t* from = (K ? kh : vh) + page + a.c.ps * DIM +
+                              (K ? (p & smask) * NB + c * 8 % NB : c / (T / 8) * a.c.ps + (p & smask)) * 2;
+        prompt_load_lds(from, scales0 + (K ? 0 : SLOADS * 1024) + i * 1024);
+      }
     }
-    return m;
+  };
+  // A value enters fp16 as code * (d 2^e), e such that the tile's greatest scale comes to
+  // [2^7, 2^8): the nearest fp16 of the value, or within 2^-32 of the greatest scale. K's
+  // scores take 2^-e back tile by tile; V's sums are kept in units of 2^-ve, which follow
+  // the greatest scale met so far.
+  int ke = 0, ve = 15;
+  auto settle = [&](auto is_k, uint64_t here) {
+    if constexpr (Q8) {
+      constexpr bool K = decltype(is_k)::value;
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      uint32_t t = 0;
+#pragma unroll
+      for (int i = 0; i < SLOADS; ++i) {
+        const int u = i * 64 + prompt_anew(lane);
+        const uint4 d = prompt_lds16(scales0 + (K ? 0 : SLOADS * 1024) + u * 16);   // behind the last chunk: the first's
+        const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+        if (here == ~0ull) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) t = max_word(t, max_word(w[j] & 0x7FFFu, w[j] >> 16 & 0x7FFFu));
+        } else {   // behind the end: anything
+          const int c = u < SC ? u : 0;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int slot = K ? (c * 8 + j) / NB : c % (T / 8) * 8 + j;
+            if (here >> slot & 1) t = max_word(t, w[j / 2] >> (j % 2 * 16) & 0x7FFFu);
+          }
+        }
+      }
+      t = max_word(t, dpp_word<0xB1>(t));
+      t = max_word(t, dpp_word<0x4E>(t));
+      t = max_word(t, dpp_word<0x141>(t));
+      t = max_word(t, dpp_word<0x140>(t));
+      t = max_word(max_word(lane_word(t, 0), lane_word(t, 16)), max_word(lane_word(t, 32), lane_word(t, 48)));
+      int e = 22 - (int)(t >> 10);   // an exponent field E: below 2^(E - 14)
+      e = e > 15 ? 15 : e < -8 ? -8 : e;
+      if (K) ke = e;
+      else ve = e < ve ? e : ve;
+    }
+  };
+  auto times = [](uint32_t x, uint32_t y) {
+    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, x) * __builtin_bit_cast(f16x2, y));
+  };
+  // Run i of the codes to buffer buf.
+  auto convert = [&](auto is_k, int i, int buf, uint64_t here) {
+    if constexpr (Q8) {
+      constexpr bool K = decltype(is_k)::value;
+      const int u = i * 64 + prompt_anew(lane);
+      if (NB % 2 && u >= 32 * NB) return;
+      const uint4 raw = K ? k_raw[i] : v_raw[i];
+      const uint32_t mul = 0x00010001u * (uint32_t)((15 + (K ? ke : ve)) << 10);   // 2^e twice
+      uint4 lo = codes_f16(make_uint2(raw.x, raw.y)), hi = codes_f16(make_uint2(raw.z, raw.w));
+      uint32_t to, chunk, swizzle;
+      if constexpr (K) {
+        const int slot = 16 * wave + u / (2 * NB), r = (slot & ~31) | prompt_slot(slot & 31);
+        to = lds0 + buf * Tile::kBytes + r * (DIM * 2);
+        chunk = u % (2 * NB) * 2;
+        swizzle = Tile::k_swizzle(r);
+        uint32_t d = *reinterpret_cast<const __attribute__((address_space(3))) uint16_t*>(
+            scales0 + (slot * NB + u % (2 * NB) / 2) * 2);
+        d = times(d | d << 16, mul);
+        lo = make_uint4(times(lo.x, d), times(lo.y, d), times(lo.z, d), times(lo.w, d));
+        hi = make_uint4(times(hi.x, d), times(hi.y, d), times(hi.z, d), times(hi.w, d));
+      } else {
+        const int r = wave * 8 * NB + u / 4;
+        to = lds0 + (2 + buf) * Tile::kBytes + r * (T * 2);
+        chunk = u % 4 * 2;
+        swizzle = Tile::v_swizzle(r);
+        const uint32_t at = scales0 + SLOADS * 1024 + (r / 32 * (T / 8) + chunk) * 16;
+        const uint4 a0 = prompt_lds16(at), a1 = prompt_lds16(at + 16);
+        lo = make_uint4(times(lo.x, times(a0.x, mul)), times(lo.y, times(a0.y, mul)), times(lo.z, times(a0.z, mul)),
+                        times(lo.w, times(a0.w, mul)));
+        hi = make_uint4(times(hi.x, times(a1.x, mul)), times(hi.y, times(a1.y, mul)), times(hi.z, times(a1.z, mul)),
+                        times(hi.w, times(a1.w, mul)));
+        if (here != ~0ull) {   // behind the end: zero
+          const uint32_t bits = (uint32_t)(here >> (8 * chunk)) & 0xFFFFu;
+          auto keep = [&](int j) { return ((bits >> 2 * j & 1) ? 0xFFFFu : 0u) | ((bits >> 2 * j & 2) ? 0xFFFF0000u : 0u); };
+          lo = make_uint4(lo.x & keep(0), lo.y & keep(1), lo.z & keep(2), lo.w & keep(3));
+          hi = make_uint4(hi.x & keep(4), hi.y & keep(5), hi.z & keep(6), hi.w & keep(7));
+        }
+      }
+      prompt_store16(to + ((chunk ^ swizzle) << 4), lo);
+      prompt_store16(to + (((chunk + 1) ^ swizzle) << 4), hi);
+    }
+  };
+  using K_ = std::true_type;
+  using V_ = std::false_type;
+  auto convert_all = [&](auto is_k, int buf, uint64_t here) {
+#pragma unroll
+    for (int i = 0; i < RUNS; ++i) convert(is_k, i, buf, here);
   };
 
   // the group's tile and the one behind its next; all groups count alike
@@ -231,7 +377,16 @@ __global__ __launch_bounds__(kPromptThreads * GROUPS, NB <= 4 ? 2 : 1) void attn
     return v;
   };
   fetch_pages(first >> shift);
-  if (mine(first) < end) issue(mine(first), 0);
+  uint64_t here0 = 0, here1 = 0;   // Q8_0: of the tile in hand and the next
+  if (mine(first) < end) {
+    if constexpr (Q8) {
+      here0 = present(mine(first));
+      fetch(K_{}, mine(first));
+      fetch(V_{}, mine(first));
+    } else {
+      issue(mine(first), 0);
+    }
+  }
 
   // q of this lane's column: the B operand, dims 16 k + 8 hf .. + 7
   uint4 q[KS];
@@ -289,6 +444,7 @@ __global__ __launch_bounds__(kPromptThreads * GROUPS, NB <= 4 ? 2 : 1) void attn
 #pragma unroll
   for (int t = 0; t < NT; ++t) o[t] = f32x16v{};
   float m = -__builtin_inff(), l = 0.f;
+  int unit_o = 0;   // Q8_0: O's sums are in units of 2^-unit_o
 
   // What a column does not see of the 32 slots from `real` on.
   auto mask = [&](f32x16v& sc, int real, uint32_t here) {
@@ -299,7 +455,7 @@ __global__ __launch_bounds__(kPromptThreads * GROUPS, NB <= 4 ? 2 : 1) void attn
   };
   // The softmax of 32 slots in ten chunks: the maximum; whether it is raised, and the
   // factor alpha that the sums so far then take; eight pairs of weights.
-  float mx, base, alpha;
+  float mx, base, alpha, by = factor;   // by: factor of the tile's scores
   bool raise;
   uint32_t w[8];
   auto soften = [&](const f32x16v& sc, int chunk) {
@@ -308,7 +464,7 @@ __global__ __launch_bounds__(kPromptThreads * GROUPS, NB <= 4 ? 2 : 1) void attn
 #pragma unroll
       for (int i = 1; i < 16; ++i) mx = fmaxf(mx, sc[i]);
     } else if (chunk == 1) {
-      mx = prompt_half_max(mx) * factor;
+      mx = prompt_half_max(mx) * by;
       raise = __any(mx > m + kPromptSlack);
       const float old = m;
       m = raise ? fmaxf(m, mx) : m;
@@ -317,8 +473,8 @@ __global__ __launch_bounds__(kPromptThreads * GROUPS, NB <= 4 ? 2 : 1) void attn
       l *= alpha;
     } else {
       const int j = chunk - 2;
-      const float x = __builtin_amdgcn_exp2f(fmaf(sc[2 * j], factor, -base));
-      const float y = __builtin_amdgcn_exp2f(fmaf(sc[2 * j + 1], factor, -base));
+      const float x = __builtin_amdgcn_exp2f(fmaf(sc[2 * j], by, -base));
+      const float y = __builtin_amdgcn_exp2f(fmaf(sc[2 * j + 1], by, -base));
       l += x + y;
       w[j] = MM == kKvBF16 ? pack_bf16x2(x, y) : __builtin_bit_cast(uint32_t, to_f16x2(x, y));
     }
@@ -353,18 +509,20 @@ __global__ __launch_bounds__(kPromptThreads * GROUPS, NB <= 4 ? 2 : 1) void attn
     constexpr uint32_t kt = BUF * Tile::kBytes, vt = BUF * Tile::kBytes;
     const int v0 = mine(first), real0 = real_of(v0);
     const bool any = v0 < end;
-    const uint64_t here = any ? present(v0) : 0;
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this tile's loads have arrived
-    if (any && here != ~0ull) {
-      // V behind the end may hold anything: zero, each wave what it has loaded
+    const uint64_t here = Q8 ? here0 : any ? present(v0) : 0;
+    if constexpr (!Q8) {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this tile's loads have arrived
+      if (any && here != ~0ull) {
+        // V behind the end may hold anything: zero, each wave what it has loaded
 #pragma unroll
-      for (int i = 0; i < LOADS; ++i) {
-        const int L = (wave * LOADS + i) * 64 + lane;
-        const uint32_t bits = (uint32_t)(here >> (8 * ((L % VC) ^ Tile::v_swizzle(L / VC)))) & 0xFFu;
-        uint16_t* p = reinterpret_cast<uint16_t*>(lds[group][2 + BUF] + L * 16);
+        for (int i = 0; i < LOADS; ++i) {
+          const int L = (wave * LOADS + i) * 64 + lane;
+          const uint32_t bits = (uint32_t)(here >> (8 * ((L % VC) ^ Tile::v_swizzle(L / VC)))) & 0xFFu;
+          uint16_t* p = reinterpret_cast<uint16_t*>(lds[group][2 + BUF] + L * 16);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (!(bits >> j & 1)) p[j] = 0;
+          for (int j = 0; j < 8; ++j)
+            if (!(bits >> j & 1)) p[j] = 0;
+        }
       }
     }
     __syncthreads();   // everyone's have, and the other buffer is free
@@ -372,29 +530,80 @@ __global__ __launch_bounds__(kPromptThreads * GROUPS, NB <= 4 ? 2 : 1) void attn
     for (int g = 0; g < GROUPS; ++g) next = seen_from(next + T);
     first = next;
     const int v1 = mine(next);
-    if (v1 < end) {
+    if (!Q8 && v1 < end) {
       if (((v1 + T - 1) >> shift) - page0 >= 64) fetch_pages(v1 >> shift);
       issue(v1, BUF ^ 1);
     }
-    if (!any || idle || real0 >= w_hi || (real0 >= a.sinks && real0 + T <= wr.near)) return;
-    using None = std::integral_constant<int, 0>;
+    // Q8_0: K of the next tile is converted beside this one's first scores, its V beside
+    // the last products; K of the one behind is asked for before these.
+    const bool more = Q8 && v1 < end;
+    auto ask_k = [&]() {
+      here0 = here1;
+      for (int g = 0; g < GROUPS; ++g) next = seen_from(next + T);
+      const int v2 = mine(next);
+      if (v2 < end) {
+        if (((v2 + T - 1) >> shift) - page0 >= 64) fetch_pages(v2 >> shift);
+        here1 = present(v2);
+        fetch(K_{}, v2);
+      }
+    };
+    if constexpr (Q8) by = __builtin_ldexpf(factor, -ke);   // of this tile's scores
+    if (!any || idle || real0 >= w_hi || (real0 >= a.sinks && real0 + T <= wr.near)) {
+      if (more) {
+        settle(K_{}, here1);
+        convert_all(K_{}, BUF ^ 1, here1);
+        fetch(V_{}, v1);
+        settle(V_{}, here1);
+        convert_all(V_{}, BUF ^ 1, here1);
+        ask_k();
+      }
+      return;
+    }
+    if constexpr (Q8) {
+      if (ve != unit_o) {
+        alpha = __builtin_ldexpf(1.0f, ve - unit_o);
+        rescale();
+        unit_o = ve;
+      }
+    }
     using Softmax = std::integral_constant<int, 10>;
-    const auto idle_work = [](int) {};
     uint4 p[2];
     f32x16v sa, sb;
     const bool edge = here != ~0ull || real0 < wr.far || real0 + T > wr.full;
     // matrix and vector units side by side, by halves of the tile
-    scores(kt, sa, None{}, idle_work);
+    // (behind the last tile old codes are converted once more, into a buffer no one reads)
+    using Convert = std::integral_constant<int, Q8 ? RUNS : 0>;
+    settle(K_{}, here1);
+    scores(kt, sa, Convert{}, [&](int c) { convert(K_{}, c, BUF ^ 1, here1); });
     if (edge) mask(sa, real0, (uint32_t)here);
     scores(kt + 32 * DIM * 2, sb, Softmax{}, [&](int c) { soften(sa, c); });
     weights(p);
     if (raise) rescale();
     if (edge) mask(sb, real0 + 32, (uint32_t)(here >> 32));
+    if (more) fetch(V_{}, v1);
     weigh(vt, 0, p, Softmax{}, [&](int c) { soften(sb, c); });
     weights(p);
     if (raise) rescale();
-    weigh(vt, 1, p, None{}, idle_work);
+    settle(V_{}, here1);
+    const uint64_t here_v = here1;
+    if (more) ask_k();
+    weigh(vt, 1, p, Convert{}, [&](int c) { convert(V_{}, c, BUF ^ 1, here_v); });
   };
+  if (Q8 && mine(first) < end) {
+    settle(K_{}, here0);
+    settle(V_{}, here0);
+    convert_all(K_{}, 0, here0);
+    convert_all(V_{}, 0, here0);
+    int next = first;
+    for (int g = 0; g < GROUPS; ++g) next = seen_from(next + T);
+    next = mine(next);
+    if (next < end) {
+      if (((next + T - 1) >> shift) - page0 >= 64) fetch_pages(next >> shift);
+      here1 = present(next);
+      fetch(K_{}, next);
+    }
+  }
+  unit_o = ve;
   while (first < end) {
     step(std::integral_constant<int, 0>{});
     if (first >= end) break;
@@ -402,6 +611,10 @@ __global__ __launch_bounds__(kPromptThreads * GROUPS, NB <= 4 ? 2 : 1) void attn
   }
 
   l += __shfl_xor(l, 32);
+  if constexpr (Q8) {
+    alpha = __builtin_ldexpf(1.0f, -unit_o);
+    rescale();
+  }
   if constexpr (GROUPS == 2) {
     // the second group's sums go to the first's waves, lane by lane
     static_assert(kPromptThreads * NT * 64 + kPromptThreads * 8 <= sizeof(lds), "sums fit");

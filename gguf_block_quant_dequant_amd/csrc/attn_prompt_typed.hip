@@ -6,7 +6,7 @@ namespace gqk {
 
 template <int NB>
 static void launch_dim(const AttnPromptArgs& a, int groups, dim3 grid, hipStream_t stream) {
-  if constexpr (NB <= 4) {
+  if constexpr (prompt_groups(GQK_KV_KIND == 2, NB * 32) == 2) {
     if (groups == 2) {
       hipLaunchKernelGGL((attn_prompt_kernel<GQK_KV_KIND, NB, 2>), grid, dim3(2 * kPromptThreads), 0, stream, a);
       return;
