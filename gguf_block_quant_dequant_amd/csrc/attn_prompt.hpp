@@ -70,11 +70,18 @@ __device__ __forceinline__ int prompt_slot(int r) { return (r & ~12) | (r & 4) <
 // lane. Assembly, so that the compiler, which cannot tell which bytes of LDS are in
 // flight, does not wait for all loads before each read of LDS; the caller waits. M0 is
 // never live in compiled code here: only such loads of the compiler's own would set it.
+// The compiler may hold uniform values in vector registers; what the assembly takes as
+// scalars is read from the first lane.
 __device__ __forceinline__ void prompt_load_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
+  lds = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds);
+  const uint64_t b = reinterpret_cast<uint64_t>(base);
+  base = reinterpret_cast<const uint8_t*>((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(b >> 32)) << 32 |
+                                          (uint32_t)__builtin_amdgcn_readfirstlane((int)b));
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(base), "s"(lds)
                : "memory");
 }
 __device__ __forceinline__ void prompt_load_lds(const uint8_t* p, uint32_t lds) {
+  lds = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds);
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(lds) : "memory");
 }
 
@@ -133,7 +140,6 @@ __global__ __launch_bounds__(kPromptThreads * GROUPS, NB <= 4 ? 2 : 1) void attn
   constexpr bool Q8 = KIND == kKvQ80;
   constexpr int RUNS = (NB + 1) / 2;               // Q8_0: runs of sixteen codes of a lane, K and V each
   constexpr int SC = T * NB * 2 / 16;              // Q8_0: 16-byte chunks of a tile's scales, K and V each (at most 64)
-  constexpr int SLOADS = Q8 ? (SC + 63) / 64 : 1;
   const int tid = threadIdx.x, lane = tid & 63;
   const int group = GROUPS == 1 ? 0 : __builtin_amdgcn_readfirstlane(tid / kPromptThreads);
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) % kPromptWaves;   // of the group
@@ -170,11 +176,12 @@ __global__ __launch_bounds__(kPromptThreads * GROUPS, NB <= 4 ? 2 : 1) void attn
 
   // K and V of two tiles of each group: K, K, V, V
   __shared__ __align__(1024) uint8_t lds[GROUPS][4][Tile::kBytes];
-  // Q8_0: the scales of a tile of K and V, a copy per wave
-  __shared__ __align__(1024) uint8_t lds_scales[Q8 ? GROUPS * kPromptWaves : 1][Q8 ? 2 * SLOADS * 1024 : 16];
+  // Q8_0, per wave: the scales of a tile of K and of V, the codes of K that it converts
+  constexpr int kRaw = 2 * SC * 16, kWave = Q8 ? kRaw + 32 * NB * 16 : 16;
+  __shared__ __align__(1024) uint8_t lds_wave[Q8 ? GROUPS * kPromptWaves : 1][kWave];
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&lds[group][0][0];
   const uint32_t scales0 =
-      (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&lds_scales[Q8 ? group * kPromptWaves + wave : 0][0];
+      (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&lds_wave[Q8 ? group * kPromptWaves + wave : 0][0];
 
   const uint8_t* const kh = a.c.k + (int64_t)h * a.c.head_bytes;
   const uint8_t* const vh = a.c.v + (int64_t)h * a.c.head_bytes;
@@ -248,126 +255,188 @@ __global__ __launch_bounds__(kPromptThreads * GROUPS, NB <= 4 ? 2 : 1) void attn
         prompt_load_lds(of[(wave * LOADS + i) & 1] + v_at[i], to + 2 * Tile::kBytes + i * 1024);
     }
   };
-  // Q8_0: a tile's codes go through registers, its scales to LDS as they are. Offsets are
-  // formed anew for each tile: registers are short.
-  uint4 k_raw[Q8 ? RUNS : 1], v_raw[Q8 ? RUNS : 1];
+  // Q8_0. A wave converts sixteen slots of K and DIM / 4 dims of V, by runs of sixteen
+  // codes: run u is codes 16 (u % (2 NB)) .. of slot u / (2 NB), or slots 16 (u % 4) .. of
+  // dim u / 4; lane l takes u = l, l + 64, ... Of a tile's V codes go through registers,
+  // K's (registers are short) and the scales through LDS as they are.
+  constexpr bool POW2 = (NB & (NB - 1)) == 0;   // a lane's runs of K then lie 64 / (2 NB) slots apart
+  uint4 v_raw[Q8 ? RUNS : 1];
+  uint32_t v_run = 0;           // offset of run l of V in a page's head, from the tile's slot on
+  uint32_t k_lo = 0, v_lo = 0;  // where run l goes in LDS: its first chunk (the second is at ^ 16)
+  auto k_target = [&](int u) {
+    const int slot = 16 * wave + u / (2 * NB), r = (slot & ~31) | prompt_slot(slot & 31);
+    return lds0 + r * (DIM * 2) + ((u % (2 * NB) * 2 ^ Tile::k_swizzle(r)) << 4);
+  };
+  auto v_target = [&](int u) {
+    const int r = wave * 8 * NB + u / 4;
+    return lds0 + 2 * Tile::kBytes + r * (T * 2) + ((u % 4 * 2 ^ Tile::v_swizzle(r)) << 4);
+  };
+  if constexpr (Q8) {
+    v_run = (wave * 8 * NB + lane / 4) * a.c.ps + (whole ? lane % 4 * 16 : 0);
+    k_lo = k_target(lane);
+    v_lo = v_target(lane);
+  }
   auto fetch = [&](auto is_k, int v) {
     if constexpr (Q8) {
       constexpr bool K = decltype(is_k)::value;
-      const int ln = prompt_anew(lane);
+      if constexpr (K) {
+        // sixteen slots of one page
+        const int vk = v + 16 * wave;
+        const uint8_t* from = kh + page_at(vk) + (vk & smask) * DIM;
 #pragma unroll
-      for (int i = 0; i < RUNS; ++i) {
-        int u = i * 64 + ln;
-        if (NB % 2 && u >= 32 * NB) u = ln;
-        if constexpr (K) {
-          const int vk = v + 16 * wave;
-          k_raw[i] = load16(kh + page_at(vk) + (((vk & smask) + u / (2 * NB)) * DIM + u % (2 * NB) * 16));
-        } else {
-          const int p = v + u % 4 * 16, id = whole ? 0 : __shfl(pid, (p >> shift) - page0);
-          const int64_t page = whole ? page_at(v) : (id < 0 ? 0 : id) * page_bytes;
-          v_raw[i] = load16(vh + page + ((wave * 8 * NB + u / 4) * a.c.ps + (p & smask)));
+        for (int i = 0; i < RUNS; ++i) {
+          if (NB % 2 && i * 64 + lane >= 32 * NB) continue;
+          prompt_load_lds(from + i * 1024, lane * 16, scales0 + kRaw + i * 1024);   // their codes lie in a row
         }
-      }
-      // K's scales [slot][block], V's [block][slot], behind the codes of their page
+        // chunk l of [slot][block], behind the page's codes
+        if (whole) {
+          from = kh + page_at(v) + a.c.ps * DIM + (v & smask) * (NB * 2);
+          if (lane < SC) prompt_load_lds(from, lane * 16, scales0);
+        } else {
+          const int ln = prompt_anew(lane), p = v + ln * 8 / NB, id = __shfl(pid, ((p >> shift) - page0) & 63);
+          const uint8_t* mine = kh + (id < 0 ? 0 : id) * page_bytes + a.c.ps * DIM + ((p & smask) * NB + ln * 8 % NB) * 2;
+          if (lane < SC) prompt_load_lds(mine, scales0);
+        }
+      } else if (whole) {
+        const uint8_t* from = vh + page_at(v) + (v & smask);
 #pragma unroll
-      for (int i = 0; i < SLOADS; ++i) {
-        const int u = i * 64 + ln, c = u < SC ? u : 0;
-        const int p = K ? v + c * 8 / NB : v + c % (T / 8) * 8, id = whole ? 0 : __shfl(pid, (p >> shift) - page0);
-        const int64_t page = whole ? page_at(v) : (id < 0 ? 0 : id) * page_bytes;
-        const uint8_t* from = (K ? kh : vh) + page + a.c.ps * DIM +
-                              (K ? (p & smask) * NB + c * 8 % NB : c / (T / 8) * a.c.ps + (p & smask)) * 2;
-        prompt_load_lds(from, scales0 + (K ? 0 : SLOADS * 1024) + i * 1024);
+        for (int i = 0; i < RUNS; ++i)
+          if (!(NB % 2) || i * 64 + lane < 32 * NB) v_raw[i] = load16(from + i * 16 * a.c.ps + v_run);
+        const int l = prompt_anew(lane);
+        const uint32_t at = l / (T / 8) * a.c.ps * 2 + l % (T / 8) * 16;   // chunk l of [block][slot]
+        if (lane < SC) prompt_load_lds(from + a.c.ps * DIM + (v & smask), at, scales0 + SC * 16);
+      } else {
+        const int ln = prompt_anew(lane), p = v + ln % 4 * 16, id = __shfl(pid, (p >> shift) - page0);
+        const uint8_t* from = vh + (id < 0 ? 0 : id) * page_bytes + (p & smask) + v_run;
+#pragma unroll
+        for (int i = 0; i < RUNS; ++i)
+          if (!(NB % 2) || i * 64 + lane < 32 * NB) v_raw[i] = load16(from + i * 16 * a.c.ps);
+        const int ps = v + ln % (T / 8) * 8, ids = __shfl(pid, (ps >> shift) - page0);
+        const uint8_t* mine = vh + (ids < 0 ? 0 : ids) * page_bytes + a.c.ps * DIM + (ln / (T / 8) * a.c.ps + (ps & smask)) * 2;
+        if (lane < SC) prompt_load_lds(mine, scales0 + SC * 16);
       }
     }
   };
-  // A value enters fp16 as code * (d 2^e), e such that the tile's greatest scale comes to
-  // [2^7, 2^8): the nearest fp16 of the value, or within 2^-32 of the greatest scale. K's
-  // scores take 2^-e back tile by tile; V's sums are kept in units of 2^-ve, which follow
+  // A value enters fp16 as code * (d 2^e), e 0 for a greatest scale of the tile from 2^-7 to
+  // 2^8 and else such that it comes to [2^7, 2^8) (or e to 15): the nearest fp16 of the
+  // value, or within 2^-18 of the greatest scale. K's scores take 2^-e back tile by tile; V's sums are kept in units of 2^-ve, which follow
   // the greatest scale met so far.
-  int ke = 0, ve = 15;
+  int ke = 0, ve = 0;
+  bool first_v = true;
   auto settle = [&](auto is_k, uint64_t here) {
     if constexpr (Q8) {
       constexpr bool K = decltype(is_k)::value;
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      uint32_t t = 0;
+      auto max_pair = [](uint32_t a, uint32_t b) {   // of unsigned halves
+        typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+        return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+      };
+      uint32_t pair = 0;
+      const int ln = prompt_anew(lane), c = ln < SC ? ln : 0;
+      const uint4 d = prompt_lds16(scales0 + ((K ? 0 : SC) + c) * 16);
+      const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+      if (here == ~0ull) {
 #pragma unroll
-      for (int i = 0; i < SLOADS; ++i) {
-        const int u = i * 64 + prompt_anew(lane);
-        const uint4 d = prompt_lds16(scales0 + (K ? 0 : SLOADS * 1024) + u * 16);   // behind the last chunk: the first's
-        const uint32_t w[4] = {d.x, d.y, d.z, d.w};
-        if (here == ~0ull) {
+        for (int j = 0; j < 4; ++j) pair = max_pair(pair, w[j] & 0x7FFF7FFFu);
+      } else {   // behind the end: anything
 #pragma unroll
-          for (int j = 0; j < 4; ++j) t = max_word(t, max_word(w[j] & 0x7FFFu, w[j] >> 16 & 0x7FFFu));
-        } else {   // behind the end: anything
-          const int c = u < SC ? u : 0;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int slot = K ? (c * 8 + j) / NB : c % (T / 8) * 8 + j;
-            if (here >> slot & 1) t = max_word(t, w[j / 2] >> (j % 2 * 16) & 0x7FFFu);
-          }
+        for (int j = 0; j < 8; ++j) {
+          const int slot = K ? (c * 8 + j) / NB : c % (T / 8) * 8 + j;
+          if (here >> slot & 1) pair = max_pair(pair, w[j / 2] >> (j % 2 * 16) & 0x7FFFu);
         }
       }
-      t = max_word(t, dpp_word<0xB1>(t));
-      t = max_word(t, dpp_word<0x4E>(t));
-      t = max_word(t, dpp_word<0x141>(t));
-      t = max_word(t, dpp_word<0x140>(t));
-      t = max_word(max_word(lane_word(t, 0), lane_word(t, 16)), max_word(lane_word(t, 32), lane_word(t, 48)));
-      int e = 22 - (int)(t >> 10);   // an exponent field E: below 2^(E - 14)
+      pair = max_word(pair >> 16, pair & 0xFFFFu);
+      // the usual case: a greatest scale of 2^-7 to 2^8 before and now
+      if (__any(pair >= 8u << 10) && !__any(pair >= 23u << 10) && (K || ve == 0)) {
+        if (K) ke = 0;
+        first_v &= K;
+        return;
+      }
+      pair = max_word(pair, dpp_word<0xB1>(pair));
+      pair = max_word(pair, dpp_word<0x4E>(pair));
+      pair = max_word(pair, dpp_word<0x141>(pair));
+      pair = max_word(pair, dpp_word<0x140>(pair));
+      pair = max_word(max_word(lane_word(pair, 0), lane_word(pair, 16)), max_word(lane_word(pair, 32), lane_word(pair, 48)));
+      // an exponent field E: below 2^(E - 14). Scales of 2^-7 to 2^8 enter as they are.
+      const int E = (int)(pair >> 10);
+      int e = E >= 8 && E <= 22 ? 0 : 22 - E;
       e = e > 15 ? 15 : e < -8 ? -8 : e;
       if (K) ke = e;
-      else ve = e < ve ? e : ve;
+      else ve = first_v || e < ve ? e : ve;
+      if (!K) first_v = false;
     }
   };
   auto times = [](uint32_t x, uint32_t y) {
     return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, x) * __builtin_bit_cast(f16x2, y));
   };
-  // Run i of the codes to buffer buf.
-  auto convert = [&](auto is_k, int i, int buf, uint64_t here) {
+  // The runs of codes to buffer buf, each in three chunks of work: where it goes and its
+  // scales, the first eight codes, the others.
+  uint32_t to_lo = 0, bits = 0;
+  uint4 d0, d1;
+  auto convert = [&](auto is_k, int chunk, int buf, uint64_t here) {
     if constexpr (Q8) {
       constexpr bool K = decltype(is_k)::value;
-      const int u = i * 64 + prompt_anew(lane);
-      if (NB % 2 && u >= 32 * NB) return;
-      const uint4 raw = K ? k_raw[i] : v_raw[i];
-      const uint32_t mul = 0x00010001u * (uint32_t)((15 + (K ? ke : ve)) << 10);   // 2^e twice
-      uint4 lo = codes_f16(make_uint2(raw.x, raw.y)), hi = codes_f16(make_uint2(raw.z, raw.w));
-      uint32_t to, chunk, swizzle;
-      if constexpr (K) {
-        const int slot = 16 * wave + u / (2 * NB), r = (slot & ~31) | prompt_slot(slot & 31);
-        to = lds0 + buf * Tile::kBytes + r * (DIM * 2);
-        chunk = u % (2 * NB) * 2;
-        swizzle = Tile::k_swizzle(r);
-        uint32_t d = *reinterpret_cast<const __attribute__((address_space(3))) uint16_t*>(
-            scales0 + (slot * NB + u % (2 * NB) / 2) * 2);
-        d = times(d | d << 16, mul);
-        lo = make_uint4(times(lo.x, d), times(lo.y, d), times(lo.z, d), times(lo.w, d));
-        hi = make_uint4(times(hi.x, d), times(hi.y, d), times(hi.z, d), times(hi.w, d));
-      } else {
-        const int r = wave * 8 * NB + u / 4;
-        to = lds0 + (2 + buf) * Tile::kBytes + r * (T * 2);
-        chunk = u % 4 * 2;
-        swizzle = Tile::v_swizzle(r);
-        const uint32_t at = scales0 + SLOADS * 1024 + (r / 32 * (T / 8) + chunk) * 16;
-        const uint4 a0 = prompt_lds16(at), a1 = prompt_lds16(at + 16);
-        lo = make_uint4(times(lo.x, times(a0.x, mul)), times(lo.y, times(a0.y, mul)), times(lo.z, times(a0.z, mul)),
-                        times(lo.w, times(a0.w, mul)));
-        hi = make_uint4(times(hi.x, times(a1.x, mul)), times(hi.y, times(a1.y, mul)), times(hi.z, times(a1.z, mul)),
-                        times(hi.w, times(a1.w, mul)));
-        if (here != ~0ull) {   // behind the end: zero
-          const uint32_t bits = (uint32_t)(here >> (8 * chunk)) & 0xFFFFu;
-          auto keep = [&](int j) { return ((bits >> 2 * j & 1) ? 0xFFFFu : 0u) | ((bits >> 2 * j & 2) ? 0xFFFF0000u : 0u); };
-          lo = make_uint4(lo.x & keep(0), lo.y & keep(1), lo.z & keep(2), lo.w & keep(3));
-          hi = make_uint4(hi.x & keep(4), hi.y & keep(5), hi.z & keep(6), hi.w & keep(7));
+      const int i = chunk / 3, part = chunk % 3;
+      if (part == 0) {
+        const uint32_t mul = 0x00010001u * (uint32_t)((15 + (K ? ke : ve)) << 10);   // 2^e twice
+        uint32_t at;
+        if constexpr (K) {
+          if constexpr (POW2) {
+            // slots 8 further (NB 4) lie 4 rows further, whose swizzle is that of the first ^ 4
+            constexpr int kStep = 64 / (2 * NB);
+            const int r = kStep == 8 ? 4 * i : kStep == 4 ? (i & 1) * 8 + (i >> 1) * 4 : 0;
+            to_lo = (k_lo ^ (Tile::k_swizzle(r) << 4)) + r * (DIM * 2);
+          } else {
+            to_lo = k_target(i * 64 + prompt_anew(lane));
+          }
+          int u = i * 64 + prompt_anew(lane);
+          if (NB % 2 && u >= 32 * NB) u = 0;
+          at = scales0 + ((16 * wave + u / (2 * NB)) * NB + u % (2 * NB) / 2) * 2;
+          uint32_t d = *reinterpret_cast<const __attribute__((address_space(3))) uint16_t*>(at);
+          d |= d << 16;
+          if (ke != 0) d = times(d, mul);
+          d0 = d1 = make_uint4(d, d, d, d);
+        } else {
+          if constexpr (NB % 2 == 0) {
+            // sixteen dims further: the same swizzle
+            to_lo = v_lo + i * 16 * (T * 2);
+            at = scales0 + (SC + (wave * 8 * NB + i * 16) / 32 * (T / 8)) * 16 + prompt_anew(lane) % 4 * 32;
+          } else {
+            const int u = i * 64 + prompt_anew(lane);
+            to_lo = v_target(u);
+            at = scales0 + (SC + (u < 32 * NB ? (wave * 8 * NB + u / 4) / 32 * (T / 8) : 0) + u % 4 * 2) * 16;
+          }
+          d0 = prompt_lds16(at);
+          d1 = prompt_lds16(at + 16);
+          if (ve != 0) {
+            d0 = make_uint4(times(d0.x, mul), times(d0.y, mul), times(d0.z, mul), times(d0.w, mul));
+            d1 = make_uint4(times(d1.x, mul), times(d1.y, mul), times(d1.z, mul), times(d1.w, mul));
+          }
+          bits = (uint32_t)(here >> (prompt_anew(lane) % 4 * 16)) & 0xFFFFu;
         }
+        to_lo += buf * Tile::kBytes;
+        return;
       }
-      prompt_store16(to + ((chunk ^ swizzle) << 4), lo);
-      prompt_store16(to + (((chunk + 1) ^ swizzle) << 4), hi);
+      uint4 raw = v_raw[i];
+      if (K) raw = prompt_lds16(scales0 + kRaw + (NB % 2 && i * 64 + lane >= 32 * NB ? 0 : i * 1024 + lane * 16));
+      const uint4 d = part == 1 ? d0 : d1;
+      uint4 x = codes_f16(part == 1 ? make_uint2(raw.x, raw.y) : make_uint2(raw.z, raw.w));
+      x = make_uint4(times(x.x, d.x), times(x.y, d.y), times(x.z, d.z), times(x.w, d.w));
+      if (!K && here != ~0ull) {   // behind the end: zero
+        auto keep = [&](int j) {
+          return ((bits >> (8 * part - 8 + 2 * j) & 1) ? 0xFFFFu : 0u) | ((bits >> (8 * part - 8 + 2 * j) & 2) ? 0xFFFF0000u : 0u);
+        };
+        x = make_uint4(x.x & keep(0), x.y & keep(1), x.z & keep(2), x.w & keep(3));
+      }
+      if (NB % 2 && i * 64 + lane >= 32 * NB) return;
+      prompt_store16(part == 1 ? to_lo : to_lo ^ 16, x);
     }
   };
   using K_ = std::true_type;
   using V_ = std::false_type;
   auto convert_all = [&](auto is_k, int buf, uint64_t here) {
 #pragma unroll
-    for (int i = 0; i < RUNS; ++i) convert(is_k, i, buf, here);
+    for (int i = 0; i < 3 * RUNS; ++i) convert(is_k, i, buf, here);
   };
 
   // the group's tile and the one behind its next; all groups count alike
@@ -534,8 +603,9 @@ __global__ __launch_bounds__(kPromptThreads * GROUPS, NB <= 4 ? 2 : 1) void attn
       if (((v1 + T - 1) >> shift) - page0 >= 64) fetch_pages(v1 >> shift);
       issue(v1, BUF ^ 1);
     }
-    // Q8_0: K of the next tile is converted beside this one's first scores, its V beside
-    // the last products; K of the one behind is asked for before these.
+    // Q8_0: K of the next tile is converted beside this one's first scores, then K of the
+    // one behind is asked for; V of the next is asked for before and converted beside the
+    // last products.
     const bool more = Q8 && v1 < end;
     auto ask_k = [&]() {
       here0 = here1;
@@ -572,21 +642,21 @@ __global__ __launch_bounds__(kPromptThreads * GROUPS, NB <= 4 ? 2 : 1) void attn
     const bool edge = here != ~0ull || real0 < wr.far || real0 + T > wr.full;
     // matrix and vector units side by side, by halves of the tile
     // (behind the last tile old codes are converted once more, into a buffer no one reads)
-    using Convert = std::integral_constant<int, Q8 ? RUNS : 0>;
+    using Convert = std::integral_constant<int, Q8 ? 3 * RUNS : 0>;
     settle(K_{}, here1);
+    if (more) fetch(V_{}, v1);
     scores(kt, sa, Convert{}, [&](int c) { convert(K_{}, c, BUF ^ 1, here1); });
+    const uint64_t here_v = here1;
+    if (more) ask_k();
     if (edge) mask(sa, real0, (uint32_t)here);
     scores(kt + 32 * DIM * 2, sb, Softmax{}, [&](int c) { soften(sa, c); });
     weights(p);
     if (raise) rescale();
     if (edge) mask(sb, real0 + 32, (uint32_t)(here >> 32));
-    if (more) fetch(V_{}, v1);
     weigh(vt, 0, p, Softmax{}, [&](int c) { soften(sb, c); });
     weights(p);
     if (raise) rescale();
-    settle(V_{}, here1);
-    const uint64_t here_v = here1;
-    if (more) ask_k();
+    settle(V_{}, here_v);
     weigh(vt, 1, p, Convert{}, [&](int c) { convert(V_{}, c, BUF ^ 1, here_v); });
   };
   if (Q8 && mine(first) < end) {
