@@ -14,6 +14,7 @@ static int verify_plan(int64_t n_rows, int64_t n_seqs, int64_t vocab, bool draft
   if (n_rows < 0 || n_seqs < 0 || vocab < 1) return GGUF_QK_ERR_SHAPE;
   if (vocab > (int64_t(1) << 30) || n_seqs > 65535) return GGUF_QK_ERR_LIMIT;
   p->splits = (vocab + kVerifySplit - 1) / kVerifySplit;
+  if (p->splits > INT32_MAX / kDrawThreads) return GGUF_QK_ERR_LIMIT;
   const int64_t blocks = abi_mul(n_rows, p->splits);
   if (blocks < 0 || blocks > INT32_MAX / kVerifyThreads) return GGUF_QK_ERR_LIMIT;   // threads of a grid axis
   p->part_bytes = blocks * (draft ? 2 : 1) * (int64_t)sizeof(double2);
@@ -31,10 +32,11 @@ static int launch_verify(const VerifyArgs& a, hipStream_t stream) {
     const int st = abi_launched();
     if (st) return st;
   }
-  hipLaunchKernelGGL((verify_choose_kernel<BF16, WIDE>), dim3((unsigned)a.splits, (unsigned)a.n_seqs), block, 0, stream, a);
+  hipLaunchKernelGGL((verify_choose_kernel<BF16, WIDE>), dim3((unsigned)a.splits, (unsigned)a.n_seqs), dim3(kDrawThreads),
+                     0, stream, a);
   const int st = abi_launched();
   if (st || a.n_rows == 0) return st;
-  hipLaunchKernelGGL(verify_draw_kernel<BF16>, dim3((unsigned)a.n_seqs), block, 0, stream, a);
+  hipLaunchKernelGGL((verify_draw_kernel<BF16, WIDE>), dim3((unsigned)a.n_seqs), dim3(kDrawThreads), 0, stream, a);
   return abi_launched();
 }
 

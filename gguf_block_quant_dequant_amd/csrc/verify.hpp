@@ -46,11 +46,11 @@ struct VerifyArgs {
   int32_t n_seqs, vocab, splits;
 };
 
-constexpr int kVerifyThreads = 256;
+constexpr int kVerifyThreads = 256;   // of the sums: 32 values each, all loads in flight
 constexpr int kVerifyWaves = kVerifyThreads / 64;
-constexpr int kVerifyPer = 32;
-constexpr int kVerifySplit = kVerifyThreads * kVerifyPer;
-constexpr int kVerifyAhead = 4;
+constexpr int kVerifySplit = kVerifyThreads * 32;
+constexpr int kDrawThreads = 1024;    // of the others, 8 values each: few blocks, whose latency counts
+constexpr int kDrawWaves = kDrawThreads / 64;
 
 // 2^z for z <= 0: 2^k 2^f with |f| <= 1/2 and the series of e^(f ln 2) to its tenth
 // power (the next term is below 2^-42). -inf gives 0.
@@ -107,43 +107,41 @@ __device__ __forceinline__ float verify_at(const VerifyArgs& a, int which, int64
   else return reinterpret_cast<const float*>(a.x[which])[at];
 }
 
-// A thread's 32 values of a split. WIDE: in 16-byte words (rows aligned), else one by
-// one; neighbouring threads hold neighbouring words. -inf behind the vocabulary.
-template <bool BF16, bool WIDE>
+// A thread's values of a split. WIDE: in 16-byte words (rows aligned), else one by one;
+// neighbouring threads hold neighbouring words. -inf behind the vocabulary.
+template <bool BF16, bool WIDE, int THREADS>
 struct VerifyValues {
-  static constexpr int VE = !WIDE ? 1 : BF16 ? 8 : 4;
-  float x[kVerifyPer];
+  static constexpr int VE = !WIDE ? 1 : BF16 ? 8 : 4, PER = kVerifySplit / THREADS;
+  float x[PER];
   // index in the split of value j
-  __device__ static __forceinline__ int index(int j, int tid) {
-    return (j / VE * kVerifyThreads + tid) * VE + j % VE;
-  }
+  __device__ static __forceinline__ int index(int j, int tid) { return (j / VE * THREADS + tid) * VE + j % VE; }
   __device__ __forceinline__ void load(const VerifyArgs& a, int which, int64_t row, int split, int tid) {
     const int64_t first = (int64_t)split * kVerifySplit;
     const int left = a.vocab - first < kVerifySplit ? (int)(a.vocab - first) : kVerifySplit;
-    const uint8_t* base = a.x[which] + (row * a.stride[which] + first) * (BF16 ? 2 : 4);
-    if (WIDE && left == kVerifySplit) {
-      uint4 w[kVerifyPer / VE];
+    if constexpr (WIDE) {
+      if (left == kVerifySplit) {
+        const uint8_t* base = a.x[which] + (row * a.stride[which] + first) * (BF16 ? 2 : 4);
+        uint4 w[PER / VE];
 #pragma unroll
-      for (int v = 0; v < kVerifyPer / VE; ++v) w[v] = reinterpret_cast<const uint4*>(base)[v * kVerifyThreads + tid];
+        for (int v = 0; v < PER / VE; ++v) w[v] = reinterpret_cast<const uint4*>(base)[v * THREADS + tid];
 #pragma unroll
-      for (int v = 0; v < kVerifyPer / VE; ++v) {
-        const uint32_t u[4] = {w[v].x, w[v].y, w[v].z, w[v].w};
+        for (int v = 0; v < PER / VE; ++v) {
+          const uint32_t u[4] = {w[v].x, w[v].y, w[v].z, w[v].w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if constexpr (BF16) {
-            if constexpr (VE == 8) {
+          for (int j = 0; j < 4; ++j) {
+            if constexpr (BF16) {
               x[8 * v + 2 * j] = __uint_as_float(u[j] << 16);
               x[8 * v + 2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+            } else {
+              x[4 * v + j] = __uint_as_float(u[j]);
             }
-          } else if constexpr (VE == 4) {
-            x[4 * v + j] = __uint_as_float(u[j]);
           }
         }
+        return;
       }
-      return;
     }
 #pragma unroll
-    for (int j = 0; j < kVerifyPer; ++j) {
+    for (int j = 0; j < PER; ++j) {
       const int i = index(j, tid);
       x[j] = i < left ? verify_at<BF16>(a, which, row, first + i) : -__builtin_inff();
     }
@@ -155,7 +153,8 @@ __global__ __launch_bounds__(kVerifyThreads) void verify_sums_kernel(const Verif
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, which = blockIdx.y;
   const int64_t row = blockIdx.x / (uint32_t)a.splits;
   const int split = blockIdx.x % (uint32_t)a.splits;
-  VerifyValues<BF16, WIDE> v;
+  using Values = VerifyValues<BF16, WIDE, kVerifyThreads>;
+  Values v;
   if (which == 0) v.load(a, 0, row, split, tid);   // in flight while the sequence is found
   const RowTile seq = find_row(a.row_start, a.n_seqs, a.n_rows, row, lane);
   if (seq.seq < 0) return;
@@ -167,7 +166,7 @@ __global__ __launch_bounds__(kVerifyThreads) void verify_sums_kernel(const Verif
   float m = -__builtin_inff();
   bool nan = false;
 #pragma unroll
-  for (int j = 0; j < kVerifyPer; ++j) {
+  for (int j = 0; j < Values::PER; ++j) {
     m = fmaxf(m, v.x[j]);
     nan |= v.x[j] != v.x[j];
   }
@@ -183,15 +182,15 @@ __global__ __launch_bounds__(kVerifyThreads) void verify_sums_kernel(const Verif
   if (t == 0.0) {
     int best = kVerifySplit;
 #pragma unroll
-    for (int j = kVerifyPer - 1; j >= 0; --j) {
-      const int i = VerifyValues<BF16, WIDE>::index(j, tid);
+    for (int j = Values::PER - 1; j >= 0; --j) {
+      const int i = Values::index(j, tid);
       if (v.x[j] == m) best = i;   // a thread's indices ascend
     }
     s = -wave_max_f64(-(double)best);
   } else if (m > -__builtin_inff() && m < __builtin_inff()) {
     const double c = verify_scale(t), dm = (double)m;
 #pragma unroll
-    for (int j = 0; j < kVerifyPer; ++j) s += exp2_f64(((double)v.x[j] - dm) * c);
+    for (int j = 0; j < Values::PER; ++j) s += exp2_f64(((double)v.x[j] - dm) * c);
     s = wave_sum_f64(s);
   }
   if (lane == 0) wave_s[wave] = s;
@@ -206,31 +205,36 @@ __global__ __launch_bounds__(kVerifyThreads) void verify_sums_kernel(const Verif
   a.part[((int64_t)which * a.n_rows + row) * a.splits + split] = make_double2((double)m, s);
 }
 
-// Maximum and sum of a row over its splits (T > 0), by one wave; every lane returns
-// them. The maximum is not finite for a row without a finite greatest logit.
-__device__ __forceinline__ double2 verify_join(const VerifyArgs& a, int which, int64_t row, double c, int lane) {
-  const double2* p = a.part + ((int64_t)which * a.n_rows + row) * a.splits;
-  double m = -__builtin_inf();
-  for (int i = lane; i < a.splits; i += 64) m = p[i].x > m ? p[i].x : m;
-  m = wave_max_f64(m);
-  double s = 0.0;
-  for (int i = lane; i < a.splits; i += 64) s = fma(p[i].y, exp2_f64((p[i].x - m) * c), s);
-  return make_double2(m, wave_sum_f64(s));
+// Sixteen lanes' maximum and sum; every lane of them returns it.
+__device__ __forceinline__ double row16_max(double v) {
+#pragma unroll
+  for (int d = 8; d >= 1; d >>= 1) {
+    const double o = __shfl_xor(v, d);
+    v = o > v ? o : v;
+  }
+  return v;
 }
-// The greatest value and its lowest index (T = 0).
-__device__ __forceinline__ double2 verify_best(const VerifyArgs& a, int64_t row, int lane) {
-  const double2* p = a.part + row * a.splits;
-  double m = -__builtin_inf(), at = (double)a.vocab;
-  for (int i = lane; i < a.splits; i += 64)
-    if (p[i].x > m) m = p[i].x, at = p[i].y;
-  const double top = wave_max_f64(m);
-  return make_double2(top, -wave_max_f64(m == top ? -at : -(double)a.vocab));
+__device__ __forceinline__ double row16_sum(double v) {
+#pragma unroll
+  for (int d = 8; d >= 1; d >>= 1) v += __shfl_xor(v, d);
+  return v;
 }
 __device__ __forceinline__ bool finite_f64(double v) { return v - v == 0.0; }
 
+// What became of one row.
+struct VerifyRow {
+  VerifyChoice choice;
+  float prob;
+  int32_t ok, best;
+};
+
+// First every block judges its sequence's rows, sixteen lanes for the target's sums of a
+// row and sixteen for the draft's, 32 rows at a time; then it sums its split.
 template <bool BF16, bool WIDE>
-__global__ __launch_bounds__(kVerifyThreads) void verify_choose_kernel(const VerifyArgs a) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+__global__ __launch_bounds__(kDrawThreads) void verify_choose_kernel(const VerifyArgs a) {
+  using Values = VerifyValues<BF16, WIDE, kDrawThreads>;
+  constexpr int kRows = kDrawThreads / 32;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = tid & 15;
   const int s = blockIdx.y, split = blockIdx.x;
   const SeqRows seq = seq_rows(a.row_start, s, a.n_rows);
   if (seq.rows == 0) {
@@ -242,78 +246,94 @@ __global__ __launch_bounds__(kVerifyThreads) void verify_choose_kernel(const Ver
     return;
   }
   const double t = verify_temperature(a, s), c = t > 0.0 ? verify_scale(t) : 0.0;
-  __shared__ int first_of[kVerifyWaves];
-  __shared__ VerifyChoice chosen_of[kVerifyWaves];
-  __shared__ int best_of[kVerifyWaves];
-  __shared__ double sums[kVerifyWaves];
-  // every wave takes rows in turn up to its first that is not accepted; the block
-  // that writes accept_prob goes through all of them
-  const bool writes = split == 0 && a.prob;
+  __shared__ VerifyRow judged[kRows];
+  __shared__ double sums[kDrawWaves];
+  const bool writes = split == 0 && a.prob;   // goes through all rows
   int first = seq.rows;
-  for (int j = wave; j < seq.rows; j += kVerifyWaves) {
-    const int64_t row = (int64_t)seq.row0 + j;
+  VerifyChoice ch;
+  int best_token = -1;
+  for (int j0 = 0; j0 < seq.rows && (first == seq.rows || writes); j0 += kRows) {
+    __syncthreads();   // judged[] is free
+    const int j = j0 + tid / 32, which = tid >> 4 & 1;
+    const bool live = j < seq.rows;
+    const int64_t row = (int64_t)seq.row0 + (live ? j : 0);
     const bool last = j == seq.rows - 1;
-    const int64_t token = last ? 0 : a.tokens[row];
+    const int64_t token = live && !last ? a.tokens[row] : -1;
     const bool known = token >= 0 && token < a.vocab;
-    VerifyChoice ch;
-    ch.mp = ch.mq = ch.ip = ch.iq = 0.0;
-    ch.row = row;
-    ch.mode = kDrawP;
-    ch.pad = 0;
-    int best = -1;
-    bool ok = false;
-    float prob = 0.f;
+    const bool use = live && (which == 0 || (a.x[1] && !last && t > 0.0));
+    float logit = 0.f;
+    if (use && known) logit = verify_at<BF16>(a, which, row, token);
+    const double2* part = a.part + ((int64_t)which * a.n_rows + row) * a.splits;
+    double m = -__builtin_inf(), at = (double)a.vocab;
+    if (use) {
+      for (int i = l16; i < a.splits; i += 16) {
+        const double2 p = part[i];
+        if (p.x > m) m = p.x, at = p.y;   // (T = 0: its lowest index; a lane's splits ascend)
+      }
+    }
+    const double top = row16_max(m);
+    double sum = 0.0;
     if (t == 0.0) {
-      const double2 b = verify_best(a, row, lane);
-      best = finite_f64(b.x) ? (int)b.y : -1;
-      ok = !last && best >= 0 && (int64_t)best == token;
-      prob = (last && best >= 0) || ok ? 1.f : 0.f;
-      ch.row = -1;
+      sum = -row16_max(m == top ? -at : -(double)a.vocab);
     } else {
-      const double2 p = verify_join(a, 0, row, c, lane);
-      bool valid = finite_f64(p.x);
-      ch.mp = p.x;
-      ch.ip = 1.0;
-      if (last) {
-        prob = valid ? 1.f : 0.f;
+      if (use)
+        for (int i = l16; i < a.splits; i += 16) sum = fma(part[i].y, exp2_f64((part[i].x - top) * c), sum);
+      sum = row16_sum(sum);
+    }
+    const double share = use && known && t > 0.0 ? exp2_f64(((double)logit - top) * c) / sum : 0.0;
+    const double q_top = __shfl_xor(top, 16), q_sum = __shfl_xor(sum, 16), q_share = __shfl_xor(share, 16);
+    if (live && which == 0 && l16 == 0) {
+      VerifyRow r;
+      r.choice.mp = top;
+      r.choice.mq = r.choice.iq = 0.0;
+      r.choice.ip = 1.0;
+      r.choice.row = row;
+      r.choice.mode = kDrawP;
+      r.choice.pad = 0;
+      r.best = -1;
+      bool valid = finite_f64(top), ok = false;
+      if (t == 0.0) {
+        r.best = valid ? (int)sum : -1;
+        ok = !last && valid && (int64_t)r.best == token;
+        r.prob = (last && valid) || ok ? 1.f : 0.f;
+        valid = false;   // nothing to draw
+      } else if (last) {
+        r.prob = valid ? 1.f : 0.f;
       } else {
-        const double pt = valid && known ? exp2_f64(((double)verify_at<BF16>(a, 0, row, token) - p.x) * c) / p.y : 0.0;
         double qt = known ? 1.0 : 0.0;
-        ch.mode = kDrawOneHot;
         if (a.x[1]) {
-          const double2 q = verify_join(a, 1, row, c, lane);
-          valid = valid && finite_f64(q.x);
-          ch.mode = kDrawRest;
-          ch.ip = 1.0 / p.y;
-          ch.mq = q.x;
-          ch.iq = 1.0 / q.y;
-          qt = valid && known ? exp2_f64(((double)verify_at<BF16>(a, 1, row, token) - q.x) * c) / q.y : 0.0;
+          valid = valid && finite_f64(q_top);
+          r.choice.mode = kDrawRest;
+          r.choice.ip = 1.0 / sum;
+          r.choice.mq = q_top;
+          r.choice.iq = 1.0 / q_sum;
+          qt = q_share;
+        } else if (known) {
+          r.choice.mode = kDrawOneHot;
         }
-        ok = valid && known && (double)a.uniform[row] * qt < pt;
-        prob = !(valid && known) ? 0.f : pt >= qt ? (pt > 0.0 ? 1.f : 0.f) : (float)(pt / qt);
-        if (ch.mode == kDrawOneHot && !known) ch.mode = kDrawP;
+        ok = valid && known && (double)a.uniform[row] * qt < share;
+        r.prob = !(valid && known) ? 0.f : share >= qt ? (share > 0.0 ? 1.f : 0.f) : (float)(share / qt);
       }
-      if (!valid) ch.row = -1;
+      if (!valid) r.choice.row = -1;
+      r.ok = ok;
+      judged[j - j0] = r;
+      if (writes) a.prob[row] = r.prob;
     }
-    if (writes && lane == 0) a.prob[row] = prob;
-    if (!ok && j < first) {
-      first = j;
-      if (lane == 0) {
-        chosen_of[wave] = ch;
-        best_of[wave] = best;
+    __syncthreads();
+    if (first == seq.rows) {
+      const int n = seq.rows - j0 < kRows ? seq.rows - j0 : kRows;
+      const uint64_t refused = __ballot(lane < n && !judged[lane < n ? lane : 0].ok);
+      if (refused) {
+        const int at0 = __builtin_ctzll(refused);
+        first = j0 + at0;
+        ch = judged[at0].choice;
+        best_token = judged[at0].best;
       }
     }
-    if (first < seq.rows && !writes) break;
   }
-  if (lane == 0) first_of[wave] = first;
-  __syncthreads();
-  int at = 0;
-#pragma unroll
-  for (int w = 1; w < kVerifyWaves; ++w) at = first_of[w] < first_of[at] ? w : at;
-  const VerifyChoice ch = chosen_of[at];
   if (split == 0 && tid == 0) {
-    a.accepted[s] = first_of[at];
-    a.next[s] = best_of[at];
+    a.accepted[s] = first;
+    a.next[s] = best_token;
     a.choice[s] = ch;
   }
   if (ch.row < 0) return;
@@ -325,112 +345,142 @@ __global__ __launch_bounds__(kVerifyThreads) void verify_choose_kernel(const Ver
     }
     return;
   }
-  VerifyValues<BF16, WIDE> p, q;
+  Values p, q;
   p.load(a, 0, ch.row, split, tid);
   double sum = 0.0;
   if (ch.mode == kDrawRest) {
     q.load(a, 1, ch.row, split, tid);
-#pragma unroll kVerifyAhead
-    for (int j = 0; j < kVerifyPer; ++j)
+#pragma unroll
+    for (int j = 0; j < Values::PER; ++j)
       sum += verify_rest(exp2_f64(((double)p.x[j] - ch.mp) * c), ch.ip, exp2_f64(((double)q.x[j] - ch.mq) * c), ch.iq);
   } else {
     const int token = a.tokens[ch.row] - split * kVerifySplit;
-#pragma unroll kVerifyAhead
-    for (int j = 0; j < kVerifyPer; ++j) {
+#pragma unroll
+    for (int j = 0; j < Values::PER; ++j) {
       const double r = exp2_f64(((double)p.x[j] - ch.mp) * c);
-      sum += VerifyValues<BF16, WIDE>::index(j, tid) == token ? 0.0 : r;
+      sum += Values::index(j, tid) == token ? 0.0 : r;
     }
   }
   sum = wave_sum_f64(sum);
   if (lane == 0) sums[wave] = sum;
   __syncthreads();
-  if (tid == 0) *rest = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+  if (tid == 0) {
+    sum = 0.0;
+    for (int w = 0; w < kDrawWaves; ++w) sum += sums[w];
+    *rest = sum;
+  }
 }
 
-// What value i of the chosen row weighs.
-template <bool BF16>
-__device__ __forceinline__ double verify_weight(const VerifyArgs& a, const VerifyChoice& ch, double c, int64_t i) {
-  const double p = exp2_f64(((double)verify_at<BF16>(a, 0, ch.row, i) - ch.mp) * c);
-  if (ch.mode == kDrawRest)
-    return verify_rest(p, ch.ip, exp2_f64(((double)verify_at<BF16>(a, 1, ch.row, i) - ch.mq) * c), ch.iq);
-  return ch.mode == kDrawOneHot && i == a.tokens[ch.row] ? 0.0 : p;
+// What value i of the chosen row weighs, its logits given.
+__device__ __forceinline__ double verify_weight(const VerifyArgs& a, const VerifyChoice& ch, double c, float x, float y,
+                                                bool token) {
+  const double p = exp2_f64(((double)x - ch.mp) * c);
+  if (ch.mode == kDrawRest) return verify_rest(p, ch.ip, exp2_f64(((double)y - ch.mq) * c), ch.iq);
+  return ch.mode == kDrawOneHot && token ? 0.0 : p;
 }
 
-template <bool BF16>
-__global__ __launch_bounds__(kVerifyThreads) void verify_draw_kernel(const VerifyArgs a) {
+// Inclusive sum over the lanes of a wave.
+__device__ __forceinline__ double wave_scan_f64(double v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const double o = __shfl_up(v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
+template <bool BF16, bool WIDE>
+__global__ __launch_bounds__(kDrawThreads) void verify_draw_kernel(const VerifyArgs a) {
+  using Values = VerifyValues<BF16, WIDE, kDrawThreads>;
+  constexpr int PER = Values::PER;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, s = blockIdx.x;
   VerifyChoice ch = a.choice[s];
   if (ch.row < 0) return;
   const double c = verify_scale(verify_temperature(a, s)), u = (double)a.uniform_next[s];
   const double* rest = a.rest + (int64_t)s * a.splits;
   const double2* part = a.part + ch.row * a.splits;
-  // every thread runs through the splits' sums
-  double total = 0.0;
-  for (int i = 0; i < a.splits; ++i) total += rest[i];
-  const bool all = !(total > 0.0) && ch.mode != kDrawP;   // p - q is nowhere above 0
-  if (all) {
+  bool all = false;   // p - q is nowhere above 0: from p
+  auto split_sum = [&](int i) -> double {
+    if (i >= a.splits) return 0.0;
+    return all ? part[i].y * exp2_f64((part[i].x - ch.mp) * c) : rest[i];
+  };
+  // every wave goes through the splits' sums, 64 at a time
+  auto whole = [&]() {
+    double sum = 0.0;
+    for (int i = 0; i < a.splits; i += 64) sum += wave_sum_f64(split_sum(i + lane));
+    return sum;
+  };
+  double total = whole();
+  if (!(total > 0.0) && ch.mode != kDrawP) {
+    all = true;
     ch.mode = kDrawP;
-    ch.ip = 1.0;
-    total = 0.0;
+    total = whole();
   }
-  auto split_sum = [&](int i) { return all ? part[i].y * exp2_f64((part[i].x - ch.mp) * c) : rest[i]; };
-  if (all)
-    for (int i = 0; i < a.splits; ++i) total += split_sum(i);
   const double goal = u * total;
-  double before = 0.0;
+  double before = 0.0, run = 0.0, last_before = 0.0;
   int split = -1, last = 0;
-  double last_before = 0.0;
-  for (int i = 0; i < a.splits; ++i) {
-    const double w = split_sum(i);
-    if (w > 0.0) last = i, last_before = before;
-    if (before + w > goal && split < 0) {
-      split = i;
-      break;
+  for (int i = 0; i < a.splits && split < 0; i += 64) {
+    const double w = split_sum(i + lane), upto = wave_scan_f64(w, lane);
+    const uint64_t hit = __ballot(run + upto > goal && w > 0.0), any = __ballot(w > 0.0);
+    if (hit) {
+      split = i + __builtin_ctzll(hit);
+      before = run + __shfl(upto - w, __builtin_ctzll(hit));
     }
-    before += w;
+    if (any) {
+      const int at = 63 - __builtin_clzll(any);
+      last = i + at;
+      last_before = run + __shfl(upto - w, at);
+    }
+    run += __shfl(upto, 63);
   }
   if (split < 0) split = last, before = last_before;   // rounding at the very end
-  const int64_t first = (int64_t)split * kVerifySplit + tid * kVerifyPer;
-  const int n = a.vocab - first < kVerifyPer ? (int)(a.vocab - first < 0 ? 0 : a.vocab - first) : kVerifyPer;
-  double sum = 0.0;
-  int64_t tail = -1;   // last value with any weight
-  for (int j = 0; j < n; ++j) {
-    const double w = verify_weight<BF16>(a, ch, c, first + j);
-    if (w > 0.0) tail = first + j;
-    sum += w;
-  }
-  // exclusive sums over the threads, in order
-  double upto = sum;
+  // The split's logits in LDS, in order: thread t weighs values PER t .. (a word of pad per PER).
+  __shared__ float logits[2][kVerifySplit + kVerifySplit / PER];
+  const bool two = ch.mode == kDrawRest;
+  for (int k = 0; k < (two ? 2 : 1); ++k) {
+    Values v;
+    v.load(a, k, ch.row, split, tid);
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const double o = __shfl_up(upto, d);
-    if (lane >= d) upto += o;
+    for (int j = 0; j < PER; ++j) {
+      const int i = Values::index(j, tid);
+      logits[k][i + i / PER] = v.x[j];
+    }
   }
-  __shared__ double wave_sum[kVerifyWaves];
-  __shared__ int hit[kVerifyWaves], end[kVerifyWaves];
+  __syncthreads();
+  const int token = ch.mode == kDrawOneHot ? a.tokens[ch.row] - split * kVerifySplit : -1;
+  double w[PER], sum = 0.0;
+  int tail = -1;   // last value with any weight
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int i = tid * PER + j, at = i + i / PER;
+    w[j] = verify_weight(a, ch, c, logits[0][at], two ? logits[1][at] : 0.f, i == token);
+    if (w[j] > 0.0) tail = j;
+    sum += w[j];
+  }
+  const double upto = wave_scan_f64(sum, lane);
+  __shared__ double wave_sum[kDrawWaves];
+  __shared__ int hit[kDrawWaves], end[kDrawWaves];
   if (lane == 63) wave_sum[wave] = upto;
   __syncthreads();
-  double run = before;
-  for (int w = 0; w < wave; ++w) run += wave_sum[w];
-  const double reach = run + upto;
+  run = before;
+  for (int v = 0; v < wave; ++v) run += wave_sum[v];
+  const bool reached = run + upto > goal;
   run += upto - sum;
-  int64_t found = -1;
-  if (reach > goal) {
-    for (int j = 0; j < n && found < 0; ++j) {
-      const double w = verify_weight<BF16>(a, ch, c, first + j);
-      run += w;
-      if (w > 0.0 && run > goal) found = first + j;
-    }
+  int found = -1;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    run += w[j];
+    if (found < 0 && reached && w[j] > 0.0 && run > goal) found = j;
   }
   const uint64_t any = __ballot(found >= 0), ends = __ballot(tail >= 0);
   if (lane == 0) hit[wave] = any ? __builtin_ctzll(any) : -1, end[wave] = ends ? 63 - __builtin_clzll(ends) : -1;
   __syncthreads();
   int from = -1, to = -1;
-  for (int w = kVerifyWaves - 1; w >= 0; --w) {
-    if (hit[w] >= 0) from = w * 64 + hit[w];
-    if (end[w] >= 0 && to < 0) to = w * 64 + end[w];
+  for (int v = kDrawWaves - 1; v >= 0; --v) {
+    if (hit[v] >= 0) from = v * 64 + hit[v];
+    if (end[v] >= 0 && to < 0) to = v * 64 + end[v];
   }
-  if (from >= 0 ? tid == from : tid == to) a.next[s] = (int32_t)(from >= 0 ? found : tail);
+  if (from >= 0 ? tid == from : tid == to) a.next[s] = split * kVerifySplit + tid * PER + (from >= 0 ? found : tail);
 }
 
 }  // namespace gqk
