@@ -56,6 +56,9 @@ struct AttnRowsArgs : AttnArgs {
   int64_t n_rows;
   int32_t sinks;
   int32_t bf16;               // q and out: BF16, not F32 (strides in elements)
+  int32_t columns, unit;      // of a block; the unit of TileRange
+  int32_t fill;               // blocks aimed for; chunks by the lengths (fill > 0): at most 64 sequences
+  int32_t round, least;       // chunks are multiples of `round` and no less than `least`
 };
 
 constexpr int kAttnJ = 8;                 // positions of a lane
@@ -105,6 +108,95 @@ __device__ __forceinline__ int attn_chunk(const AttnArgs& a, int lane) {
   c = (c + kRound - 1) / kRound * kRound;
   c = c < kAttnLeast ? kAttnLeast : c;
   return c < a.chunk ? c : a.chunk;   // splits * a.chunk covers any length
+}
+
+// The same for several new tokens: chunks such that all column tiles of all sequences
+// make about a.fill blocks, and that the launched splits cover each. A lane's sequence
+// has these rows and slots. (Positions are split where the tiles times kv heads are fewer
+// than the blocks aimed for: their sums in units of 64 stay below 2^30.)
+template <int COLS>
+__device__ __forceinline__ int attn_rows_chunk(const AttnRowsArgs& a, const SeqRows& r, int held) {
+  uint32_t total = 0, most = 0;
+  if (r.rows > 0) {
+    const int width = r.rows * a.group;   // all its columns as one tile: no tile reads more
+    const TileRange t = tile_range(held, r.rows, a.group, 0, width, a.window, a.sinks, a.unit);
+    most = t.n > 0 ? t.n : 0;
+    total = (most + 63) / 64 * ((width + COLS - 1) / COLS);
+  }
+  auto step = [&](uint32_t t, uint32_t m) {
+    total += t;
+    most = max_word(most, m);
+  };
+  step(dpp_word<0xB1>(total), dpp_word<0xB1>(most));
+  step(dpp_word<0x4E>(total), dpp_word<0x4E>(most));
+  step(dpp_word<0x141>(total), dpp_word<0x141>(most));
+  step(dpp_word<0x140>(total), dpp_word<0x140>(most));
+  total = lane_word(total, 0) + lane_word(total, 16) + lane_word(total, 32) + lane_word(total, 48);
+  most = max_word(max_word(lane_word(most, 0), lane_word(most, 16)), max_word(lane_word(most, 32), lane_word(most, 48)));
+  uint32_t c = (total * (uint32_t)a.c.hkv / (uint32_t)a.fill + 1) * 64;
+  const uint32_t cover = (most + a.splits - 1) / a.splits;
+  c = c > cover ? c : cover;
+  c = c < (uint32_t)a.least ? a.least : c;
+  c = (c + a.round - 1) / a.round * a.round;
+  return (int)(c < (uint32_t)a.chunk ? c : a.chunk);   // splits * a.chunk covers any length
+}
+// For a block that knows its sequence: the chunk alone. All 64 lanes of a wave call it.
+template <int COLS>
+__device__ __forceinline__ int attn_rows_chunk(const AttnRowsArgs& a, int lane) {
+  if (a.fill == 0) return a.chunk;
+  SeqRows r = {0, 0};
+  int held = 0;
+  if (lane < a.n_seqs) {
+    r = seq_rows(a.row_start, lane, a.n_rows);
+    held = (int)kv_length(a.lengths[lane], a.max_len, a.table_stride, a.c.shift);
+  }
+  return attn_rows_chunk<COLS>(a, r, held);
+}
+
+// Where a block of COLS columns stands: tile `target` of all sequences' (seq -1: behind the
+// last), its sequence's slots, the chunk. All 64 lanes of a wave call it.
+struct RowsPlan {
+  RowTile t;
+  int32_t held, chunk;
+};
+template <int COLS>
+__device__ __forceinline__ RowsPlan attn_rows_plan(const AttnRowsArgs& a, int target, int lane) {
+  RowsPlan p;
+  p.held = 0;
+  p.chunk = a.chunk;
+  if (a.n_seqs > 64) {
+    p.t = find_row_tile(a.row_start, a.n_seqs, a.n_rows, a.group, COLS, target, lane);
+    if (p.t.seq >= 0) p.held = (int)kv_length(a.lengths[p.t.seq], a.max_len, a.table_stride, a.c.shift);
+    return p;
+  }
+  // one sequence per lane: every load at once
+  SeqRows r = {0, 0};
+  int held = 0;
+  if (lane < a.n_seqs) {
+    held = a.lengths[lane];
+    r = seq_rows(a.row_start, lane, a.n_rows);
+    held = (int)kv_length(held, a.max_len, a.table_stride, a.c.shift);
+  }
+  const int own = (r.rows * a.group + COLS - 1) / COLS;
+  int upto = own;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(upto, d);
+    if (lane >= d) upto += o;
+  }
+  const uint64_t past = __ballot(upto > target);
+  if (a.fill != 0) p.chunk = attn_rows_chunk<COLS>(a, r, held);
+  if (!past) {
+    p.t = {-1, 0, 0, 0};
+    return p;
+  }
+  const int l = __builtin_ctzll(past);
+  p.t.seq = l;
+  p.t.tile = target - __builtin_amdgcn_readlane(upto - own, l);
+  p.t.row0 = __builtin_amdgcn_readlane(r.row0, l);
+  p.t.rows = __builtin_amdgcn_readlane(r.rows, l);
+  p.held = __builtin_amdgcn_readlane(held, l);
+  return p;
 }
 
 // Two values rounded to fp16 (nearest-even), in one instruction.
@@ -217,13 +309,15 @@ __device__ __forceinline__ void each_block(Fn&& fn) {
 
 // One block: a chunk of one sequence's positions, up to 16 query heads of one
 // kv head; its waves take the chunk's tiles in turn and join in LDS.
-// ARGS AttnRowsArgs: up to 16 (row, query head) pairs, each with positions of its
+// ARGS AttnRowsArgs: up to 16 CT (row, query head) pairs, each with positions of its
 // own (SlotRange); the tile's positions are numbered without the stretch between
-// the first slots and the window, so that the chunks cover only what is read.
-template <int KIND, int NB, bool TRACK, class ARGS = AttnArgs>
+// the first slots and the window, so that the chunks cover only what is read. CT 2: two
+// tiles of columns beside one read of K and V.
+template <int KIND, int NB, bool TRACK, class ARGS = AttnArgs, int CT = 1>
 __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const ARGS a) {
   constexpr bool ROWS = std::is_same<ARGS, AttnRowsArgs>::value;
-  static_assert(!(ROWS && TRACK), "weights are tracked for one token per sequence");
+  static_assert(!(ROWS && TRACK) && (ROWS || CT == 1), "weights are tracked for one token per sequence");
+  constexpr int COLS = 16 * CT;
   constexpr int DIM = NB * 32;
   constexpr int NT = 2 * NB;   // 16-dim tiles of the output
   constexpr int J = kAttnJ, TILE = kAttnTile, WORDS = 4 * NB, NW = (WORDS + 15) / 16;
@@ -242,15 +336,17 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const ARGS a)
   // with the turn 203; 64 of 0 .. 4096, 4 heads: 68.5, 66.5).
   const int split = blockIdx.z;
   int s, h, ht, row0 = 0, rows = 1;   // ht: tile of columns; ROWS: the sequence's rows
+  int row_held = 0, row_chunk = 0;
   if constexpr (ROWS) {
     h = blockIdx.x;
-    const RowTile t = find_row_tile(a.row_start, a.n_seqs, a.n_rows, a.group, 16,
-                                    (int)((blockIdx.y + blockIdx.z) % gridDim.y), lane);
-    if (t.seq < 0) return;
-    s = t.seq;
-    ht = t.tile;
-    row0 = t.row0;
-    rows = t.rows;
+    const RowsPlan p = attn_rows_plan<COLS>(a, (int)((blockIdx.y + blockIdx.z) % gridDim.y), lane);
+    if (p.t.seq < 0) return;
+    s = p.t.seq;
+    ht = p.t.tile;
+    row0 = p.t.row0;
+    rows = p.t.rows;
+    row_held = p.held;
+    row_chunk = p.chunk;
   } else {
     s = (int)((blockIdx.y + blockIdx.z) % (uint32_t)a.n_seqs);
     h = blockIdx.x / a.head_tiles;
@@ -259,21 +355,25 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const ARGS a)
   // The chunk's page ids, one per lane (a chunk spans at most 64 pages). Without
   // a window and with a chunk known beforehand they are asked for beside the
   // length, not behind it.
-  const int32_t length = a.lengths[s];
+  int32_t length = 0;
+  if constexpr (!ROWS) length = a.lengths[s];
   int32_t pid = 0;
   if (!ROWS && a.window == 0 && a.share == 0.f && lane < a.chunk_pages)
     pid = kv_page(a.table + (int64_t)s * a.table_stride, ((int64_t)split * a.chunk >> a.c.shift) + lane, a.table_stride,
                   a.c.n_pages);
-  const int held = (int)kv_length(length, a.max_len, a.table_stride, a.c.shift);
+  const int held = ROWS ? row_held : (int)kv_length(length, a.max_len, a.table_stride, a.c.shift);
   // ROWS: n counts the positions read, gap lie unread behind the first pad of
   // them, all columns see [first, full) of the positions
   int n = held, first, base, full, gap = 0, pad = 0, near = 0;
-  SlotRange range;   // ROWS: of this lane's column
+  SlotRange range[CT];   // ROWS: of this lane's columns
   if constexpr (ROWS) {
     const int width = rows * a.group;   // columns of the sequence
-    const TileRange r = tile_range(held, rows, a.group, ht, 16, a.window, a.sinks, a.c.ps > kAttnTile ? a.c.ps : kAttnTile);
-    const int c = ht * 16 + col;
-    range = slot_range(held, rows, (c < width ? c : width - 1) / a.group, a.window);
+    const TileRange r = tile_range(held, rows, a.group, ht, COLS, a.window, a.sinks, a.c.ps > kAttnTile ? a.c.ps : kAttnTile);
+#pragma unroll
+    for (int u = 0; u < CT; ++u) {
+      const int c = ht * COLS + 16 * u + col;
+      range[u] = slot_range(held, rows, (c < width ? c : width - 1) / a.group, a.window);
+    }
     n = r.n;
     gap = r.gap;
     pad = r.pad;
@@ -287,11 +387,11 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const ARGS a)
     full = n;
   }
   const int columns = ROWS ? rows * a.group : a.group;
-  const int heads = columns - ht * 16 < 16 ? columns - ht * 16 : 16;   // valid columns
-  const int head0 = h * a.group + (ROWS ? 0 : ht * 16);
+  const int heads = columns - ht * COLS < COLS ? columns - ht * COLS : COLS;   // valid columns
+  const int head0 = h * a.group + (ROWS ? 0 : ht * COLS);
   // the row of q and out and the query head of column c
-  auto column_row = [&](int c) -> int64_t { return ROWS ? row0 + (ht * 16 + c) / a.group : s; };
-  auto column_head = [&](int c) -> int { return head0 + (ROWS ? (ht * 16 + c) % a.group : c); };
+  auto column_row = [&](int c) -> int64_t { return ROWS ? row0 + (ht * COLS + c) / a.group : s; };
+  auto column_head = [&](int c) -> int { return head0 + (ROWS ? (ht * COLS + c) % a.group : c); };
   auto store_out = [&](int c, int d, const f32x4& x) {   // dims d .. d + 3
     if constexpr (ROWS) {
       const int64_t at = column_row(c) * a.out_stride + (int64_t)column_head(c) * DIM + d;
@@ -306,7 +406,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const ARGS a)
     }
   };
   // splits cover little more than 2^25 positions: no overflow
-  if (base + split * (a.share == 0.f ? a.chunk : kAttnLeast) >= n) {
+  if (base + split * (ROWS ? row_chunk : a.share == 0.f ? a.chunk : kAttnLeast) >= n) {
     // nothing here, whatever the chunk; a sequence without positions is zero
     // (with more splits than one the join writes it)
     if (a.splits == 1) {
@@ -320,7 +420,8 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const ARGS a)
     }
     return;
   }
-  const int chunk = ROWS ? a.chunk : __builtin_amdgcn_readfirstlane(attn_chunk(a, lane));
+  int chunk = row_chunk;
+  if constexpr (!ROWS) chunk = __builtin_amdgcn_readfirstlane(attn_chunk(a, lane));
   const int begin = base + split * chunk;
   if (begin >= n) return;   // not with one split
   const int end = n - begin < chunk ? n : begin + chunk;
@@ -405,13 +506,16 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const ARGS a)
   }
 
   // q of this lane's head: the B operand, dims 32 b + 8 g .. + 7
-  Q q[NB];
-  float sfac = 1.0f;   // undoes the row's power-of-two scale (fp16 parts)
-  {
+  Q q[CT][NB];
+  float sfac[CT];   // undoes the row's power-of-two scale (fp16 parts)
+#pragma unroll
+  for (int u = 0; u < CT; ++u) {
+    const int own = 16 * u + col;
+    sfac[u] = 1.0f;
     float x[NB][8];
-    const bool live = col < heads;
-    const int64_t q_at = column_row(live ? col : 0) * a.q_stride + (int64_t)column_head(live ? col : 0) * DIM + 8 * g;
-    const float* qp = a.q + (int64_t)s * a.q_stride + (int64_t)(head0 + (live ? col : 0)) * DIM + 8 * g;
+    const bool live = own < heads;
+    const int64_t q_at = column_row(live ? own : 0) * a.q_stride + (int64_t)column_head(live ? own : 0) * DIM + 8 * g;
+    const float* qp = a.q + (int64_t)s * a.q_stride + (int64_t)(head0 + (live ? own : 0)) * DIM + 8 * g;
     if constexpr (ROWS) qp = a.q + (a.bf16 ? 0 : q_at);
     float amax = 0.f;
 #pragma unroll
@@ -420,9 +524,9 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const ARGS a)
       bool wide = true;
       if constexpr (ROWS) wide = !a.bf16;
       if (wide) {
-        const float4 u = *reinterpret_cast<const float4*>(qp + 32 * b);
+        const float4 w = *reinterpret_cast<const float4*>(qp + 32 * b);
         const float4 v = *reinterpret_cast<const float4*>(qp + 32 * b + 4);
-        const float z[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+        const float z[8] = {w.x, w.y, w.z, w.w, v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] = z[j];
       } else {
@@ -450,20 +554,25 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const ARGS a)
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[b][j] = __builtin_ldexpf(x[b][j], e);
-      sfac = __builtin_ldexpf(1.0f, -e);
+      sfac[u] = __builtin_ldexpf(1.0f, -e);
     }
 #pragma unroll
-    for (int b = 0; b < NB; ++b) q[b].set(x[b]);
+    for (int b = 0; b < NB; ++b) q[u][b].set(x[b]);
   }
 
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-  f32x4 o[NT];
+  f32x4 o[CT][NT];
+  float m[CT], l[CT];   // of this lane's heads; l over this lane's positions
 #pragma unroll
-  for (int t = 0; t < NT; ++t) o[t] = zero;
-  float m = -__builtin_inff(), l = 0.f;   // of this lane's head; l over this lane's positions
+  for (int u = 0; u < CT; ++u) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) o[u][t] = zero;
+    m[u] = -__builtin_inff();
+    l[u] = 0.f;
+  }
 
-  // Scores of positions t0 + J g + j of this lane's head, from the K loaded.
-  auto scores = [&](const AttnK<KIND, NB>& K, float (&sc)[J]) {
+  // Scores of positions t0 + J g + j of this lane's head u, from the K loaded.
+  auto scores = [&](int u, const AttnK<KIND, NB>& K, float (&sc)[J]) {
     if constexpr (KIND == kKvQ80) {
       auto tile = [&](auto tt) {
         constexpr int t = decltype(tt)::value;
@@ -473,7 +582,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const ARGS a)
           const uint4 kc = codes_f16(K.c[t][b]);
           r[b] = zero;
 #pragma unroll
-          for (int i = Q::kN - 1; i >= 0; --i) r[b] = attn_mfma<PART>(kc, q[b].p[i], r[b]);
+          for (int i = Q::kN - 1; i >= 0; --i) r[b] = attn_mfma<PART>(kc, q[u][b].p[i], r[b]);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) sc[4 * t + i] = 0.f;
@@ -483,7 +592,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const ARGS a)
           sc[j1] = fmaf(r[b1][j1 & 3], half_hi(d), sc[j1]);
         });
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sc[4 * t + i] *= sfac;
+        for (int i = 0; i < 4; ++i) sc[4 * t + i] *= sfac[u];
       };
       tile(std::integral_constant<int, 0>{});
       tile(std::integral_constant<int, 1>{});
@@ -494,9 +603,9 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const ARGS a)
 #pragma unroll
         for (int i = Q::kN - 1; i >= 0; --i)
 #pragma unroll
-          for (int b = 0; b < NB; ++b) acc = attn_mfma<PART>(K.x[t][b], q[b].p[i], acc);
+          for (int b = 0; b < NB; ++b) acc = attn_mfma<PART>(K.x[t][b], q[u][b].p[i], acc);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sc[4 * t + i] = acc[i] * sfac;
+        for (int i = 0; i < 4; ++i) sc[4 * t + i] = acc[i] * sfac[u];
       }
     }
   };
@@ -511,26 +620,26 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const ARGS a)
     }
   };
   // Running maximum and sum; p becomes the weights relative to the maximum.
-  auto softmax = [&](const float (&sc)[J], float (&p)[J]) {
+  auto softmax = [&](int u, const float (&sc)[J], float (&p)[J]) {
     float mx = sc[0];
 #pragma unroll
     for (int j = 1; j < J; ++j) mx = fmaxf(mx, sc[j]);
     mx = fmaxf(mx, __shfl_xor(mx, 16));
     mx = fmaxf(mx, __shfl_xor(mx, 32));
-    if (__any(mx > m)) {
-      const float mn = fmaxf(m, mx);
-      const float alpha = __builtin_amdgcn_exp2f(m - mn);   // mn is finite where a position counts
+    if (__any(mx > m[u])) {
+      const float mn = fmaxf(m[u], mx);
+      const float alpha = __builtin_amdgcn_exp2f(m[u] - mn);   // mn is finite where a position counts
       const float al = mn == -__builtin_inff() ? 1.0f : alpha;
-      m = mn;
-      l *= al;
+      m[u] = mn;
+      l[u] *= al;
 #pragma unroll
-      for (int t = 0; t < NT; ++t) o[t] *= al;
+      for (int t = 0; t < NT; ++t) o[u][t] *= al;
     }
-    const float base = m == -__builtin_inff() ? 0.f : m;   // nothing seen yet
+    const float base = m[u] == -__builtin_inff() ? 0.f : m[u];   // nothing seen yet
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       p[j] = __builtin_amdgcn_exp2f(sc[j] - base);
-      l += p[j];
+      l[u] += p[j];
     }
   };
   // Weights enter fp16 times a power of two. F16: 2^14. Q8_0: a weight times its
@@ -592,13 +701,16 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const ARGS a)
 #pragma unroll
       for (int j = 0; j < NW; ++j) by[j] = (uint32_t)grow[j];
       const float f = __builtin_ldexpf(1.0f, (int)scale_word<4 * b>(by));
-      o[2 * b] *= f;
-      o[2 * b + 1] *= f;
+#pragma unroll
+      for (int u = 0; u < CT; ++u) {
+        o[u][2 * b] *= f;
+        o[u][2 * b + 1] *= f;
+      }
     };
     each_block<0, NB>(block);
   };
   // O^T += V^T P^T, from the V given.
-  auto accumulate = [&](const AttnV<KIND, NB>& v, float (&p)[J]) {
+  auto accumulate = [&](int u, const AttnV<KIND, NB>& v, float (&p)[J]) {
     if constexpr (KIND == kKvQ80) {
       fit_scales(v.d);
       const float up = __builtin_ldexpf(1.0f, ks);
@@ -620,7 +732,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const ARGS a)
           for (int t = 2 * b; t < 2 * b + 2; ++t) {
             const uint4 vc = codes_f16(v.c[t]);
 #pragma unroll
-            for (int i = P::kN - 1; i >= 0; --i) o[t] = attn_mfma<PART>(vc, pp.p[i], o[t]);
+            for (int i = P::kN - 1; i >= 0; --i) o[u][t] = attn_mfma<PART>(vc, pp.p[i], o[u][t]);
           }
         }
       });
@@ -634,18 +746,22 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const ARGS a)
 #pragma unroll
       for (int i = P::kN - 1; i >= 0; --i)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) o[t] = attn_mfma<PART>(v.x[t], pp.p[i], o[t]);
+        for (int t = 0; t < NT; ++t) o[u][t] = attn_mfma<PART>(v.x[t], pp.p[i], o[u][t]);
     }
   };
 
   for (int t0 = t_lo; t0 < t_hi; t0 += step) {
-    float sc[J], p[J];
-    scores(K, sc);
+    float sc[CT][J], p[J];
+#pragma unroll
+    for (int u = 0; u < CT; ++u) scores(u, K, sc[u]);
     const bool more = t0 + step < t_hi;   // uniform over the wave
     if (more) load_k(K, t0 + step);
-    keep_scores(t0, sc);
-    softmax(sc, p);
-    accumulate(V, p);
+    keep_scores(t0, sc[0]);
+#pragma unroll
+    for (int u = 0; u < CT; ++u) {
+      softmax(u, sc[u], p);
+      accumulate(u, V, p);
+    }
     if (more) load_v(V, t0 + step);
   }
   for (int t0 = mine; t0 < end; t0 += step) {
@@ -663,20 +779,19 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const ARGS a)
     int hi = end - p0, lo = first - p0;
     hi = hi < 0 ? 0 : hi > J ? J : hi;
     lo = lo < 0 ? 0 : lo > J ? J : lo;
-    uint32_t live = ((1u << hi) - 1u) & ~((1u << lo) - 1u);   // of the lane's positions
-    uint32_t real = live;                                      // of those whose values are looked at
+    uint32_t live[CT];   // of the lane's positions
+    live[0] = ((1u << hi) - 1u) & ~((1u << lo) - 1u);
+    uint32_t real = live[0];   // of those whose values are looked at
     if constexpr (ROWS) {
-      const int at = p0 + skipped;
-      live = slot_bits(range, a.sinks, at);
+#pragma unroll
+      for (int u = 0; u < CT; ++u) live[u] = slot_bits(range[u], a.sinks, p0 + skipped);
       real = low_bits(end - p0);   // no column sees those behind, nor are their page ids known
     }
-    if (any_bad && __shfl(pid, ((p0 >> a.c.shift) - page0) & 63) < 0) live = real = 0u;
-    float sc[J], p[J];
-    scores(ek, sc);
+    if (any_bad && __shfl(pid, ((p0 >> a.c.shift) - page0) & 63) < 0) {
+      real = 0u;
 #pragma unroll
-    for (int j = 0; j < J; ++j) sc[j] = (live >> j & 1) ? sc[j] : -__builtin_inff();
-    keep_scores(t0, sc);
-    softmax(sc, p);
+      for (int u = 0; u < CT; ++u) live[u] = 0u;
+    }
     // V behind the length may hold anything: masked positions become 0 (Q8_0:
     // their scales; any code is finite)
     auto pair = [&](int i) { return ((real >> 2 * i & 1) ? 0xFFFFu : 0u) | ((real >> 2 * i & 2) ? 0xFFFF0000u : 0u); };
@@ -691,11 +806,22 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const ARGS a)
       for (int t = 0; t < NT; ++t)
         mv.x[t] = make_uint4(ev.x[t].x & w0, ev.x[t].y & w1, ev.x[t].z & w2, ev.x[t].w & w3);
     }
-    accumulate(mv, p);
+#pragma unroll
+    for (int u = 0; u < CT; ++u) {
+      float sc[J], p[J];
+      scores(u, ek, sc);
+#pragma unroll
+      for (int j = 0; j < J; ++j) sc[j] = (live[u] >> j & 1) ? sc[j] : -__builtin_inff();
+      if (u == 0) keep_scores(t0, sc);
+      softmax(u, sc, p);
+      accumulate(u, mv, p);
+    }
   }
   if constexpr (KIND == kKvF16) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) o[t] *= 1.0f / kPScaleF16;
+    for (int u = 0; u < CT; ++u)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) o[u][t] *= 1.0f / kPScaleF16;
   }
   if constexpr (KIND == kKvQ80) {
     auto block = [&](auto bb) {
@@ -704,21 +830,30 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const ARGS a)
 #pragma unroll
       for (int j = 0; j < NW; ++j) by[j] = (uint32_t)-(ks + e[j]);
       const float f = __builtin_ldexpf(1.0f, (int)scale_word<4 * b>(by));
-      o[2 * b] *= f;
-      o[2 * b + 1] *= f;
+#pragma unroll
+      for (int u = 0; u < CT; ++u) {
+        o[u][2 * b] *= f;
+        o[u][2 * b + 1] *= f;
+      }
     };
     each_block<0, NB>(block);
   }
-  l += __shfl_xor(l, 16);
-  l += __shfl_xor(l, 32);
+#pragma unroll
+  for (int u = 0; u < CT; ++u) {
+    l[u] += __shfl_xor(l[u], 16);
+    l[u] += __shfl_xor(l[u], 32);
+  }
 
   // Join of the waves, 32 dims at a time: [wave][head][32 + 4 floats].
   constexpr int kRow = 36;
-  __shared__ __align__(16) float ml[kAttnWaves][16][2];
-  __shared__ __align__(16) float part[kAttnWaves][16][kRow];
+  __shared__ __align__(16) float ml[kAttnWaves][COLS][2];
+  __shared__ __align__(16) float part[kAttnWaves][COLS][kRow];
   if (lane < 16) {
-    ml[wave][lane][0] = m;
-    ml[wave][lane][1] = l;
+#pragma unroll
+    for (int u = 0; u < CT; ++u) {
+      ml[wave][16 * u + lane][0] = m[u];
+      ml[wave][16 * u + lane][1] = l[u];
+    }
   }
   __syncthreads();
   auto joined = [&](int c, float* wf) {   // weight of each wave, returns {M, L}
@@ -745,8 +880,10 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const ARGS a)
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-      *reinterpret_cast<f32x4*>(&part[wave][col][16 * t + 4 * g]) = o[2 * b + t];
+    for (int u = 0; u < CT; ++u)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        *reinterpret_cast<f32x4*>(&part[wave][16 * u + col][16 * t + 4 * g]) = o[u][2 * b + t];
     __syncthreads();
     for (int i = tid; i < heads * 8; i += kAttnThreads) {   // four dims each
       const int c = i >> 3, d4 = (i & 7) * 4;
@@ -899,15 +1036,19 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const AttnArgs 
     if (pos + j >= first && pos + j < n) w[j] = o[j] + acc[j];
 }
 
+// The chunk that the blocks took.
+__device__ __forceinline__ int attn_join_chunk(const AttnRowsArgs& a, int lane) {
+  return attn_rows_chunk<128>(a, lane);   // only tiles of 128 columns have chunks by the lengths
+}
 // The same for several new tokens per sequence: the splits of (row, query head), those
-// of the row's tile of `columns` such pairs. -1: the row belongs to no sequence.
-__device__ __forceinline__ int attn_row_splits(const AttnRowsArgs& a, int64_t row, int head, int columns, int unit) {
+// of the row's tile of columns. -1: the row belongs to no sequence.
+__device__ __forceinline__ int attn_row_splits(const AttnRowsArgs& a, int64_t row, int head, int chunk) {
   const SeqOf q = seq_of_row(a.row_start, a.n_seqs, a.n_rows, row);
   if (q.seq < 0) return -1;
   const int held = (int)kv_length(a.lengths[q.seq], a.max_len, a.table_stride, a.c.shift);
   const int c = (int)(row - q.rows.row0) * a.group + head % a.group;
-  const TileRange r = tile_range(held, q.rows.rows, a.group, c / columns, columns, a.window, a.sinks, unit);
-  return r.n > 0 ? (r.n + a.chunk - 1) / a.chunk : 0;
+  const TileRange r = tile_range(held, q.rows.rows, a.group, c / a.columns, a.columns, a.window, a.sinks, a.unit);
+  return r.n > 0 ? (r.n + chunk - 1) / chunk : 0;
 }
 __device__ __forceinline__ void attn_store_row(const AttnRowsArgs& a, int64_t at, const f32x4& x) {
   if (a.bf16)
@@ -919,10 +1060,10 @@ __device__ __forceinline__ void attn_store_row(const AttnRowsArgs& a, int64_t at
 
 // A block per (row, query head).
 template <int DIM>
-__global__ __launch_bounds__(kJoinThreads) void attn_join_rows_kernel(const AttnRowsArgs a, int columns, int unit) {
+__global__ __launch_bounds__(kJoinThreads) void attn_join_rows_kernel(const AttnRowsArgs a) {
   const int tid = threadIdx.x, lane = tid & 63, head = blockIdx.y;
   const int64_t row = blockIdx.x;
-  const int splits = attn_row_splits(a, row, head, columns, unit);
+  const int splits = attn_row_splits(a, row, head, attn_join_chunk(a, lane));
   if (splits < 0) return;
   f32x4 sum;
   bool store;
@@ -933,14 +1074,15 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_rows_kernel(const Attn
 // Few splits of many rows: DIM / 4 lanes per (row, query head), several per block.
 constexpr int kJoinFew = 16;   // most splits
 template <int DIM>
-__global__ __launch_bounds__(kJoinThreads) void attn_join_few_kernel(const AttnRowsArgs a, int columns, int unit) {
+__global__ __launch_bounds__(kJoinThreads) void attn_join_few_kernel(const AttnRowsArgs a) {
   constexpr int kLanes = DIM / 4, kItems = kJoinThreads / kLanes;
   const int tid = threadIdx.x, c = tid % kLanes;
   const int64_t item = (int64_t)blockIdx.x * kItems + tid / kLanes;
+  const int chunk = attn_join_chunk(a, tid & 63);   // by all lanes
   if (tid >= kItems * kLanes || item >= a.n_rows * a.n_heads) return;
   const int64_t row = item / a.n_heads;
   const int head = (int)(item - row * a.n_heads);
-  const int splits = attn_row_splits(a, row, head, columns, unit);
+  const int splits = attn_row_splits(a, row, head, chunk);
   if (splits < 0) return;
   const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + item * a.splits;
   const float* po = a.part_o + item * a.splits * DIM + c * 4;

@@ -19,7 +19,7 @@ constexpr int64_t kPromptLeast = 512;     // shortest chunk of the prompt kernel
 
 struct ExtendPlan {
   bool prompt;                // the kernel for many rows
-  int32_t group, splits, chunk, unit, columns, groups;
+  int32_t group, splits, chunk, unit, columns, groups, fill;
   int64_t tiles;              // tiles of columns, at most
   int64_t ml_bytes, bytes;
 };
@@ -35,7 +35,12 @@ static int extend_plan(const KvView& c, int32_t type, int64_t n_seqs, int64_t n_
   p->group = (int32_t)(n_heads / c.hkv);
   if (n_rows * p->group > INT32_MAX / 2) return GGUF_QK_ERR_LIMIT;
   p->prompt = type == GGUF_KV_TYPE_BF16 && n_rows * p->group > 2 * kFewColumns * n_seqs;
-  p->columns = p->prompt ? kPromptColumns : kFewColumns;
+  // two tiles of columns where a sequence has more than one on average (F16, drafted tokens
+  // of 4 heads of 128 behind 8000 slots: 8 x 5 54 us with one, which reads K and V twice, 45
+  // with two; 16 x 8 93 and 75)
+  const bool q8 = c.head_bytes != kv_head_bytes(false, c.dim, c.ps);
+  p->columns = p->prompt ? kPromptColumns
+               : n_rows * p->group > kFewColumns * n_seqs ? attn_most_columns(q8, c.dim) : kFewColumns;
   const int tile = p->prompt ? kPromptSlots : kAttnTile;
   p->unit = c.ps > tile ? c.ps : tile;
   p->tiles = (n_rows * p->group + n_seqs * (p->columns - 1)) / p->columns;
@@ -52,11 +57,12 @@ static int extend_plan(const KvView& c, int32_t type, int64_t n_seqs, int64_t n_
   const int64_t cells = p->tiles * c.hkv;
   int64_t chunk;
   if (p->prompt) {
-    p->groups = cells < kPromptSingle ? prompt_groups(c.head_bytes != kv_head_bytes(false, c.dim, c.ps), c.dim) : 1;
+    p->groups = cells < kPromptSingle ? prompt_groups(q8, c.dim) : 1;
     const int64_t blocks = p->groups == 2 || c.dim > 128 ? kPromptBlocks : 2 * kPromptBlocks;
     const int64_t want = cells > 0 && cells < blocks ? blocks / cells : 1;
     chunk = ((span + want - 1) / want + 63) / 64 * 64;
     if (chunk < kPromptLeast) chunk = kPromptLeast;
+    p->fill = (int32_t)blocks;
   } else {
     const int64_t round = kAttnTile * kAttnWaves;
     int64_t most = int64_t(64) << c.shift;
@@ -67,9 +73,15 @@ static int extend_plan(const KvView& c, int32_t type, int64_t n_seqs, int64_t n_
     if (chunk < kAttnLeast) chunk = kAttnLeast;
     if (span <= 4 * round) chunk = 4 * round;
     if (chunk > most) chunk = most;
+    p->fill = 0;
   }
   p->chunk = (int32_t)chunk;
   p->splits = (int32_t)((span + chunk - 1) / chunk);
+  // Under a bound above the lengths, the prompt kernel's chunks are cut to the lengths on
+  // the device: 256 rows behind 8000 slots under a bound of 131072, 166 us with the host's
+  // chunks, 41 so. (The kernel for few rows has short chunks anyway, and more blocks that
+  // find nothing: 8 x 5 rows behind 3000 slots under 131072, 43 us without and 67 so.)
+  if (p->splits == 1 || chunk <= kPromptLeast || n_seqs > 64) p->fill = 0;
   const int64_t partials = p->splits > 1 ? abi_mul(n_rows * n_heads, p->splits) : 0;
   const int64_t ob = abi_mul(partials, c.dim * 4), mb = abi_mul(partials, 8);
   if (partials < 0 || ob < 0 || mb < 0 || ob > INT64_MAX - mb - 16) return GGUF_QK_ERR_LIMIT;
@@ -79,14 +91,14 @@ static int extend_plan(const KvView& c, int32_t type, int64_t n_seqs, int64_t n_
 }
 
 template <int DIM>
-static void launch_join_rows(const AttnRowsArgs& a, int columns, int unit, hipStream_t stream) {
+static void launch_join_rows(const AttnRowsArgs& a, hipStream_t stream) {
   constexpr int kItems = kJoinThreads / (DIM / 4);
   const int64_t items = a.n_rows * a.n_heads, blocks = (items + kItems - 1) / kItems;
   if (a.splits <= kJoinFew && blocks <= INT32_MAX / kJoinThreads)
-    hipLaunchKernelGGL(attn_join_few_kernel<DIM>, dim3((unsigned)blocks), dim3(kJoinThreads), 0, stream, a, columns, unit);
+    hipLaunchKernelGGL(attn_join_few_kernel<DIM>, dim3((unsigned)blocks), dim3(kJoinThreads), 0, stream, a);
   else   // rows <= 2^23: threads of a grid axis
     hipLaunchKernelGGL(attn_join_rows_kernel<DIM>, dim3((unsigned)a.n_rows, (unsigned)a.n_heads), dim3(kJoinThreads), 0,
-                       stream, a, columns, unit);
+                       stream, a);
 }
 
 }  // namespace gqk
@@ -170,23 +182,28 @@ int gguf_attn_extend(const gguf_kv_cache* cache, const void* q, int32_t type, in
   a.n_rows = n_rows;
   a.sinks = (int32_t)sinks;
   a.bf16 = type == GGUF_KV_TYPE_BF16;
+  a.columns = p.columns;
+  a.unit = p.unit;
+  a.fill = p.fill;
+  a.round = kPromptSlots;
+  a.least = kPromptLeast;
   const dim3 grid((unsigned)a.c.hkv, (unsigned)p.tiles, (unsigned)p.splits);
   a.tiles = (int32_t)p.tiles;
   if (p.prompt) {
     if (cache->type == GGUF_KV_TYPE_F16) launch_prompt_f16(a, p.groups, grid, stream);
     else if (cache->type == GGUF_KV_TYPE_BF16) launch_prompt_bf16(a, p.groups, grid, stream);
     else launch_prompt_q8_0(a, p.groups, grid, stream);
-  } else if (cache->type == GGUF_KV_TYPE_F16) launch_attn_rows_f16(a, grid, stream);
-  else if (cache->type == GGUF_KV_TYPE_BF16) launch_attn_rows_bf16(a, grid, stream);
-  else launch_attn_rows_q8_0(a, grid, stream);
+  } else if (cache->type == GGUF_KV_TYPE_F16) launch_attn_rows_f16(a, p.columns, grid, stream);
+  else if (cache->type == GGUF_KV_TYPE_BF16) launch_attn_rows_bf16(a, p.columns, grid, stream);
+  else launch_attn_rows_q8_0(a, p.columns, grid, stream);
   st = abi_launched();
   if (st || p.splits == 1) return st;
   switch (a.c.dim) {
-    case 64: launch_join_rows<64>(a, p.columns, p.unit, stream); break;
-    case 96: launch_join_rows<96>(a, p.columns, p.unit, stream); break;
-    case 128: launch_join_rows<128>(a, p.columns, p.unit, stream); break;
-    case 192: launch_join_rows<192>(a, p.columns, p.unit, stream); break;
-    default: launch_join_rows<256>(a, p.columns, p.unit, stream); break;
+    case 64: launch_join_rows<64>(a, stream); break;
+    case 96: launch_join_rows<96>(a, stream); break;
+    case 128: launch_join_rows<128>(a, stream); break;
+    case 192: launch_join_rows<192>(a, stream); break;
+    default: launch_join_rows<256>(a, stream); break;
   }
   return abi_launched();
 }

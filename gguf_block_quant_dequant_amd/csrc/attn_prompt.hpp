@@ -146,14 +146,14 @@ __global__ __launch_bounds__(kPromptThreads * GROUPS, NB <= 4 ? 2 : 1) void attn
   const int col = lane & 31, hf = lane >> 5;
   const int h = blockIdx.x, split = blockIdx.z;
   // the last tiles of a sequence see most: they go first
-  const RowTile rt = find_row_tile(a.row_start, a.n_seqs, a.n_rows, a.group, kPromptColumns, a.tiles - 1 - (int)blockIdx.y, lane);
+  const RowsPlan plan = attn_rows_plan<kPromptColumns>(a, a.tiles - 1 - (int)blockIdx.y, lane);
+  const RowTile rt = plan.t;
   if (rt.seq < 0) return;
-  const int s = rt.seq;
-  const int held = (int)kv_length(a.lengths[s], a.max_len, a.table_stride, a.c.shift);
+  const int s = rt.seq, held = plan.held, chunk = plan.chunk;
   const int width = rt.rows * a.group;
   const int unit = a.c.ps > T ? a.c.ps : T;
   const TileRange r = tile_range(held, rt.rows, a.group, rt.tile, kPromptColumns, a.window, a.sinks, unit);
-  const int begin = split * a.chunk, end = r.n - begin < a.chunk ? r.n : begin + a.chunk;   // numbered without the gap
+  const int begin = split * chunk, end = r.n - begin < chunk ? r.n : begin + chunk;   // numbered without the gap
   const int c = rt.tile * kPromptColumns + wave * 32 + col;   // this lane's column
   const bool live = c < width;
   const int cc = live ? c : width - 1;

@@ -12,7 +12,14 @@ static void launch_dim(const AttnArgs& a, bool track, dim3 grid, hipStream_t str
 }
 
 template <int NB>
-static void launch_dim(const AttnRowsArgs& a, dim3 grid, hipStream_t stream) {
+static void launch_dim(const AttnRowsArgs& a, int columns, dim3 grid, hipStream_t stream) {
+  if constexpr (attn_most_columns(GQK_KV_KIND == 2, NB * 32) == 32) {
+    if (columns == 32) {
+      hipLaunchKernelGGL((attn_decode_kernel<GQK_KV_KIND, NB, false, AttnRowsArgs, 2>), grid, dim3(kAttnThreads), 0,
+                         stream, a);
+      return;
+    }
+  }
   hipLaunchKernelGGL((attn_decode_kernel<GQK_KV_KIND, NB, false, AttnRowsArgs>), grid, dim3(kAttnThreads), 0, stream, a);
 }
 
@@ -33,18 +40,18 @@ void launch_attn_q8_0(const AttnArgs& a, bool track, dim3 grid, hipStream_t stre
 }
 
 #if GQK_KV_KIND == 0
-void launch_attn_rows_f16(const AttnRowsArgs& a, dim3 grid, hipStream_t stream) {
+void launch_attn_rows_f16(const AttnRowsArgs& a, int columns, dim3 grid, hipStream_t stream) {
 #elif GQK_KV_KIND == 1
-void launch_attn_rows_bf16(const AttnRowsArgs& a, dim3 grid, hipStream_t stream) {
+void launch_attn_rows_bf16(const AttnRowsArgs& a, int columns, dim3 grid, hipStream_t stream) {
 #else
-void launch_attn_rows_q8_0(const AttnRowsArgs& a, dim3 grid, hipStream_t stream) {
+void launch_attn_rows_q8_0(const AttnRowsArgs& a, int columns, dim3 grid, hipStream_t stream) {
 #endif
   switch (a.c.dim) {
-    case 64: return launch_dim<2>(a, grid, stream);
-    case 96: return launch_dim<3>(a, grid, stream);
-    case 128: return launch_dim<4>(a, grid, stream);
-    case 192: return launch_dim<6>(a, grid, stream);
-    default: return launch_dim<8>(a, grid, stream);
+    case 64: return launch_dim<2>(a, columns, grid, stream);
+    case 96: return launch_dim<3>(a, columns, grid, stream);
+    case 128: return launch_dim<4>(a, columns, grid, stream);
+    case 192: return launch_dim<6>(a, columns, grid, stream);
+    default: return launch_dim<8>(a, columns, grid, stream);
   }
 }
 
