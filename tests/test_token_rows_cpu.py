@@ -91,3 +91,57 @@ def test_rows_and_slots_stay_inside(tmp_path):
     assert build.returncode == 0, build.stderr
     run = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
     assert run.returncode == 0 and run.stdout.strip() == "ok", run.stdout + run.stderr
+
+
+SEARCH = r"""
+#include <climits>
+#include <cstdio>
+#include <vector>
+#include "token_rows.hpp"
+using namespace gqk;
+#define CHECK(x) do { if (!(x)) { std::printf("line %d: %s\n", __LINE__, #x); return 1; } } while (0)
+
+int main() {
+  uint32_t state = 1;
+  auto random = [&](int n) { state = state * 1664525u + 1013904223u; return (int)((state >> 8) % (uint32_t)n); };
+  for (int trial = 0; trial < 3000; ++trial) {
+    const int n_seqs = 1 + random(trial % 10 == 0 ? 200 : 9), n_rows = random(60);
+    std::vector<int32_t> starts(n_seqs + 1);
+    starts[0] = random(8) - 4;   // before the first row, and rows of nobody in front
+    for (int s = 0; s < n_seqs; ++s) starts[s + 1] = starts[s] + (random(3) == 0 ? 0 : random(9));
+    for (int row = 0; row < n_rows; ++row) {
+      int seq = -1;
+      for (int s = 0; s < n_seqs; ++s)
+        if (row >= starts[s] && row < starts[s + 1]) seq = s;
+      const SeqOf f = seq_of_row(starts.data(), n_seqs, n_rows, row);
+      CHECK(f.seq == seq);
+      if (seq >= 0) CHECK(f.rows.row0 <= row && row < f.rows.row0 + f.rows.rows && f.rows.row0 == (starts[seq] < 0 ? 0 : starts[seq]));
+    }
+    // entries in any order: a sequence of the call and rows within, or none
+    for (auto& x : starts) x = random(5) == 0 ? (random(2) ? INT_MAX : INT_MIN) : random(80) - 10;
+    for (int row = 0; row < n_rows; ++row) {
+      const SeqOf f = seq_of_row(starts.data(), n_seqs, n_rows, row);
+      CHECK(f.seq >= -1 && f.seq < n_seqs);
+      if (f.seq >= 0) CHECK(f.rows.row0 >= 0 && f.rows.row0 <= row && row < f.rows.row0 + f.rows.rows && f.rows.row0 + f.rows.rows <= n_rows);
+    }
+  }
+  for (int64_t row : {0, 5, 8388607}) {
+    const SeqOf f = seq_of_row(nullptr, 1 << 20, 1 << 23, row);
+    CHECK(f.seq == row && f.rows.row0 == row && f.rows.rows == 1);
+  }
+  std::puts("ok");
+  return 0;
+}
+"""
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="no host compiler")
+def test_rows_find_their_sequence(tmp_path):
+    src, exe = tmp_path / "search.cpp", tmp_path / "search"
+    src.write_text(SEARCH)
+    build = subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-fsanitize=undefined",
+                            "-fno-sanitize-recover=undefined", "-I", CSRC, str(src), "-o", str(exe)],
+                           capture_output=True, text=True)
+    assert build.returncode == 0, build.stderr
+    run = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
+    assert run.returncode == 0 and run.stdout.strip() == "ok", run.stdout + run.stderr
