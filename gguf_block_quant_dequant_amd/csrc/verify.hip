@@ -32,7 +32,7 @@ static int launch_verify(const VerifyArgs& a, hipStream_t stream) {
     const int st = abi_launched();
     if (st) return st;
   }
-  hipLaunchKernelGGL((verify_choose_kernel<BF16, WIDE>), dim3((unsigned)a.splits, (unsigned)a.n_seqs), dim3(kDrawThreads),
+  hipLaunchKernelGGL((verify_choose_kernel<BF16, WIDE>), dim3((unsigned)a.splits, (unsigned)a.n_seqs), dim3(kChooseThreads),
                      0, stream, a);
   const int st = abi_launched();
   if (st || a.n_rows == 0) return st;

@@ -1,16 +1,22 @@
 // Verification of drafted tokens (gguf_verify_draft in include/gguf_tokens.h).
 // Three launches over rows cut into splits of 8192 values:
 //   sums    per split the maximum m and s = sum 2^((x - m) log2(e) / T) of target
-//           and draft (T = 0: m and its lowest index);
-//   choose  every block joins its sequence's splits (a few hundred values), finds the
-//           first row that is not accepted and sums its split of what the next token
-//           is drawn from, p or max(p - q, 0);
+//           and draft (T = 0: m and its lowest index), from registers;
+//   choose  every block joins the splits' sums of its sequence's rows, sixteen lanes to a
+//           row of each side, finds the first row that is not accepted and sums its split
+//           of what the next token is drawn from, p or max(p - q, 0);
 //   draw    one block per sequence finds the split, then the value, where the running
 //           sum passes uniform * total.
 // A draw is a whole number that must not depend on how sums are formed: with
 // exponentials in fp32 (2^-22) a running sum over a vocabulary would cross a boundary
 // that the exact one does not about once in 10^4 draws. Exponentials and sums are fp64
-// instead, whose products run at fp32's rate here: a polynomial of degree 10.
+// instead, whose products run at fp32's rate here.
+//
+// Bound: one read of the logits at large sizes, beside it the exponentials; three launches
+// and their chains of loads at small ones. 32 sequences of 2 to 7 drafts over 128256 values, fp32,
+// both sides: sums 43 us (180 MB, 4.2 TB/s; 33 without the exponentials, 49 with a
+// polynomial of degree 10 in place of the table), choose 14 (18 with blocks of 1024 threads,
+// whose registers let one of them run per CU), draw 11. One sequence of 4 drafts: 6, 5, 7.
 #pragma once
 
 #include "token_rows.hpp"
@@ -49,26 +55,38 @@ struct VerifyArgs {
 constexpr int kVerifyThreads = 256;   // of the sums: 32 values each, all loads in flight
 constexpr int kVerifyWaves = kVerifyThreads / 64;
 constexpr int kVerifySplit = kVerifyThreads * 32;
-constexpr int kDrawThreads = 1024;    // of the others, 8 values each: few blocks, whose latency counts
+constexpr int kChooseThreads = 512;   // 16 values each
+constexpr int kDrawThreads = 1024;    // 8 values each: few blocks, whose latency counts
 constexpr int kDrawWaves = kDrawThreads / 64;
 
-// 2^z for z <= 0: 2^k 2^f with |f| <= 1/2 and the series of e^(f ln 2) to its tenth
-// power (the next term is below 2^-42). -inf gives 0.
-__device__ __forceinline__ double exp2_f64(double z) {
-  z = z > -1100.0 ? z : -1100.0;
-  const double k = __builtin_rint(z), f = z - k;
-  double p = 7.0549116208011233e-9;   // ln(2)^n / n!, n = 10 .. 0
-  p = fma(p, f, 1.0178086009239699e-7);
-  p = fma(p, f, 1.3215486790144309e-6);
-  p = fma(p, f, 1.5252733804059840e-5);
-  p = fma(p, f, 1.5403530393381609e-4);
-  p = fma(p, f, 1.3333558146428443e-3);
-  p = fma(p, f, 9.6181291076284772e-3);
-  p = fma(p, f, 5.5504108664821580e-2);
-  p = fma(p, f, 2.4022650695910071e-1);
-  p = fma(p, f, 6.9314718055994531e-1);
-  p = fma(p, f, 1.0);
-  return __builtin_ldexp(p, (int)k);
+// 2^(j / 32)
+__device__ const double kVerifyPowers[32] = {
+    1.0, 1.0218971486541166, 1.0442737824274138, 1.0671404006768237,
+    1.0905077326652577, 1.1143867425958924, 1.1387886347566916, 1.1637248587775775,
+    1.189207115002721, 1.215247359980469, 1.241857812073484, 1.2690509571917332,
+    1.2968395546510096, 1.3252366431597413, 1.3542555469368927, 1.383909881963832,
+    1.4142135623730951, 1.4451808069770467, 1.4768261459394993, 1.5091644275934228,
+    1.5422108254079407, 1.5759808451078865, 1.6104903319492543, 1.645755478153965,
+    1.681792830507429, 1.718619298122478, 1.7562521603732995, 1.7947090750031072,
+    1.8340080864093424, 1.8741676341103, 1.9152065613971474, 1.9571441241754002};
+
+// 2^z for z <= 0: 2^k 2^(j / 32) 2^r with |r| <= 1/64, k and j from the low bits of z + 1.5 2^47
+// (whose last place is 1/32), 2^(j / 32) from `powers` (the 32 above in LDS: lanes read one
+// address or different banks), 2^r from the series of e^(r ln 2) to its fifth power, that one
+// economized by Chebyshev's T5 into the first and third. Off by 2^-43 at most. -inf gives 0.
+__device__ __forceinline__ double exp2_f64(double z, const double* powers) {
+  z = __builtin_fmax(z, -1100.0);
+  const double t = z + 0x1.8p47, r = z - (t - 0x1.8p47);
+  const int n = (int)(uint32_t)__builtin_bit_cast(uint64_t, t);
+  double p = fma(9.618129107628477e-3, r, 5.5504515572724004e-2);
+  p = fma(p, r, 2.4022650695910072e-1);
+  p = fma(p, r, 6.931471805351096e-1);
+  p = fma(p, r, 1.0);
+  return __builtin_ldexp(p * powers[n & 31], n >> 5);
+}
+// `powers` of a block; the caller waits for the block.
+__device__ __forceinline__ void load_powers(double* powers, int tid) {
+  if (tid < 32) powers[tid] = kVerifyPowers[tid];
 }
 
 __device__ __forceinline__ double verify_temperature(const VerifyArgs& a, int seq) {
@@ -170,6 +188,8 @@ __global__ __launch_bounds__(kVerifyThreads) void verify_sums_kernel(const Verif
     m = fmaxf(m, v.x[j]);
     nan |= v.x[j] != v.x[j];
   }
+  __shared__ double powers[32];
+  load_powers(powers, tid);
   __shared__ float wave_m[kVerifyWaves];
   __shared__ double wave_s[kVerifyWaves];
   m = wave_max(m);
@@ -190,7 +210,7 @@ __global__ __launch_bounds__(kVerifyThreads) void verify_sums_kernel(const Verif
   } else if (m > -__builtin_inff() && m < __builtin_inff()) {
     const double c = verify_scale(t), dm = (double)m;
 #pragma unroll
-    for (int j = 0; j < Values::PER; ++j) s += exp2_f64(((double)v.x[j] - dm) * c);
+    for (int j = 0; j < Values::PER; ++j) s += exp2_f64(((double)v.x[j] - dm) * c, powers);
     s = wave_sum_f64(s);
   }
   if (lane == 0) wave_s[wave] = s;
@@ -231,9 +251,9 @@ struct VerifyRow {
 // First every block judges its sequence's rows, sixteen lanes for the target's sums of a
 // row and sixteen for the draft's, 32 rows at a time; then it sums its split.
 template <bool BF16, bool WIDE>
-__global__ __launch_bounds__(kDrawThreads) void verify_choose_kernel(const VerifyArgs a) {
-  using Values = VerifyValues<BF16, WIDE, kDrawThreads>;
-  constexpr int kRows = kDrawThreads / 32;
+__global__ __launch_bounds__(kChooseThreads) void verify_choose_kernel(const VerifyArgs a) {
+  using Values = VerifyValues<BF16, WIDE, kChooseThreads>;
+  constexpr int kRows = kChooseThreads / 32;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = tid & 15;
   const int s = blockIdx.y, split = blockIdx.x;
   const SeqRows seq = seq_rows(a.row_start, s, a.n_rows);
@@ -246,14 +266,16 @@ __global__ __launch_bounds__(kDrawThreads) void verify_choose_kernel(const Verif
     return;
   }
   const double t = verify_temperature(a, s), c = t > 0.0 ? verify_scale(t) : 0.0;
+  __shared__ double powers[32];
+  load_powers(powers, tid);
   __shared__ VerifyRow judged[kRows];
-  __shared__ double sums[kDrawWaves];
+  __shared__ double sums[kChooseThreads / 64];
   const bool writes = split == 0 && a.prob;   // goes through all rows
   int first = seq.rows;
   VerifyChoice ch;
   int best_token = -1;
   for (int j0 = 0; j0 < seq.rows && (first == seq.rows || writes); j0 += kRows) {
-    __syncthreads();   // judged[] is free
+    __syncthreads();   // judged[] is free (powers[] is there)
     const int j = j0 + tid / 32, which = tid >> 4 & 1;
     const bool live = j < seq.rows;
     const int64_t row = (int64_t)seq.row0 + (live ? j : 0);
@@ -277,10 +299,10 @@ __global__ __launch_bounds__(kDrawThreads) void verify_choose_kernel(const Verif
       sum = -row16_max(m == top ? -at : -(double)a.vocab);
     } else {
       if (use)
-        for (int i = l16; i < a.splits; i += 16) sum = fma(part[i].y, exp2_f64((part[i].x - top) * c), sum);
+        for (int i = l16; i < a.splits; i += 16) sum = fma(part[i].y, exp2_f64((part[i].x - top) * c, powers), sum);
       sum = row16_sum(sum);
     }
-    const double share = use && known && t > 0.0 ? exp2_f64(((double)logit - top) * c) / sum : 0.0;
+    const double share = use && known && t > 0.0 ? exp2_f64(((double)logit - top) * c, powers) / sum : 0.0;
     const double q_top = __shfl_xor(top, 16), q_sum = __shfl_xor(sum, 16), q_share = __shfl_xor(share, 16);
     if (live && which == 0 && l16 == 0) {
       VerifyRow r;
@@ -341,7 +363,7 @@ __global__ __launch_bounds__(kDrawThreads) void verify_choose_kernel(const Verif
   if (ch.mode == kDrawP) {   // known from the sums
     if (tid == 0) {
       const double2 p = a.part[ch.row * a.splits + split];
-      *rest = p.y * exp2_f64((p.x - ch.mp) * c);
+      *rest = p.y * exp2_f64((p.x - ch.mp) * c, powers);
     }
     return;
   }
@@ -352,12 +374,12 @@ __global__ __launch_bounds__(kDrawThreads) void verify_choose_kernel(const Verif
     q.load(a, 1, ch.row, split, tid);
 #pragma unroll
     for (int j = 0; j < Values::PER; ++j)
-      sum += verify_rest(exp2_f64(((double)p.x[j] - ch.mp) * c), ch.ip, exp2_f64(((double)q.x[j] - ch.mq) * c), ch.iq);
+      sum += verify_rest(exp2_f64(((double)p.x[j] - ch.mp) * c, powers), ch.ip, exp2_f64(((double)q.x[j] - ch.mq) * c, powers), ch.iq);
   } else {
     const int token = a.tokens[ch.row] - split * kVerifySplit;
 #pragma unroll
     for (int j = 0; j < Values::PER; ++j) {
-      const double r = exp2_f64(((double)p.x[j] - ch.mp) * c);
+      const double r = exp2_f64(((double)p.x[j] - ch.mp) * c, powers);
       sum += Values::index(j, tid) == token ? 0.0 : r;
     }
   }
@@ -366,16 +388,16 @@ __global__ __launch_bounds__(kDrawThreads) void verify_choose_kernel(const Verif
   __syncthreads();
   if (tid == 0) {
     sum = 0.0;
-    for (int w = 0; w < kDrawWaves; ++w) sum += sums[w];
+    for (int w = 0; w < kChooseThreads / 64; ++w) sum += sums[w];
     *rest = sum;
   }
 }
 
 // What value i of the chosen row weighs, its logits given.
 __device__ __forceinline__ double verify_weight(const VerifyArgs& a, const VerifyChoice& ch, double c, float x, float y,
-                                                bool token) {
-  const double p = exp2_f64(((double)x - ch.mp) * c);
-  if (ch.mode == kDrawRest) return verify_rest(p, ch.ip, exp2_f64(((double)y - ch.mq) * c), ch.iq);
+                                                bool token, const double* powers) {
+  const double p = exp2_f64(((double)x - ch.mp) * c, powers);
+  if (ch.mode == kDrawRest) return verify_rest(p, ch.ip, exp2_f64(((double)y - ch.mq) * c, powers), ch.iq);
   return ch.mode == kDrawOneHot && token ? 0.0 : p;
 }
 
@@ -399,10 +421,13 @@ __global__ __launch_bounds__(kDrawThreads) void verify_draw_kernel(const VerifyA
   const double c = verify_scale(verify_temperature(a, s)), u = (double)a.uniform_next[s];
   const double* rest = a.rest + (int64_t)s * a.splits;
   const double2* part = a.part + ch.row * a.splits;
+  __shared__ double powers[32];
+  load_powers(powers, tid);
+  __syncthreads();
   bool all = false;   // p - q is nowhere above 0: from p
   auto split_sum = [&](int i) -> double {
     if (i >= a.splits) return 0.0;
-    return all ? part[i].y * exp2_f64((part[i].x - ch.mp) * c) : rest[i];
+    return all ? part[i].y * exp2_f64((part[i].x - ch.mp) * c, powers) : rest[i];
   };
   // every wave goes through the splits' sums, 64 at a time
   auto whole = [&]() {
@@ -453,7 +478,7 @@ __global__ __launch_bounds__(kDrawThreads) void verify_draw_kernel(const VerifyA
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
     const int i = tid * PER + j, at = i + i / PER;
-    w[j] = verify_weight(a, ch, c, logits[0][at], two ? logits[1][at] : 0.f, i == token);
+    w[j] = verify_weight(a, ch, c, logits[0][at], two ? logits[1][at] : 0.f, i == token, powers);
     if (w[j] > 0.0) tail = j;
     sum += w[j];
   }

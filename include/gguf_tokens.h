@@ -130,7 +130,7 @@ int gguf_attn_extend(const gguf_kv_cache* cache, const void* q, int32_t type, in
  * nothing, has accept_prob 0, and draws -1. Rows of no sequence are left alone.
  *
  * target and draft of one type, F32 or BF16, [n_rows][vocab], strides in elements from
- * row to row (>= vocab), aligned to their elements. Exponentials (to 2^-42) and sums
+ * row to row (>= vocab), aligned to their elements. Exponentials (to 2^-43) and sums
  * are fp64: a draw differs from the exact one only where uniform_next falls within
  * some 1e-12 of a boundary. T >= 0 and finite (a negative or NaN T is taken as 0).
  * vocab <= 2^30. */
