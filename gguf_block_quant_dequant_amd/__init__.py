@@ -899,59 +899,61 @@ def gguf_qk_rope(q, k, pos=None, freqs=None, axes=None, halves=True, magnitude=1
     pair's axis; freqs fp64 [n_rot / 2] radians per position (both None: norms only).
     halves: pair i is elements i and i + n_rot / 2, else 2 i and 2 i + 1. Returns
     (q_out, k_out), which may be given (q and k themselves: in place)."""
-    given = [x for x in (q, k) if x is not None]
-    if not given:
+    one = k if q is None else q
+    if one is None:
         raise ValueError("q or k must be given")
-    for x in given:
-        if not isinstance(x, torch.Tensor):
+    for x in (q, k):
+        if x is not None and not isinstance(x, torch.Tensor):
             raise TypeError("q and k must be torch tensors")
-        if not x.is_cuda:
-            raise ValueError("q and k must be device tensors")
-        if x.dim() != 3:
-            raise ValueError("q and k must be [n_tokens, n_heads, head_dim]")
-    dev, (n, _, d), dt = given[0].get_device(), given[0].shape, given[0].dtype
-    if dt not in _SOURCES or any(x.dtype is not dt or x.shape[0] != n or x.shape[2] != d for x in given):
-        raise ValueError("q and k must be fp32 or bf16 of one type, with the same tokens and head_dim")
+    if one.dim() != 3:
+        raise ValueError("q and k must be [n_tokens, n_heads, head_dim]")
+    dev, dt = one.get_device(), one.dtype
+    n, _, d = one.shape
+    if dev < 0:
+        raise ValueError("q and k must be device tensors")
+    type_id = _source_id(dt)
     if (pos is None) != (freqs is None) or (axes is not None and freqs is None):
         raise ValueError("pos and freqs belong together, and axes to them")
     ref = None
     if freqs is not None:
         fp, half = _tensor(freqs, "freqs", dev, torch.float64), freqs.numel()
-        pp = _tensor(pos, "pos", dev, torch.int32)
-        if pos.dim() not in (1, 2) or pos.shape[-1] != n:
+        pp, shape = _tensor(pos, "pos", dev, torch.int32), pos.shape
+        if len(shape) not in (1, 2) or shape[-1] != n:
             raise ValueError("pos must be [n_tokens] or [n_axes, n_tokens]")
         ap = None if axes is None else _ints(axes, "axes", dev, half)
-        rope = RopeStruct(fp, ap, pp, n, 1 if pos.dim() == 1 else pos.shape[0], 2 * half,
+        rope = RopeStruct(fp, ap, pp, n, 1 if len(shape) == 1 else shape[0], 2 * half,
                           ROPE_HALVES if halves else ROPE_ADJACENT, magnitude)
         ref = ctypes.addressof(rope)
-    norms = []
-    for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
-        p = None
-        if w is not None:
-            p = _tensor(w, name, dev, torch.float32)
-            if w.numel() != d:
-                raise ValueError(f"{name} holds {w.numel()} values, expected {d}")
-        norms.append(p)
+    qw = None if q_norm is None else _floats(q_norm, "q_norm", dev, d)
+    kw = None if k_norm is None else _floats(k_norm, "k_norm", dev, d)
+
+    def rows(x, name):
+        """(address, row stride, heads)"""
+        shape = x.shape
+        if len(shape) != 3 or shape[0] != n or shape[2] != d or x.dtype is not dt:
+            raise ValueError("q and k must be of one type, with the same tokens and head_dim")
+        return *_rows(x, name, dev, shape[1] * d, (dt,)), shape[1]
 
     def run(st):
-        outs, args = [], []
-        for x, o, name in ((q, q_out, "q"), (k, k_out, "k")):
-            if x is None:
-                outs.append(None)
-                args += [None, 0, None, 0, 0]
-                continue
-            if o is None:
-                o = torch.empty(x.shape, dtype=dt, device=x.device)
-            elif o.shape != x.shape:
-                raise ValueError(f"{name}_out must have {name}'s shape")
-            row = x.shape[1] * d
-            (xp, xs), (op, os_) = _rows(x, name, dev, row, (dt,)), _rows(o, name + "_out", dev, row, (dt,))
-            outs.append(o)
-            args += [xp, xs, op, os_, x.shape[1]]
+        qo, ko, qp, kp, qop, kop, qs, ks, qos, kos, qh, kh = q_out, k_out, None, None, None, None, 0, 0, 0, 0, 0, 0
+        if q is not None:
+            qp, qs, qh = rows(q, "q")
+            if qo is None:
+                qo = torch.empty(q.shape, dtype=dt, device=q.device)
+            qop, qos, h = rows(qo, "q_out")
+            if h != qh:
+                raise ValueError("q_out must have q's shape")
+        if k is not None:
+            kp, ks, kh = rows(k, "k")
+            if ko is None:
+                ko = torch.empty(k.shape, dtype=dt, device=k.device)
+            kop, kos, h = rows(ko, "k_out")
+            if h != kh:
+                raise ValueError("k_out must have k's shape")
         if n:   # empty tensors have no address
-            _check(lib().gguf_qk_rope(*args, TENSOR_F32 if dt is torch.float32 else TENSOR_BF16, n, d, *norms, eps, ref,
-                                      st), "gguf_qk_rope")
-        return outs[0], outs[1]
+            _check(lib().gguf_qk_rope(qp, qs, qop, qos, qh, kp, ks, kop, kos, kh, type_id, n, d, qw, kw, eps, ref, st),
+                   "gguf_qk_rope")
+        return None if q is None else qo, None if k is None else ko
     return _call(dev, stream, run)
 
 
