@@ -8,18 +8,26 @@
 namespace gqk {
 
 constexpr int64_t kExtendMaxLen = int64_t(1) << 25;
-constexpr int64_t kExtendBlocks = 1024;   // blocks a call aims for
+// Blocks a call of the few-rows kernel aims for (8 sequences of 3 to 5 rows behind 5000 to
+// 8187 slots, F16: 40 us with 512, 34.5 with 1024, 42 with 2048; the same of 5 behind 8000,
+// BF16: 53, 54, 68).
+constexpr int64_t kExtendBlocks = 1024;
 constexpr int64_t kExtendChunk = 1024;    // longest chunk of positions of the few-rows kernel
 constexpr int kFewColumns = 16;           // columns of its tiles
 constexpr int64_t kPromptBlocks = 256;    // blocks that run at once: one per CU, or two of one group of waves to head dim 128
 // Blocks from which one group of waves each, two blocks at a time, does better: 8 prompts
 // to 4096 (4680 blocks) 560 us against 685; one of 4096 (512) 110 against 104.
 constexpr int64_t kPromptSingle = 1024;
-constexpr int64_t kPromptLeast = 512;     // shortest chunk of the prompt kernel
+// Shortest chunk of the prompt kernel, per group of waves: a block's start and end take as
+// long as four to five steps of 64 slots (Q8_0, one sequence of 16 rows behind 8000 slots: 32
+// us with 512, 22 with 256, 21 with 128; 64 rows behind 30000: 52, 54, 53. BF16, two groups,
+// a prompt of 1024: 32 with 256 in all, 28 with 512; 512 rows behind 2000: 32, and 34 with
+// 1024).
+constexpr int64_t kPromptLeast = 256;
 
 struct ExtendPlan {
   bool prompt;                // the kernel for many rows
-  int32_t group, splits, chunk, unit, columns, groups, fill;
+  int32_t group, splits, chunk, unit, columns, groups, fill, least;
   int64_t tiles;              // tiles of columns, at most
   int64_t ml_bytes, bytes;
 };
@@ -34,11 +42,18 @@ static int extend_plan(const KvView& c, int32_t type, int64_t n_seqs, int64_t n_
     return GGUF_QK_ERR_LIMIT;
   p->group = (int32_t)(n_heads / c.hkv);
   if (n_rows * p->group > INT32_MAX / 2) return GGUF_QK_ERR_LIMIT;
-  p->prompt = type == GGUF_KV_TYPE_BF16 && n_rows * p->group > 2 * kFewColumns * n_seqs;
+  // The kernel for many rows, whose tiles go straight to LDS, where a sequence's rows fill
+  // more than a tile of 16 columns of the one for few; from head dim 96 on (64 sequences of 5
+  // rows of 4 heads behind 1000 slots, BF16, 128: 62 us with the few-rows kernel, 32 with the
+  // other; 192: 72, 44; 8 behind 8000: 55, 40; one behind 8000: 18, 21). More than two tiles at
+  // head dim 64 (8 behind 8000, 8 kv heads: 46, 51; one: 14, 19) and for Q8_0 (64 behind 1000,
+  // 128: 33, 49; one behind 8000: 16, 22), which it converts for all its columns.
+  const bool q8 = c.head_bytes != kv_head_bytes(false, c.dim, c.ps);
+  const int few = q8 || c.dim < 96 ? 2 * kFewColumns : kFewColumns;
+  p->prompt = type == GGUF_KV_TYPE_BF16 && n_rows * p->group > few * n_seqs;
   // two tiles of columns where a sequence has more than one on average (F16, drafted tokens
   // of 4 heads of 128 behind 8000 slots: 8 x 5 54 us with one, which reads K and V twice, 45
   // with two; 16 x 8 93 and 75)
-  const bool q8 = c.head_bytes != kv_head_bytes(false, c.dim, c.ps);
   p->columns = p->prompt ? kPromptColumns
                : n_rows * p->group > kFewColumns * n_seqs ? attn_most_columns(q8, c.dim) : kFewColumns;
   const int tile = p->prompt ? kPromptSlots : kAttnTile;
@@ -61,7 +76,8 @@ static int extend_plan(const KvView& c, int32_t type, int64_t n_seqs, int64_t n_
     const int64_t blocks = p->groups == 2 || c.dim > 128 ? kPromptBlocks : 2 * kPromptBlocks;
     const int64_t want = cells > 0 && cells < blocks ? blocks / cells : 1;
     chunk = ((span + want - 1) / want + 63) / 64 * 64;
-    if (chunk < kPromptLeast) chunk = kPromptLeast;
+    p->least = (int32_t)kPromptLeast * p->groups;
+    if (chunk < p->least) chunk = p->least;
     p->fill = (int32_t)blocks;
   } else {
     const int64_t round = kAttnTile * kAttnWaves;
@@ -73,7 +89,7 @@ static int extend_plan(const KvView& c, int32_t type, int64_t n_seqs, int64_t n_
     if (chunk < kAttnLeast) chunk = kAttnLeast;
     if (span <= 4 * round) chunk = 4 * round;
     if (chunk > most) chunk = most;
-    p->fill = 0;
+    p->fill = p->least = 0;
   }
   p->chunk = (int32_t)chunk;
   p->splits = (int32_t)((span + chunk - 1) / chunk);
@@ -81,7 +97,7 @@ static int extend_plan(const KvView& c, int32_t type, int64_t n_seqs, int64_t n_
   // the device: 256 rows behind 8000 slots under a bound of 131072, 166 us with the host's
   // chunks, 41 so. (The kernel for few rows has short chunks anyway, and more blocks that
   // find nothing: 8 x 5 rows behind 3000 slots under 131072, 43 us without and 67 so.)
-  if (p->splits == 1 || chunk <= kPromptLeast || n_seqs > 64) p->fill = 0;
+  if (p->splits == 1 || chunk <= p->least || n_seqs > 64) p->fill = 0;
   const int64_t partials = p->splits > 1 ? abi_mul(n_rows * n_heads, p->splits) : 0;
   const int64_t ob = abi_mul(partials, c.dim * 4), mb = abi_mul(partials, 8);
   if (partials < 0 || ob < 0 || mb < 0 || ob > INT64_MAX - mb - 16) return GGUF_QK_ERR_LIMIT;
@@ -186,7 +202,7 @@ int gguf_attn_extend(const gguf_kv_cache* cache, const void* q, int32_t type, in
   a.unit = p.unit;
   a.fill = p.fill;
   a.round = kPromptSlots;
-  a.least = kPromptLeast;
+  a.least = p.least;
   const dim3 grid((unsigned)a.c.hkv, (unsigned)p.tiles, (unsigned)p.splits);
   a.tiles = (int32_t)p.tiles;
   if (p.prompt) {

@@ -2,8 +2,7 @@
 // queries; gguf_attn_extend in include/gguf_tokens.h).
 //
 // A block takes 128 columns, (row, query head) pairs of one kv head, 32 per wave, and
-// walks over the slots they see in tiles of 64 (32 past head dim 128), which its waves
-// share in LDS:
+// walks over the slots they see in tiles of 64, which its waves share in LDS:
 //   S^T = K Q^T    32 x 32 tiles, A = K (rows: slots), B = Q (columns), in registers
 //   O^T += V^T P^T A = V^T (rows: dims), B = P^T
 // Transposed products leave a lane with one column throughout, so that the running
@@ -11,7 +10,21 @@
 // half). K's rows lie in LDS with bits 2 and 3 of the slot swapped: the sixteen
 // scores of a lane then are two runs of eight consecutive slots, which is the B operand
 // of the second product as it stands, and V, stored transposed in the cache, is its A
-// operand.
+// operand. Columns are pairs so that the query heads of a kv head share its K and V, and
+// the causal mask costs a tile or two per block, not one per head.
+//
+// Bound: the matrix units' power. 16384 tokens, causal, 16 heads of 128 over 4, BF16:
+// 1.06 ms, 1.04 PFLOP/s, where a library product of 8192 x 8192 x 8192 reaches 1.19 (with
+// inputs of zeros the two reach 1.33 and 1.79: the clock follows the power that the data
+// draws). What the order of instructions gave (prompt of 4096): the vector work of a
+// half tile's softmax between the matrix instructions of the other half's product, operands
+// read from LDS four instructions ahead, 229 -> 167 us at head dim 256, 147 -> 130 at 192.
+// At smaller sizes a block's start and end, about 10 us (its place, the page ids, q, the
+// first tiles of K and V in turn; the join of the two groups and the store), beside 2.2 us
+// per pair of tiles: one prompt of 4096 90 - 104 us (0.66 - 0.76 PFLOP/s), of 512 18.
+//
+// Weights enter the second product as bf16 (BF16 caches) or fp16, as the values do: a
+// wider weight would double the product. Maxima, sums and outputs are fp32.
 #pragma once
 
 #include "attn.hpp"
@@ -276,7 +289,10 @@ __global__ __launch_bounds__(kPromptThreads * GROUPS, NB <= 4 ? 2 : 1) void attn
     k_lo = k_target(lane);
     v_lo = v_target(lane);
   }
-  auto fetch = [&](auto is_k, int v) {
+  // (Inlined by force: of a call the compiler keeps what the lambdas capture, all of the
+  // kernel's state, in scratch memory; 8 sequences of 8 rows behind 500 slots took 127 us so
+  // at head dim 256, 32 inlined.)
+  auto fetch = [&](auto is_k, int v) __attribute__((always_inline)) {
     if constexpr (Q8) {
       constexpr bool K = decltype(is_k)::value;
       if constexpr (K) {
@@ -319,11 +335,13 @@ __global__ __launch_bounds__(kPromptThreads * GROUPS, NB <= 4 ? 2 : 1) void attn
   };
   // A value enters fp16 as code * (d 2^e), e 0 for a greatest scale of the tile from 2^-7 to
   // 2^8 and else such that it comes to [2^7, 2^8) (or e to 15): the nearest fp16 of the
-  // value, or within 2^-18 of the greatest scale. K's scores take 2^-e back tile by tile; V's sums are kept in units of 2^-ve, which follow
-  // the greatest scale met so far.
+  // value, or within 2^-18 of the greatest scale. (fp16 holds a code exactly, not its product
+  // with a scale: two parts would double both products.) K's scores take 2^-e back tile by
+  // tile; V's sums are kept in units of 2^-ve, which follow the greatest scale met so far.
+  // The conversions double the vector work: 1024 rows behind 30000 slots 400 us, F16 285.
   int ke = 0, ve = 0;
   bool first_v = true;
-  auto settle = [&](auto is_k, uint64_t here) {
+  auto settle = [&](auto is_k, uint64_t here) __attribute__((always_inline)) {
     if constexpr (Q8) {
       constexpr bool K = decltype(is_k)::value;
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -373,7 +391,7 @@ __global__ __launch_bounds__(kPromptThreads * GROUPS, NB <= 4 ? 2 : 1) void attn
   // scales, the first eight codes, the others.
   uint32_t to_lo = 0, bits = 0;
   uint4 d0, d1;
-  auto convert = [&](auto is_k, int chunk, int buf, uint64_t here) {
+  auto convert = [&](auto is_k, int chunk, int buf, uint64_t here) __attribute__((always_inline)) {
     if constexpr (Q8) {
       constexpr bool K = decltype(is_k)::value;
       const int i = chunk / 3, part = chunk % 3;
@@ -434,7 +452,7 @@ __global__ __launch_bounds__(kPromptThreads * GROUPS, NB <= 4 ? 2 : 1) void attn
   };
   using K_ = std::true_type;
   using V_ = std::false_type;
-  auto convert_all = [&](auto is_k, int buf, uint64_t here) {
+  auto convert_all = [&](auto is_k, int buf, uint64_t here) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < 3 * RUNS; ++i) convert(is_k, i, buf, here);
   };
@@ -573,7 +591,7 @@ __global__ __launch_bounds__(kPromptThreads * GROUPS, NB <= 4 ? 2 : 1) void attn
   };
 
   // One tile, in buffer BUF.
-  auto step = [&](auto buffer) {
+  auto step = [&](auto buffer) __attribute__((always_inline)) {
     constexpr int BUF = decltype(buffer)::value;
     constexpr uint32_t kt = BUF * Tile::kBytes, vt = BUF * Tile::kBytes;
     const int v0 = mine(first), real0 = real_of(v0);

@@ -4,6 +4,10 @@
 // all heads (fp64 turns, so that far positions keep their angle: fp32 would lose
 // 2^-24 of 131072 radians), into LDS; then groups of lanes take a head each. A lane
 // holds whole pairs: two runs of VEC elements half a rotation apart, or adjacent ones.
+//
+// Bound: HBM, one read and one write of q and k. 8192 tokens of 32 + 8 heads of 128, bf16:
+// 27 us with the rows in the Infinity Cache, 38 without (168 MB, 4.4 TB/s, as a copy of
+// that size). 16 tokens: 5 us, a launch, the position and one row in turn.
 #pragma once
 
 #include "device_common.hpp"

@@ -90,12 +90,15 @@ int gguf_qk_rope(const void* q, int64_t q_stride, void* q_out, int64_t q_out_str
  * aligned), out may not overlap an input. max_len (<= 2^25) bounds the lengths:
  * longer sequences are taken to end there, as at the table's row.
  *
- * Accuracy. F32: that of gguf_attn_decode. BF16: scores from exact products of the
- * cache's values (Q8_0: of their nearest fp16) with q, sums and softmax in fp32; where
- * rows fill the matrix tiles (more than 32 rows times query heads per kv head and
- * sequence on average) the softmax weights enter the second product rounded to the
- * operand type: bf16 for a BF16 cache (2^-8 of each weight), fp16 otherwise (2^-11 of
- * each, or 2^-25 of the row's greatest); the output is rounded once.
+ * Accuracy. F32: that of gguf_attn_decode. BF16: scores and sums in fp32, and where a
+ * sequence has on average more than 32 rows times query heads per kv head (16 for F16 and
+ * BF16 caches of head dims from 96 on):
+ *   scores from exact products of q with the cache's values (Q8_0: the nearest fp16 of a
+ *     value, or within 2^-18 of the greatest scale of the slots read);
+ *   softmax weights rounded to the operand type of the second product: bf16 for a BF16
+ *     cache (2^-8 of each weight), fp16 otherwise (2^-11 of each, or 2^-25 of the row's
+ *     greatest).
+ * Below that as F32; the output is rounded once.
  * q, and keys and values within the length, have to be finite, as have their scaled
  * scores. */
 int64_t gguf_attn_extend_workspace(const gguf_kv_cache* cache, int32_t type, int64_t n_seqs,
