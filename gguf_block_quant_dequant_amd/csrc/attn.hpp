@@ -23,6 +23,14 @@
 // run at a fraction of their rate (16 columns for n_heads / n_kv_heads heads,
 // times two or three parts of the fp32 operand), which costs nothing here and
 // keeps fp32 accuracy.
+//
+// The same kernel over AttnRowsArgs is the attention of several new tokens
+// (gguf_attn_extend in include/gguf_tokens.h) where a sequence has few: the
+// columns are (row, query head) pairs, 16 or 32 of them beside one read of K and
+// V. 64 sequences of one token behind a window of 4096 and 4 first slots, BF16: 93 us
+// (476 MB, 5.1 TB/s); 8 of 3 to 5 behind 5000 to 8187 slots, F16: 30 us (109 MB, 3.6
+// TB/s: two blocks per CU of which each has 2 to 4 steps, their starts and joins
+// beside little reading) and 6 the join.
 #pragma once
 
 #include <type_traits>
@@ -506,7 +514,13 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const ARGS a)
   }
 
   // q of this lane's head: the B operand, dims 32 b + 8 g .. + 7
-  Q q[CT][NB];
+  // Two tiles' parts of q take up to 96 registers at head dim 128 (BF16; one wave per SIMD
+  // fits then): in LDS, where the block holds them once. 64 sequences of 5 rows of 4 heads
+  // behind 4000 slots: 151 us in registers, 127 so. (F16 at 64 and 128 keeps two waves or
+  // three either way, and registers.)
+  constexpr bool QL = CT == 2 && (KIND != kKvF16 || NB == 3 || NB > 4);
+  Q q[QL ? 1 : CT][NB];
+  __shared__ __align__(16) uint4 q_lds[QL ? CT * NB * Q::kN * 64 : 1];
   float sfac[CT];   // undoes the row's power-of-two scale (fp16 parts)
 #pragma unroll
   for (int u = 0; u < CT; ++u) {
@@ -557,8 +571,15 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const ARGS a)
       sfac[u] = __builtin_ldexpf(1.0f, -e);
     }
 #pragma unroll
-    for (int b = 0; b < NB; ++b) q[u][b].set(x[b]);
+    for (int b = 0; b < NB; ++b) {
+      q[QL ? 0 : u][b].set(x[b]);
+      if (QL && wave == 0) {
+#pragma unroll
+        for (int i = 0; i < Q::kN; ++i) q_lds[((u * NB + b) * Q::kN + i) * 64 + lane] = q[0][b].p[i];
+      }
+    }
   }
+  if constexpr (QL) __syncthreads();
 
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
   f32x4 o[CT][NT];
@@ -596,6 +617,24 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const ARGS a)
       };
       tile(std::integral_constant<int, 0>{});
       tile(std::integral_constant<int, 1>{});
+    } else if constexpr (QL) {
+      int at = u * NB * Q::kN * 64 + lane;
+      asm volatile("" : "+v"(at));   // read in each step, not kept
+      f32x4 acc[J / 4];
+#pragma unroll
+      for (int t = 0; t < J / 4; ++t) acc[t] = zero;
+#pragma unroll
+      for (int i = Q::kN - 1; i >= 0; --i)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const uint4 x = q_lds[at + (b * Q::kN + i) * 64];
+#pragma unroll
+          for (int t = 0; t < J / 4; ++t) acc[t] = attn_mfma<PART>(K.x[t][b], x, acc[t]);
+        }
+#pragma unroll
+      for (int t = 0; t < J / 4; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[4 * t + i] = acc[t][i] * sfac[u];
     } else {
 #pragma unroll
       for (int t = 0; t < J / 4; ++t) {

@@ -14,6 +14,7 @@ constexpr int64_t kExtendMaxLen = int64_t(1) << 25;
 constexpr int64_t kExtendBlocks = 1024;
 constexpr int64_t kExtendChunk = 1024;    // longest chunk of positions of the few-rows kernel
 constexpr int kFewColumns = 16;           // columns of its tiles
+constexpr int64_t kTwoTileReads = 65536;  // slots of all sequences
 constexpr int64_t kPromptBlocks = 256;    // blocks that run at once: one per CU, or two of one group of waves to head dim 128
 // Blocks from which one group of waves each, two blocks at a time, does better: 8 prompts
 // to 4096 (4680 blocks) 560 us against 685; one of 4096 (512) 110 against 104.
@@ -51,11 +52,14 @@ static int extend_plan(const KvView& c, int32_t type, int64_t n_seqs, int64_t n_
   const bool q8 = c.head_bytes != kv_head_bytes(false, c.dim, c.ps);
   const int few = q8 || c.dim < 96 ? 2 * kFewColumns : kFewColumns;
   p->prompt = type == GGUF_KV_TYPE_BF16 && n_rows * p->group > few * n_seqs;
-  // two tiles of columns where a sequence has more than one on average (F16, drafted tokens
-  // of 4 heads of 128 behind 8000 slots: 8 x 5 54 us with one, which reads K and V twice, 45
-  // with two; 16 x 8 93 and 75)
-  p->columns = p->prompt ? kPromptColumns
-               : n_rows * p->group > kFewColumns * n_seqs ? attn_most_columns(q8, c.dim) : kFewColumns;
+  // Two tiles of columns where a sequence has more than one on average (F16, 5 rows of 4 heads
+  // of 128 behind 8000 slots: 8 sequences 54 us with one, which reads K and V twice, 45 with
+  // two; 16 x 8 93 and 73). Past head dim 128 one wave per SIMD is left and one tile has twice
+  // the blocks: two where the reads outweigh that (256, 64 sequences behind 4000 slots: 205,
+  // 150; 16 x 8 behind 8000: 115, 105; 8 x 5 behind 8000: 69, 74; one: 22, 26).
+  const int64_t reads = n_seqs * (window > 0 && window < max_len ? window : max_len);
+  const bool two = n_rows * p->group > kFewColumns * n_seqs && (c.dim <= 128 || reads > kTwoTileReads);
+  p->columns = p->prompt ? kPromptColumns : two ? attn_most_columns(q8) : kFewColumns;
   const int tile = p->prompt ? kPromptSlots : kAttnTile;
   p->unit = c.ps > tile ? c.ps : tile;
   p->tiles = (n_rows * p->group + n_seqs * (p->columns - 1)) / p->columns;

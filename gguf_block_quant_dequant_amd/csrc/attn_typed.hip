@@ -13,7 +13,7 @@ static void launch_dim(const AttnArgs& a, bool track, dim3 grid, hipStream_t str
 
 template <int NB>
 static void launch_dim(const AttnRowsArgs& a, int columns, dim3 grid, hipStream_t stream) {
-  if constexpr (attn_most_columns(GQK_KV_KIND == 2, NB * 32) == 32) {
+  if constexpr (attn_most_columns(GQK_KV_KIND == 2) == 32) {
     if (columns == 32) {
       hipLaunchKernelGGL((attn_decode_kernel<GQK_KV_KIND, NB, false, AttnRowsArgs, 2>), grid, dim3(kAttnThreads), 0,
                          stream, a);

@@ -118,6 +118,19 @@ def test_bf16_rows_equal_each_other_however_they_are_grouped():
             check(part, some([b - a], 13))
 
 
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_drafts_under_loose_bounds(kind, dim):
+    # two tiles of columns beside one read (F16 and BF16: past head dim 128 where the bound is far)
+    rng = np.random.default_rng([29, dim])
+    for rows in ([9, 7, 1], [1, 1, 1], [11, 0, 23]):
+        d = make_rows(rng, TYPES[kind], [700, 90, 40], rows, -(-700 // 32) + 1, 6, 2, dim, 32, False)
+        say("drafts", kind, dim, rows)
+        check(d, None, 700, 131072, 1 << 22, 300)
+        check(d, None, 700, 131072, window=100, sinks=5)
+        check(d, None, 131072, window=70000, sinks=40)
+
+
 PROFILES = {
     "small": lambda n, rng: 2.0 ** rng.uniform(-22, -12, n),
     "tiny": lambda n, rng: np.full(n, 2.0 ** -24),
