@@ -207,6 +207,26 @@ __device__ __forceinline__ RowsPlan attn_rows_plan(const AttnRowsArgs& a, int ta
   return p;
 }
 
+// Whether any sequence reaches a split of chunks by the bound. Under a loose bound most
+// blocks find that none does, and with few waves per SIMD what each of them takes counts: up
+// to 64 lengths are scalar loads (64 sequences of one token behind 1000 slots under a bound of
+// 131072, 32768 blocks: 65 us, 124 when each looks for its place first; 100 of 5: 126, 314).
+// Calls of few splits mostly reach them, and would pay 1 % for it. All 64 lanes of a wave
+// call it.
+constexpr int kReachSplits = 8;
+__device__ __forceinline__ bool attn_rows_reach(const AttnRowsArgs& a, int split, int lane) {
+  const int64_t at = (int64_t)split * a.chunk;
+  if (a.n_seqs <= 64) {
+    int32_t longest = 0;
+#pragma unroll 8
+    for (int i = 0; i < a.n_seqs; ++i) longest = a.lengths[i] > longest ? a.lengths[i] : longest;
+    return longest > at;
+  }
+  for (int s0 = 0; s0 < a.n_seqs; s0 += 64)
+    if (__any(s0 + lane < a.n_seqs && a.lengths[s0 + lane] > at)) return true;
+  return false;
+}
+
 // Two values rounded to fp16 (nearest-even), in one instruction.
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ f16x2 to_f16x2(float a, float b) {
@@ -347,6 +367,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const ARGS a)
   int row_held = 0, row_chunk = 0;
   if constexpr (ROWS) {
     h = blockIdx.x;
+    if (split > 0 && a.splits > kReachSplits && !attn_rows_reach(a, split, lane)) return;
     const RowsPlan p = attn_rows_plan<COLS>(a, (int)((blockIdx.y + blockIdx.z) % gridDim.y), lane);
     if (p.t.seq < 0) return;
     s = p.t.seq;
