@@ -99,8 +99,9 @@ static int extend_plan(const KvView& c, int32_t type, int64_t n_seqs, int64_t n_
   p->splits = (int32_t)((span + chunk - 1) / chunk);
   // Under a bound above the lengths, the prompt kernel's chunks are cut to the lengths on
   // the device: 256 rows behind 8000 slots under a bound of 131072, 166 us with the host's
-  // chunks, 41 so. (The kernel for few rows has short chunks anyway, and more blocks that
-  // find nothing: 8 x 5 rows behind 3000 slots under 131072, 43 us without and 67 so.)
+  // chunks, 41 so. (The kernel for few rows holds the page ids of 64 pages, so that its chunks
+  // cannot grow with the lengths; cut to them, 8 x 5 rows behind 3000 slots under 131072 took
+  // 67 us and 43 without, 30 since empty blocks end early.)
   if (p->splits == 1 || chunk <= p->least || n_seqs > 64) p->fill = 0;
   const int64_t partials = p->splits > 1 ? abi_mul(n_rows * n_heads, p->splits) : 0;
   const int64_t ob = abi_mul(partials, c.dim * 4), mb = abi_mul(partials, 8);

@@ -36,7 +36,7 @@ typedef struct gguf_rope {
   const int32_t* axes;   /* device, n_rot / 2: the position axis of each pair (time,
                             height, width of image and video tokens, in sections or by
                             turns), a value outside 0 .. n_axes - 1 leaves the pair
-                            unturned; NULL: axis 0 for all */
+                            unturned (angle 0); NULL: axis 0 for all */
   const int32_t* pos;    /* device, [n_axes] rows of n_tokens positions */
   int64_t pos_stride;    /* from axis to axis, >= n_tokens */
   int32_t n_axes;        /* 1 .. 16 */
@@ -129,8 +129,8 @@ int gguf_attn_extend(const gguf_kv_cache* cache, const void* q, int32_t type, in
  * the drafted token. accept_prob[r] (may be NULL) = min(1, p[t] / q[t]), 1 for a
  * sequence's last row; 0 for a token outside 0 .. vocab - 1, which is never accepted.
  * A sequence without rows has accepted 0 and next -1. Logits of -inf (ruled out) have
- * probability 0; a row without a finite greatest logit (all -inf, NaN, +inf) accepts
- * nothing, has accept_prob 0, and draws -1. Rows of no sequence are left alone.
+ * probability 0; a row without a finite greatest logit (all -inf, NaN, +inf), of
+ * target or draft, accepts nothing, has accept_prob 0, and draws -1. Rows of no sequence are left alone.
  *
  * target and draft of one type, F32 or BF16, [n_rows][vocab], strides in elements from
  * row to row (>= vocab), aligned to their elements. Exponentials (to 2^-43) and sums
