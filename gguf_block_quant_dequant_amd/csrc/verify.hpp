@@ -16,7 +16,7 @@
 // and their chains of loads at small ones. 32 sequences of 2 to 7 drafts over 128256 values, fp32,
 // both sides: sums 43 us (180 MB, 4.2 TB/s; 33 without the exponentials, 49 with a
 // polynomial of degree 10 in place of the table), choose 14 (18 with blocks of 1024 threads,
-// whose registers let one of them run per CU), draw 11. One sequence of 4 drafts: 6, 5, 7.
+// whose registers let one of them run per CU), draw 10. One sequence of 4 drafts: 6, 5, 7.
 #pragma once
 
 #include "token_rows.hpp"
@@ -416,18 +416,23 @@ __global__ __launch_bounds__(kDrawThreads) void verify_draw_kernel(const VerifyA
   using Values = VerifyValues<BF16, WIDE, kDrawThreads>;
   constexpr int PER = Values::PER;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, s = blockIdx.x;
-  VerifyChoice ch = a.choice[s];
-  if (ch.row < 0) return;
-  const double c = verify_scale(verify_temperature(a, s)), u = (double)a.uniform_next[s];
+  // everything that is at a known place is asked for at once, before any of it is looked at
   const double* rest = a.rest + (int64_t)s * a.splits;
-  const double2* part = a.part + ch.row * a.splits;
+  const double rest0 = lane < a.splits ? rest[lane] : 0.0;
+  const double t = verify_temperature(a, s), u = (double)a.uniform_next[s];
+  VerifyChoice ch = a.choice[s];
   __shared__ double powers[32];
   load_powers(powers, tid);
   __syncthreads();
+  if (ch.row < 0) return;
+  const double c = verify_scale(t);
+  const int64_t refused = ch.mode == kDrawOneHot ? a.tokens[ch.row] : -1;
+  const double2* part = a.part + ch.row * a.splits;
   bool all = false;   // p - q is nowhere above 0: from p
   auto split_sum = [&](int i) -> double {
     if (i >= a.splits) return 0.0;
-    return all ? part[i].y * exp2_f64((part[i].x - ch.mp) * c, powers) : rest[i];
+    if (all) return part[i].y * exp2_f64((part[i].x - ch.mp) * c, powers);
+    return i < 64 ? rest0 : rest[i];   // (i % 64 is the lane)
   };
   // every wave goes through the splits' sums, 64 at a time
   auto whole = [&]() {
@@ -462,17 +467,17 @@ __global__ __launch_bounds__(kDrawThreads) void verify_draw_kernel(const VerifyA
   // The split's logits in LDS, in order: thread t weighs values PER t .. (a word of pad per PER).
   __shared__ float logits[2][kVerifySplit + kVerifySplit / PER];
   const bool two = ch.mode == kDrawRest;
-  for (int k = 0; k < (two ? 2 : 1); ++k) {
-    Values v;
-    v.load(a, k, ch.row, split, tid);
+  Values p, q;
+  p.load(a, 0, ch.row, split, tid);
+  if (two) q.load(a, 1, ch.row, split, tid);
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int i = Values::index(j, tid);
-      logits[k][i + i / PER] = v.x[j];
-    }
+  for (int j = 0; j < PER; ++j) {
+    const int i = Values::index(j, tid);
+    logits[0][i + i / PER] = p.x[j];
+    if (two) logits[1][i + i / PER] = q.x[j];
   }
   __syncthreads();
-  const int token = ch.mode == kDrawOneHot ? a.tokens[ch.row] - split * kVerifySplit : -1;
+  const int64_t token = refused - (int64_t)split * kVerifySplit;
   double w[PER], sum = 0.0;
   int tail = -1;   // last value with any weight
 #pragma unroll
