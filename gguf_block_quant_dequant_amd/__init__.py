@@ -965,8 +965,9 @@ def _source_id(dtype):
 
 def gguf_attn_extend_workspace(cache: KvCache, dtype, n_seqs: int, n_rows: int, n_heads: int, max_len: int,
                                window: int = 0, sinks: int = 0) -> int:
-    """Bytes of workspace of a gguf_attn_extend call with queries of this dtype, or a
-    negative status."""
+    """Bytes of workspace of gguf_attn_extend calls with queries of this dtype, at most
+    n_seqs sequences, n_rows rows and max_len, and this window and sinks, or a negative
+    status."""
     return lib().gguf_attn_extend_workspace(cache.address, _source_id(dtype), n_seqs, n_rows, n_heads, max_len, window,
                                             sinks)
 

@@ -12,7 +12,8 @@ constexpr int64_t kExtendMaxLen = int64_t(1) << 25;
 // 8187 slots, F16: 40 us with 512, 34.5 with 1024, 42 with 2048; the same of 5 behind 8000,
 // BF16: 53, 54, 68).
 constexpr int64_t kExtendBlocks = 1024;
-constexpr int64_t kExtendChunk = 1024;    // longest chunk of positions of the few-rows kernel
+constexpr int64_t kExtendChunk = 1024;    // longest chunk of positions of the few-rows kernel: 64 pages of 16
+constexpr int64_t kExtendOnce = 4 * kAttnTile * kAttnWaves;   // positions that it does not split
 constexpr int kFewColumns = 16;           // columns of its tiles
 constexpr int64_t kTwoTileReads = 65536;  // slots of all sequences
 constexpr int64_t kPromptBlocks = 256;    // blocks that run at once: one per CU, or two of one group of waves to head dim 128
@@ -30,8 +31,67 @@ struct ExtendPlan {
   bool prompt;                // the kernel for many rows
   int32_t group, splits, chunk, unit, columns, groups, fill, least;
   int64_t tiles;              // tiles of columns, at most
-  int64_t ml_bytes, bytes;
+  int64_t ml_bytes, bytes;    // where the partial outputs lie; the workspace named
 };
+
+// (row, query head) pairs per sequence up to which BF16 queries stay with the kernel for few
+// rows (see extend_plan).
+static int64_t few_pairs(const KvView& c, bool q8) {
+  return q8 || c.dim < 96 ? 2 * kFewColumns : kFewColumns;
+}
+
+// Positions that the columns of a tile read, at most: the first slots, the window and the
+// tile's rows, in whole units.
+static int64_t tile_span(int64_t max_len, int64_t window, int64_t sinks, int64_t columns, int64_t group, int64_t unit) {
+  int64_t span = max_len;
+  if (window > 0 && window < max_len) {
+    const int64_t pad = (sinks + unit - 1) / unit * unit;
+    const int64_t seen = pad + window + (columns - 1) / group + 1 + unit;
+    if (seen < span) span = seen;
+  }
+  return span < 1 ? 1 : span;
+}
+
+// Blocks that a call of the kernel for many rows aims for.
+static int64_t prompt_blocks(int groups, int dim) {
+  return groups == 2 || dim > 128 ? kPromptBlocks : 2 * kPromptBlocks;
+}
+
+// Partial results (rows times query heads times splits) of the largest call with at most
+// these sequences and rows and this bound; 0 where no such call is split. Splits are at most
+// the blocks aimed for over the cells (tiles times kv heads), so that rows * n_heads * splits <=
+// columns * blocks; with the longest chunks of the few-rows kernel they are span / longest; and
+// never more than the shortest chunks give. (rows * group <= columns * tiles.) Each of these
+// grows with the sequences, the rows and the bound.
+static int64_t most_partials(const KvView& c, int32_t type, bool q8, int64_t group, int64_t n_seqs, int64_t n_rows,
+                             int64_t n_heads, int64_t max_len, int64_t window, int64_t sinks) {
+  if (n_seqs == 0 || n_rows == 0) return 0;
+  const bool bf16 = type == GGUF_KV_TYPE_BF16;
+  const int64_t few = few_pairs(c, q8);
+  const int64_t fewest = bf16 && few * n_seqs / group < n_rows ? few * n_seqs / group : n_rows;   // of the few-rows kernel
+  const int columns = attn_most_columns(q8);
+  int64_t most = 0;
+  int64_t span = tile_span(max_len, window, sinks, columns, group, c.ps > kAttnTile ? c.ps : kAttnTile);
+  if (span > kExtendOnce) {
+    const int64_t rows = fewest * n_heads, least = rows * ((span + kAttnLeast - 1) / kAttnLeast);
+    const int64_t longest = rows * ((span + kExtendChunk - 1) / kExtendChunk);
+    most = columns * kExtendBlocks;
+    if (most < longest) most = longest;
+    if (most > least) most = least;
+  }
+  if (bf16 && n_rows * group > few) {
+    span = tile_span(max_len, window, sinks, kPromptColumns, group, c.ps > kPromptSlots ? c.ps : kPromptSlots);
+    const int groups = prompt_groups(q8, c.dim);   // where positions are split
+    const int64_t shortest = kPromptLeast * groups;
+    if (span > shortest) {
+      int64_t partials = kPromptColumns * prompt_blocks(groups, c.dim);
+      const int64_t least = n_rows * n_heads * ((span + shortest - 1) / shortest);
+      if (partials > least) partials = least;
+      if (most < partials) most = partials;
+    }
+  }
+  return most;
+}
 
 static int extend_plan(const KvView& c, int32_t type, int64_t n_seqs, int64_t n_rows, int64_t n_heads, int64_t max_len,
                        int64_t window, int64_t sinks, ExtendPlan* p) {
@@ -50,8 +110,7 @@ static int extend_plan(const KvView& c, int32_t type, int64_t n_seqs, int64_t n_
   // head dim 64 (8 behind 8000, 8 kv heads: 46, 51; one: 14, 19) and for Q8_0 (64 behind 1000,
   // 128: 33, 49; one behind 8000: 16, 22), which it converts for all its columns.
   const bool q8 = c.head_bytes != kv_head_bytes(false, c.dim, c.ps);
-  const int few = q8 || c.dim < 96 ? 2 * kFewColumns : kFewColumns;
-  p->prompt = type == GGUF_KV_TYPE_BF16 && n_rows * p->group > few * n_seqs;
+  p->prompt = type == GGUF_KV_TYPE_BF16 && n_rows * p->group > few_pairs(c, q8) * n_seqs;
   // Two tiles of columns where a sequence has more than one on average (F16, 5 rows of 4 heads
   // of 128 behind 8000 slots: 8 sequences 54 us with one, which reads K and V twice, 45 with
   // two; 16 x 8 93 and 73). Past head dim 128 one wave per SIMD is left and one tile has twice
@@ -64,20 +123,12 @@ static int extend_plan(const KvView& c, int32_t type, int64_t n_seqs, int64_t n_
   p->unit = c.ps > tile ? c.ps : tile;
   p->tiles = (n_rows * p->group + n_seqs * (p->columns - 1)) / p->columns;
   if (p->tiles > 65535) return GGUF_QK_ERR_LIMIT;   // along a grid axis
-  // positions that a tile's columns read, at most: the first slots, the window
-  // and the tile's rows, in whole units
-  int64_t span = max_len;
-  if (window > 0 && window < max_len) {
-    const int64_t pad = (sinks + p->unit - 1) / p->unit * p->unit;
-    const int64_t seen = pad + window + (p->columns - 1) / p->group + 1 + p->unit;
-    if (seen < span) span = seen;
-  }
-  if (span < 1) span = 1;
+  const int64_t span = tile_span(max_len, window, sinks, p->columns, p->group, p->unit);
   const int64_t cells = p->tiles * c.hkv;
   int64_t chunk;
   if (p->prompt) {
     p->groups = cells < kPromptSingle ? prompt_groups(q8, c.dim) : 1;
-    const int64_t blocks = p->groups == 2 || c.dim > 128 ? kPromptBlocks : 2 * kPromptBlocks;
+    const int64_t blocks = prompt_blocks(p->groups, c.dim);
     const int64_t want = cells > 0 && cells < blocks ? blocks / cells : 1;
     chunk = ((span + want - 1) / want + 63) / 64 * 64;
     p->least = (int32_t)kPromptLeast * p->groups;
@@ -85,14 +136,12 @@ static int extend_plan(const KvView& c, int32_t type, int64_t n_seqs, int64_t n_
     p->fill = (int32_t)blocks;
   } else {
     const int64_t round = kAttnTile * kAttnWaves;
-    int64_t most = int64_t(64) << c.shift;
-    if (most > kExtendChunk) most = kExtendChunk;
     int64_t want = cells > 0 ? kExtendBlocks / cells : 1;
     if (want < 1) want = 1;
     chunk = ((span + want - 1) / want + round - 1) / round * round;
     if (chunk < kAttnLeast) chunk = kAttnLeast;
-    if (span <= 4 * round) chunk = 4 * round;
-    if (chunk > most) chunk = most;
+    if (span <= kExtendOnce) chunk = kExtendOnce;
+    if (chunk > kExtendChunk) chunk = kExtendChunk;
     p->fill = p->least = 0;
   }
   p->chunk = (int32_t)chunk;
@@ -103,11 +152,11 @@ static int extend_plan(const KvView& c, int32_t type, int64_t n_seqs, int64_t n_
   // cannot grow with the lengths; cut to them, 8 x 5 rows behind 3000 slots under 131072 took
   // 67 us and 43 without, 30 since empty blocks end early.)
   if (p->splits == 1 || chunk <= p->least || n_seqs > 64) p->fill = 0;
-  const int64_t partials = p->splits > 1 ? abi_mul(n_rows * n_heads, p->splits) : 0;
-  const int64_t ob = abi_mul(partials, c.dim * 4), mb = abi_mul(partials, 8);
-  if (partials < 0 || ob < 0 || mb < 0 || ob > INT64_MAX - mb - 16) return GGUF_QK_ERR_LIMIT;
-  p->ml_bytes = (mb + 15) / 16 * 16;
-  p->bytes = p->ml_bytes + ob;
+  // (rows times heads below 2^39, splits at most 2^17)
+  const int64_t partials = most_partials(c, type, q8, p->group, n_seqs, n_rows, n_heads, max_len, window, sinks);
+  if (abi_mul(partials, c.dim * 4 + 16) < 0) return GGUF_QK_ERR_LIMIT;
+  p->bytes = (partials * 8 + 15) / 16 * 16 + partials * c.dim * 4;
+  p->ml_bytes = p->splits > 1 ? (n_rows * n_heads * p->splits * 8 + 15) / 16 * 16 : 0;
   return GGUF_QK_OK;
 }
 

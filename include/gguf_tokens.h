@@ -100,7 +100,16 @@ int gguf_qk_rope(const void* q, int64_t q_stride, void* q_out, int64_t q_out_str
  *     greatest).
  * Below that as F32; the output is rounded once.
  * q, and keys and values within the length, have to be finite, as have their scaled
- * scores. */
+ * scores.
+ *
+ * Workspace. The size named serves every call with at most as many sequences and rows and
+ * at most as large a bound, and the same cache, type, n_heads, window and sinks. It holds
+ * partial results, head_dim + 2 fp32 numbers per row, query head and part of the positions:
+ * at most 34 MB for prompts (BF16), but few rows and all F32 rows are cut into parts of at
+ * most 1024 slots of the bound (or of window and first slots) however many they are, so that
+ * there it grows with rows times bound: 64 sequences of 5 rows of 16 heads of 128 under a
+ * bound of 131072 341 MB, 4096 F32 rows under 32768 1.1 GB. Bounds near the lengths, BF16
+ * queries for prompts and calls over parts of the rows keep it small. */
 int64_t gguf_attn_extend_workspace(const gguf_kv_cache* cache, int32_t type, int64_t n_seqs,
                                    int64_t n_rows, int64_t n_heads, int64_t max_len, int64_t window,
                                    int64_t sinks);
