@@ -70,6 +70,16 @@ struct RopeRun {
   }
 };
 
+// The angle pos * freq in turns, without its whole ones: -1/2 .. 1/2. The roundings of the
+// products are carried along: fp64 alone would lose 2^-21 of a radian at 2^31 radians.
+__device__ __forceinline__ float rope_turn(double pos, double freq) {
+#pragma clang fp contract(off)
+  constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;   // 1 / (2 pi)
+  const double x = pos * freq, dx = __builtin_fma(pos, freq, -x);
+  const double t = x * kHi, dt = __builtin_fma(x, kHi, -t) + __builtin_fma(dx, kHi, x * kLo);
+  return (float)((t - __builtin_rint(t)) + dt);
+}
+
 // A unit is two runs of VEC elements: within n_rot VEC pairs, behind it plain
 // elements. UNITS per lane: 1 for runs of 16 bytes (head dims to 512 then take at
 // most 64 lanes), 4 for single elements.
@@ -84,11 +94,8 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(const RopeArgs a) {
     const int t = i / half, p = i - t * half;
     const int axis = a.axes ? a.axes[p] : 0;
     float2 cs = make_float2(1.f, 0.f);
-    if (axis >= 0 && axis < a.n_axes) {
-      const double turns = (double)a.pos[axis * a.pos_stride + t0 + t] * (a.freqs[p] * 0.15915494309189533577);
-      const float f = (float)(turns - __builtin_rint(turns));   // of a turn, -1/2 .. 1/2
-      sincospif(2.0f * f, &cs.y, &cs.x);
-    }
+    if (axis >= 0 && axis < a.n_axes)
+      sincospif(2.0f * rope_turn((double)a.pos[axis * a.pos_stride + t0 + t], a.freqs[p]), &cs.y, &cs.x);
     turn[i] = make_float2(cs.x * a.magnitude, cs.y * a.magnitude);
   }
   __syncthreads();

@@ -54,9 +54,9 @@ typedef struct gguf_rope {
  * q [n_tokens][n_heads * head_dim] and k [n_tokens][n_kv_heads * head_dim], strides in
  * elements from row to row; type F32 (GEMV outputs) or BF16 (prefill outputs),
  * outputs of the same type, all sums and products fp32, rounded once. Angles are
- * reduced in fp64: positions of any size lose nothing. q_norm and k_norm: fp32
- * [head_dim], either may be NULL (not normed). rope NULL: norms only. n_heads or
- * n_kv_heads may be 0 (its pointers are then not looked at).
+ * reduced in fp64 with what its products round off: positions of any size lose nothing.
+ * q_norm and k_norm: fp32 [head_dim], either may be NULL (not normed). rope NULL: norms
+ * only. n_heads or n_kv_heads may be 0 (its pointers are then not looked at).
  * head_dim even, 2 .. 512. q_out may be q and k_out may be k (same stride); otherwise
  * outputs may not overlap inputs or each other. Rows of q and k may lie interleaved in
  * one buffer (slices of one product's output) where their strides are equal. Pointers
