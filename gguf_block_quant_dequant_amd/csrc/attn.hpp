@@ -540,6 +540,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_decode_kernel(const ARGS a)
   // behind 4000 slots: 151 us in registers, 127 so. (F16 at 64 and 128 keeps two waves or
   // three either way, and registers.)
   constexpr bool QL = CT == 2 && (KIND != kKvF16 || NB == 3 || NB > 4);
+  static_assert(!QL || KIND != kKvQ80, "the scores of Q8_0 caches read q from registers, a set per tile");
   Q q[QL ? 1 : CT][NB];
   __shared__ __align__(16) uint4 q_lds[QL ? CT * NB * Q::kN * 64 : 1];
   float sfac[CT];   // undoes the row's power-of-two scale (fp16 parts)
