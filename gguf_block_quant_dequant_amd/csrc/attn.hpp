@@ -65,9 +65,14 @@ struct AttnRowsArgs : AttnArgs {
   int32_t sinks;
   int32_t bf16;               // q and out: BF16, not F32 (strides in elements)
   int32_t columns, unit;      // of a block; the unit of TileRange
-  int32_t fill;               // blocks aimed for; chunks by the lengths (fill > 0): at most 64 sequences
-  int32_t round, least;       // chunks are multiples of `round` and no less than `least`
+  // Tiles of kPromptColumns: blocks aimed for; chunks by the lengths (fill > 0): at most 64
+  // sequences; no chunk is less than `least`.
+  int32_t fill, least;
 };
+
+// Of the kernel for many rows (attn_prompt.hpp): columns of its tiles, whose chunks are
+// multiples of these slots.
+constexpr int kPromptColumns = 128, kPromptSlots = 64;
 
 constexpr int kAttnJ = 8;                 // positions of a lane
 constexpr int kAttnTile = 4 * kAttnJ;     // and of a wave's step
@@ -118,18 +123,17 @@ __device__ __forceinline__ int attn_chunk(const AttnArgs& a, int lane) {
   return c < a.chunk ? c : a.chunk;   // splits * a.chunk covers any length
 }
 
-// The same for several new tokens: chunks such that all column tiles of all sequences
-// make about a.fill blocks, and that the launched splits cover each. A lane's sequence
-// has these rows and slots. (Positions are split where the tiles times kv heads are fewer
-// than the blocks aimed for: their sums in units of 64 stay below 2^30.)
-template <int COLS>
+// The same for many new tokens: chunks such that all column tiles of all sequences make
+// about a.fill blocks, and that the launched splits cover each. A lane's sequence has these
+// rows and slots. (Positions are split where the tiles times kv heads are fewer than the
+// blocks aimed for: their sums in units of 64 stay below 2^30.)
 __device__ __forceinline__ int attn_rows_chunk(const AttnRowsArgs& a, const SeqRows& r, int held) {
   uint32_t total = 0, most = 0;
   if (r.rows > 0) {
     const int width = r.rows * a.group;   // all its columns as one tile: no tile reads more
     const TileRange t = tile_range(held, r.rows, a.group, 0, width, a.window, a.sinks, a.unit);
     most = t.n > 0 ? t.n : 0;
-    total = (most + 63) / 64 * ((width + COLS - 1) / COLS);
+    total = (most + 63) / 64 * ((width + kPromptColumns - 1) / kPromptColumns);
   }
   auto step = [&](uint32_t t, uint32_t m) {
     total += t;
@@ -145,11 +149,11 @@ __device__ __forceinline__ int attn_rows_chunk(const AttnRowsArgs& a, const SeqR
   const uint32_t cover = (most + a.splits - 1) / a.splits;
   c = c > cover ? c : cover;
   c = c < (uint32_t)a.least ? a.least : c;
-  c = (c + a.round - 1) / a.round * a.round;
+  c = (c + kPromptSlots - 1) / kPromptSlots * kPromptSlots;
   return (int)(c < (uint32_t)a.chunk ? c : a.chunk);   // splits * a.chunk covers any length
 }
-// For a block that knows its sequence: the chunk alone. All 64 lanes of a wave call it.
-template <int COLS>
+// For a block that knows its sequence: the chunk alone, of tiles of any size. All 64 lanes of
+// a wave call it.
 __device__ __forceinline__ int attn_rows_chunk(const AttnRowsArgs& a, int lane) {
   if (a.fill == 0) return a.chunk;
   SeqRows r = {0, 0};
@@ -158,7 +162,7 @@ __device__ __forceinline__ int attn_rows_chunk(const AttnRowsArgs& a, int lane) 
     r = seq_rows(a.row_start, lane, a.n_rows);
     held = (int)kv_length(a.lengths[lane], a.max_len, a.table_stride, a.c.shift);
   }
-  return attn_rows_chunk<COLS>(a, r, held);
+  return attn_rows_chunk(a, r, held);
 }
 
 // Where a block of COLS columns stands: tile `target` of all sequences' (seq -1: behind the
@@ -193,7 +197,9 @@ __device__ __forceinline__ RowsPlan attn_rows_plan(const AttnRowsArgs& a, int ta
     if (lane >= d) upto += o;
   }
   const uint64_t past = __ballot(upto > target);
-  if (a.fill != 0) p.chunk = attn_rows_chunk<COLS>(a, r, held);
+  if constexpr (COLS == kPromptColumns) {
+    if (a.fill != 0) p.chunk = attn_rows_chunk(a, r, held);
+  }
   if (!past) {
     p.t = {-1, 0, 0, 0};
     return p;
@@ -1097,12 +1103,8 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const AttnArgs 
     if (pos + j >= first && pos + j < n) w[j] = o[j] + acc[j];
 }
 
-// The chunk that the blocks took.
-__device__ __forceinline__ int attn_join_chunk(const AttnRowsArgs& a, int lane) {
-  return attn_rows_chunk<128>(a, lane);   // only tiles of 128 columns have chunks by the lengths
-}
-// The same for several new tokens per sequence: the splits of (row, query head), those
-// of the row's tile of columns. -1: the row belongs to no sequence.
+// Several new tokens per sequence: the splits of (row, query head), those of the row's
+// tile of columns. -1: the row belongs to no sequence.
 __device__ __forceinline__ int attn_row_splits(const AttnRowsArgs& a, int64_t row, int head, int chunk) {
   const SeqOf q = seq_of_row(a.row_start, a.n_seqs, a.n_rows, row);
   if (q.seq < 0) return -1;
@@ -1124,7 +1126,7 @@ template <int DIM>
 __global__ __launch_bounds__(kJoinThreads) void attn_join_rows_kernel(const AttnRowsArgs a) {
   const int tid = threadIdx.x, lane = tid & 63, head = blockIdx.y;
   const int64_t row = blockIdx.x;
-  const int splits = attn_row_splits(a, row, head, attn_join_chunk(a, lane));
+  const int splits = attn_row_splits(a, row, head, attn_rows_chunk(a, lane));
   if (splits < 0) return;
   f32x4 sum;
   bool store;
@@ -1139,7 +1141,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_few_kernel(const AttnR
   constexpr int kLanes = DIM / 4, kItems = kJoinThreads / kLanes;
   const int tid = threadIdx.x, c = tid % kLanes;
   const int64_t item = (int64_t)blockIdx.x * kItems + tid / kLanes;
-  const int chunk = attn_join_chunk(a, tid & 63);   // by all lanes
+  const int chunk = attn_rows_chunk(a, tid & 63);   // by all lanes
   if (tid >= kItems * kLanes || item >= a.n_rows * a.n_heads) return;
   const int64_t row = item / a.n_heads;
   const int head = (int)(item - row * a.n_heads);

@@ -255,7 +255,6 @@ int gguf_attn_extend(const gguf_kv_cache* cache, const void* q, int32_t type, in
   a.columns = p.columns;
   a.unit = p.unit;
   a.fill = p.fill;
-  a.round = kPromptSlots;
   a.least = p.least;
   const dim3 grid((unsigned)a.c.hkv, (unsigned)p.tiles, (unsigned)p.splits);
   a.tiles = (int32_t)p.tiles;

@@ -39,7 +39,6 @@ struct AttnPromptArgs : AttnRowsArgs {
   int32_t tiles;   // tiles of columns of the grid
 };
 
-constexpr int kPromptColumns = 128;
 constexpr int kPromptWaves = 4;     // that share a tile of slots
 constexpr int kPromptThreads = kPromptWaves * 64;
 // The maximum that weights are relative to is raised only where one exceeds it by a
@@ -57,8 +56,6 @@ __device__ __forceinline__ f32x16v prompt_mfma(const uint4& a, const uint4& b, c
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-constexpr int kPromptSlots = 64;   // of a tile
-
 // Slots of a tile, and where its values lie in LDS: rows of 16-byte chunks, a chunk at
 // chunk ^ swizzle(row), so that sixteen consecutive rows' chunks of one number lie in
 // sixteen different groups of banks.
@@ -73,7 +70,8 @@ struct PromptTile {
   __device__ static __forceinline__ int k_swizzle(int row) {
     return kKChunks % 16 == 0 ? row & 15 : kKChunks % 8 == 0 ? row >> 1 & 7 : row >> 2 & 3;
   }
-  __device__ static __forceinline__ int v_swizzle(int row) { return kVChunks == 8 ? row >> 1 & 7 : row >> 2 & 3; }
+  static_assert(kVChunks == 8, "v_swizzle");
+  __device__ static __forceinline__ int v_swizzle(int row) { return row >> 1 & 7; }
 };
 
 // Slot (within 32) of row `r` of K in LDS, and back.
