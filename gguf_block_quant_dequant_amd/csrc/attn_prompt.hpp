@@ -487,8 +487,9 @@ __global__ __launch_bounds__(kPromptThreads * GROUPS, NB <= 4 ? 2 : 1) void attn
     }
     factor = a.qscale == 0.f ? 1.f : fabsf(a.qscale);
     if constexpr (MM == kKvF16) {
-      // to fp16 (exact): the row's greatest magnitude goes to [512, 1024), what lies
-      // 2^-34 of it and lower loses bits
+      // to fp16: the row's greatest magnitude goes to [512, 1024). Exact down to 2^-26 of it
+      // (2^-17, whose eight bits end at fp16's last, 2^-24); what lies lower is within 2^-34 of
+      // it (half of that last place)
       float x[KS][8], amax = 0.f;
 #pragma unroll
       for (int k = 0; k < KS; ++k) {

@@ -16,7 +16,7 @@
 // and their chains of loads at small ones. 32 sequences of 2 to 7 drafts over 128256 values, fp32,
 // both sides: sums 43 us (180 MB, 4.2 TB/s; 33 without the exponentials, 49 with a
 // polynomial of degree 10 in place of the table), choose 14 (18 with blocks of 1024 threads,
-// whose registers let one of them run per CU), draw 10. One sequence of 4 drafts: 6, 5, 7.
+// whose registers let one of them run per CU), draw 11. One sequence of 4 drafts: 6, 5, 7.
 #pragma once
 
 #include "token_rows.hpp"
@@ -249,7 +249,7 @@ struct VerifyRow {
 };
 
 // First every block judges its sequence's rows, sixteen lanes for the target's sums of a
-// row and sixteen for the draft's, 32 rows at a time; then it sums its split.
+// row and sixteen for the draft's, 16 rows at a time; then it sums its split.
 template <bool BF16, bool WIDE>
 __global__ __launch_bounds__(kChooseThreads) void verify_choose_kernel(const VerifyArgs a) {
   using Values = VerifyValues<BF16, WIDE, kChooseThreads>;

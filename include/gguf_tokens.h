@@ -57,11 +57,12 @@ typedef struct gguf_rope {
  * reduced in fp64 with what its products round off: positions of any size lose nothing.
  * q_norm and k_norm: fp32 [head_dim], either may be NULL (not normed). rope NULL: norms
  * only. n_heads or n_kv_heads may be 0 (its pointers are then not looked at).
- * head_dim even, 2 .. 512. q_out may be q and k_out may be k (same stride); otherwise
- * outputs may not overlap inputs or each other. Rows of q and k may lie interleaved in
- * one buffer (slices of one product's output) where their strides are equal. Pointers
- * aligned to their elements; rows that are 16-byte aligned, with head_dim and n_rot
- * multiples of 16 (BF16) or 8 (F32), run several times faster than others. */
+ * head_dim even, 2 .. 512; n_heads and n_kv_heads at most 65535. q_out may be q and k_out
+ * may be k (same stride); otherwise outputs may not overlap inputs or each other. Rows of q
+ * and k may lie interleaved in one buffer (slices of one product's output) where their
+ * strides are equal. Pointers aligned to their elements; rows that are 16-byte aligned, with head_dim and n_rot
+ * multiples of 16 (BF16) or 8 (F32), run two to four times faster than others (32 + 8 heads
+ * of 128: 8192 tokens in BF16 28 us and 106, 4096 in F32 27 and 55). */
 int gguf_qk_rope(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, int64_t n_heads,
                  const void* k, int64_t k_stride, void* k_out, int64_t k_out_stride, int64_t n_kv_heads,
                  int32_t type, int64_t n_tokens, int64_t head_dim, const float* q_norm,
@@ -90,11 +91,23 @@ int gguf_qk_rope(const void* q, int64_t q_stride, void* q_out, int64_t q_out_str
  * aligned), out may not overlap an input. max_len (<= 2^25) bounds the lengths:
  * longer sequences are taken to end there, as at the table's row.
  *
+ * Limits (GGUF_QK_ERR_LIMIT past them): 2^23 rows, 2^20 sequences, 65535 query heads, 2^25
+ * first slots, and 65535 tiles of columns, that is (n_rows * g + n_seqs * (c - 1)) / c with g
+ * query heads per kv head and c = 16 or 32, or 128 where many rows run (below).
+ *
+ * One call, one kernel. Which kernel runs and how positions are split goes by the call's
+ * totals, not by each sequence: a sequence of few rows and many slots among enough rows of
+ * others is read by one block per kv head. Such calls are better made apart, each with its own
+ * rows and row_start: one token behind 131072 slots beside a prompt of 1024 rows (BF16, 16
+ * heads of 128 over 4) takes 2060 us in one call, 57 + 30 in two.
+ *
  * Accuracy. F32: that of gguf_attn_decode. BF16: scores and sums in fp32, and where a
- * sequence has on average more than 32 rows times query heads per kv head (16 for F16 and
- * BF16 caches of head dims from 96 on):
- *   scores from exact products of q with the cache's values (Q8_0: the nearest fp16 of a
- *     value, or within 2^-18 of the greatest scale of the slots read);
+ * sequence has on average over the call more than 32 rows times query heads per kv head (16
+ * for F16 and BF16 caches of head dims from 96 on) many rows run, for all of its sequences, so
+ * that a row's roundings depend on the others:
+ *   scores from exact products of q with the cache's values (F16 and Q8_0 caches: q's
+ *     elements below 2^-26 of their head's greatest within 2^-34 of that; Q8_0: the nearest
+ *     fp16 of a value, or within 2^-18 of the greatest scale of the slots read);
  *   softmax weights rounded to the operand type of the second product: bf16 for a BF16
  *     cache (2^-8 of each weight), fp16 otherwise (2^-11 of each, or 2^-25 of the row's
  *     greatest).
@@ -135,17 +148,19 @@ int gguf_attn_extend(const gguf_kv_cache* cache, const void* q, int32_t type, in
  *     max(p - q, 0): the lowest i whose running sum exceeds uniform_next[s] times
  *     the whole (from p where p - q is nowhere above 0).
  * T = 0: p is 1 at the greatest logit (of equal ones the lowest index) and q is 1 at
- * the drafted token. accept_prob[r] (may be NULL) = min(1, p[t] / q[t]), 1 for a
- * sequence's last row; 0 for a token outside 0 .. vocab - 1, which is never accepted.
+ * the drafted token. accept_prob[r] (may be NULL) = min(1, p[t] / q[t]), 0 where p[t] is
+ * 0, 1 for a sequence's last row; 0 for a token outside 0 .. vocab - 1, which is never accepted.
  * A sequence without rows has accepted 0 and next -1. Logits of -inf (ruled out) have
  * probability 0; a row without a finite greatest logit (all -inf, NaN, +inf), of
  * target or draft, accepts nothing, has accept_prob 0, and draws -1. Rows of no sequence are left alone.
  *
  * target and draft of one type, F32 or BF16, [n_rows][vocab], strides in elements from
  * row to row (>= vocab), aligned to their elements. Exponentials (to 2^-43) and sums
- * are fp64: a draw differs from the exact one only where uniform_next falls within
- * some 1e-12 of a boundary. T >= 0 and finite (a negative or NaN T is taken as 0).
- * vocab <= 2^30. */
+ * are fp64: a draw differs from the exact one only where the sum that uniform_next names
+ * falls within 1e-12 of a boundary, with p's whole as 1; the whole of max(p - q, 0) is less
+ * (a draft within 1 % of its target: some 0.01), so that there uniform_next itself counts to
+ * 1e-12 over it. T >= 0 and finite (a negative or NaN T is taken as 0).
+ * vocab <= 2^30, n_seqs <= 65535, n_rows * ceil(vocab / 8192) < 2^23. */
 int64_t gguf_verify_draft_workspace(int64_t n_rows, int64_t n_seqs, int64_t vocab, int32_t has_draft);
 int gguf_verify_draft(const void* target, int64_t target_stride, const void* draft, int64_t draft_stride,
                       int32_t type, const int32_t* tokens, const float* uniform, const float* uniform_next,

@@ -65,3 +65,17 @@ def test_the_named_size_grows_with_sequences_rows_and_bound(kind):
                 what = (type_, a, heads, b, window, sinks, (n, rows, max_len))
                 assert named(c, type_, *a, heads, b, window, sinks) <= have, what
                 assert serves(c, have, type_, *a, heads, b, window, sinks), what
+
+
+def test_limits_that_the_header_names():
+    c = cache()
+    # tiles of 16 columns, 4 query heads per kv head: (4 n + 15 n) / 16 <= 65535
+    assert named(c, F32, 55188, 55188, 16, 64) == 0 and named(c, F32, 55189, 55189, 16, 64) == g.ERR_LIMIT
+    # of 128: (4 n + 127) / 128
+    assert named(c, BF16, 1, 65535 * 32, 16, 64) == 0 and named(c, BF16, 1, 65535 * 32 + 1, 16, 64) == g.ERR_LIMIT
+    assert named(c, F32, 1, 1 << 20, 16, 64) == g.ERR_LIMIT
+    for rows, vocab in (((1 << 23) - 1, 8192), ((1 << 22) - 1, 8193)):
+        assert g.gguf_verify_draft_workspace(rows, 4, vocab, True) > 0
+        assert g.gguf_verify_draft_workspace(rows + 1, 4, vocab, True) == g.ERR_LIMIT
+    assert g.gguf_verify_draft_workspace(8, 65535, 100, True) > 0
+    assert g.gguf_verify_draft_workspace(8, 65536, 100, True) == g.ERR_LIMIT
