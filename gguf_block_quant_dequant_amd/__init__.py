@@ -980,7 +980,8 @@ def gguf_attn_extend(cache: KvCache, q, page_table, lengths, max_len, row_start=
     one row per sequence), the last of them at slot lengths[s] - 1. A row sees the slots
     up to its own; with a window the last `window` of those and the first `sinks` of the
     sequence. scale 1 / sqrt(head_dim) unless given. Returns out, of q's shape and type
-    (rows of no sequence are left as they were). `workspace`: a tensor of at least
+    (rows of no sequence are left as they were). A long sequence with few rows is better
+    passed apart from prompts: the call's totals choose its one kernel and its splits. `workspace`: a tensor of at least
     gguf_attn_extend_workspace bytes that no overlapping call uses (None: the call
     allocates one)."""
     if not isinstance(q, torch.Tensor):
